@@ -318,6 +318,150 @@ int thd_attn_merge(const void* out_a, const float* lse_a, const void* out_b, con
                    void* stream);
 
 /*
+ * thd_qk_norm_rope — RMS norm of each query and key head and the rotation by its
+ * row's position, in one pass over packed rows: what stands between the
+ * projection and thd_attn_fwd.
+ *
+ * For a head x of head_dim values of row i of sequence b, at position
+ * p = i + position_offsets[b]:
+ *     n = x * w / sqrt(mean(x^2) + eps)        (n = x where the weight is NULL)
+ *     y_i = n_i cos[p, c] - n_j sin[p, c]
+ *     y_j = n_j cos[p, c] + n_i sin[p, c]      for each rotated pair (i, j)
+ * Pair c of rotary_dim / 2 is (c, c + rotary_dim / 2), or (2c, 2c + 1) with
+ * `interleaved`; values from rotary_dim on are n.  Computed in fp32 and rounded
+ * once.
+ *
+ * q, k         device, rows of Hq (Hkv) heads of head_dim values, dtype; row t
+ *              starts at q + t * q_stride elements (so q and k may be parts of one
+ *              fused projection), q_stride >= Hq * head_dim, a multiple of 8;
+ *              16-byte aligned.  num_heads_q or num_heads_kv may be 0: that side
+ *              is left out.
+ * q_weight, k_weight  device [head_dim], 16-byte aligned, or NULL (that side is not
+ *              normed); fp32 if weight_fp32 is 1, dtype if it is 0.
+ * eps          finite, >= 0.
+ * rope_cos, rope_sin  device fp32 [rope_rows, rotary_dim / 2], 16-byte aligned; a
+ *              position outside the tables takes their nearest row.  Not read
+ *              when rotary_dim is 0.
+ * rotary_dim   a multiple of 16 in [0, head_dim].
+ * cu_seqlens, cu_seqlens_padded  as in thd_attn_fwd; slots ascend and do not overlap.
+ * position_offsets  device int32 [>= batch_size], or NULL (0).
+ * q_out, k_out device, [T, Hq, head_dim] and [T, Hkv, head_dim], contiguous, 16-byte
+ *              aligned; may be q and k themselves when those are contiguous.
+ *              Rows of no sequence are written as zeros.
+ * head_dim     a multiple of 16 in [16, 128].
+ * Errors: THD_ERR_ARG, THD_ERR_UNSUPPORTED, THD_ERR_CUDA.
+ */
+int thd_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* q_weight,
+                     const void* k_weight, int weight_fp32, float eps, const float* rope_cos, const float* rope_sin,
+                     int rope_rows, int rotary_dim, int interleaved, const int32_t* cu_seqlens,
+                     const int32_t* cu_seqlens_padded, const int32_t* position_offsets, int batch_size, void* q_out,
+                     void* k_out, int total_tokens, int num_heads_q, int num_heads_kv, int head_dim, int dtype,
+                     void* stream);
+
+/* Bytes of device workspace thd_qk_norm_rope_bwd needs; 0 for an unsupported head_dim. */
+size_t thd_qk_norm_rope_bwd_workspace_size(int head_dim);
+
+/*
+ * thd_qk_norm_rope_bwd — gradients of thd_qk_norm_rope for the same batch.
+ *
+ * With h the incoming gradient turned back and r = 1 / sqrt(mean(x^2) + eps):
+ *     dw = sum over rows and heads of h * x * r
+ *     dx = r * (h * w - x * r^2 * mean(h * w * x))      (dx = h without a weight)
+ * grad_q, grad_k  device, contiguous, shapes of q_out, k_out: incoming gradients.
+ * q, k         the forward's inputs (not read where the weight is NULL).
+ * dq, dk       device, rows with their own strides (as q, k); may be grad_q and grad_k
+ *              themselves.  Rows of no sequence are written as zeros.
+ * dq_weight, dk_weight  device fp32 [head_dim]; NULL exactly where the weight is NULL.
+ *              The sums are taken in a fixed order: the same call gives the same bits.
+ * workspace    device, >= thd_qk_norm_rope_bwd_workspace_size(head_dim) bytes,
+ *              16-byte aligned, uninitialised; not shared by calls that overlap on
+ *              the GPU.  Not needed when both weights are NULL.
+ * Other arguments and errors as thd_qk_norm_rope, and THD_ERR_WORKSPACE.
+ */
+int thd_qk_norm_rope_bwd(const void* grad_q, const void* grad_k, const void* q, int64_t q_stride, const void* k,
+                         int64_t k_stride, const void* q_weight, const void* k_weight, int weight_fp32, float eps,
+                         const float* rope_cos, const float* rope_sin, int rope_rows, int rotary_dim, int interleaved,
+                         const int32_t* cu_seqlens, const int32_t* cu_seqlens_padded, const int32_t* position_offsets,
+                         int batch_size, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride, float* dq_weight,
+                         float* dk_weight, int total_tokens, int num_heads_q, int num_heads_kv, int head_dim,
+                         int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * thd_kv_append — new keys and values of a packed batch into a paged cache, the
+ * keys normed and rotated on the way as by thd_qk_norm_rope, and the queries too.
+ *
+ * Row i of sequence b goes to slot cache_lens[b] + i of its sequence: entry
+ * slot / page_size of row b of page_table names the page, slot % page_size the
+ * token in it.  A slot past the table (max_pages), or whose entry is outside
+ * [0, num_pages), is not written.  No two rows may share a slot.  The caller adds
+ * the new lengths to cache_lens afterwards.
+ *
+ * q, k, v      rows as in thd_qk_norm_rope; num_heads_q may be 0 (no queries).
+ * positions    device int32 [T], the position of each row, or NULL: cache_lens[b] + i.
+ * cache_lens   device int32 [>= batch_size]: keys of each sequence already cached.
+ * q_out        device [T, Hq, head_dim], contiguous; may be q.  Rows of no sequence are
+ *              written as zeros.
+ * k_cache, v_cache  device, dtype, 16-byte aligned: token t of head h of page g starts at
+ *              g * strides[0] + t * strides[1] + h * strides[2] elements (k_cache),
+ *              strides[3..5] for v_cache; strides are >= 0 and multiples of 8.
+ * cache_strides host int64 [6].
+ * page_table   device int32; row b starts at b * page_table_stride, max_pages entries.
+ * Other arguments and errors as thd_qk_norm_rope.
+ */
+int thd_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                  const void* q_weight, const void* k_weight, int weight_fp32, float eps, const float* rope_cos,
+                  const float* rope_sin, int rope_rows, int rotary_dim, int interleaved, const int32_t* positions,
+                  const int32_t* cu_seqlens, const int32_t* cu_seqlens_padded, const int32_t* cache_lens,
+                  int batch_size, void* q_out, void* k_cache, void* v_cache, const int64_t* cache_strides,
+                  int num_pages, int page_size, const int32_t* page_table, int64_t page_table_stride, int max_pages,
+                  int total_tokens, int num_heads_q, int num_heads_kv, int head_dim, int dtype, void* stream);
+
+/* Bytes of device workspace thd_attn_paged needs; 0 for an unsupported head_dim. */
+size_t thd_attn_paged_workspace_size(int head_dim);
+
+/*
+ * thd_attn_paged — attention of packed new tokens over a paged cache: one token per
+ * sequence (decoding), a chunk of them, or a tree of drafted tokens.
+ *
+ * Sequence b has n = cu_seqlens_q[b+1] - cu_seqlens_q[b] new tokens and
+ * L = kv_lens[b] keys in the cache, the new tokens' own among them, last.  New
+ * token i sees key j < L iff j <= L - n + i (the bottom-right causal mask type of
+ * thd_attn_fwd); with a tree mask iff j < L - n, or bit (j - (L - n)) of the
+ * token's mask is set.  A token that sees no key gets zeros and lse -inf.
+ * Values that a token does not see must still be finite where they lie among
+ * the L cached ones; whatever lies behind them in a page is not looked at.
+ *
+ * q            device [T, Hq, head_dim], contiguous, 16-byte aligned.
+ * k_cache, v_cache, cache_strides, num_pages, page_size, page_table,
+ * page_table_stride, max_pages  as in thd_kv_append.  kv_lens above
+ *              max_pages * page_size counts as that; an entry outside [0, num_pages)
+ *              gives unspecified output.  Entries of pages behind the keys are
+ *              not read.
+ * kv_lens      device int32 [>= batch_size].
+ * cu_seqlens_q, cu_seqlens_q_padded  as in thd_attn_fwd; slots ascend and do not overlap.
+ * max_seqlen_q >= 0; a hint (0: unknown): the most new tokens of a sequence.  It picks
+ *              the rows of a tile; any value gives results within rounding.
+ * tree_mask    device int64 [T, tree_words], or NULL: bit j % 64 of word j / 64 of a row
+ *              says whether it sees new token j of its sequence; tokens past the words
+ *              are not seen.
+ * out          device [T, Hq, head_dim], contiguous, 16-byte aligned; rows of no sequence
+ *              are written as zeros.
+ * lse          device fp32 [Hq, T] or NULL, as in thd_attn_fwd.
+ * head_dim     a multiple of 8 in [8, 128].
+ * workspace    device, >= thd_attn_paged_workspace_size(head_dim) bytes, 16-byte aligned,
+ *              uninitialised; not shared by calls that overlap on the GPU.
+ * Nothing is read from the device on the host, so a captured call may be replayed
+ * with other lengths, tables and masks in the same buffers.
+ * Errors: THD_ERR_ARG, THD_ERR_UNSUPPORTED, THD_ERR_WORKSPACE, THD_ERR_CUDA.
+ */
+int thd_attn_paged(const void* q, const void* k_cache, const void* v_cache, const int64_t* cache_strides,
+                   int num_pages, int page_size, const int32_t* page_table, int64_t page_table_stride, int max_pages,
+                   const int32_t* kv_lens, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_q_padded,
+                   int batch_size, int max_seqlen_q, const int64_t* tree_mask, int tree_words, float softmax_scale,
+                   void* out, float* lse, int total_tokens, int num_heads_q, int num_heads_kv, int head_dim, int dtype,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * thd_set_wait_limit_ns — the time limit of one pipeline wait inside the
  * attention kernels (forward, windowed forward, no-allocation forward,
  * backward), for calls made after it on any host thread; returns the previous

@@ -16,7 +16,8 @@ import torch
 
 __all__ = ["thd_attn_fwd", "thd_attn_bwd", "thd_attn_fwd_noalloc", "thd_attn_noalloc_status", "thd_attn_merge", "thd_padding_mask",
            "thd_padding_mask_cross", "MASK_PADDING", "MASK_PADDING_CAUSAL", "MASK_PADDING_CAUSAL_BOTTOM_RIGHT", "thd_attn_workspace_size", "thd_set_wait_limit_ns", "thd_set_wait_injection", "thd_status_string",
-           "ThdError", "library_path", "load_library", "STATUS_WAIT_TIMEOUT"]
+           "ThdError", "library_path", "load_library", "STATUS_WAIT_TIMEOUT", "thd_qk_norm_rope", "thd_qk_norm_rope_bwd",
+           "thd_qk_norm_rope_bwd_workspace_size", "thd_kv_append", "thd_attn_paged", "thd_attn_paged_workspace_size"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -75,6 +76,21 @@ def load_library():
     lib.thd_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
     lib.thd_set_wait_injection.restype = ctypes.c_int
     lib.thd_set_wait_injection.argtypes = [ctypes.c_int]
+    L = ctypes.c_int64
+    lib.thd_qk_norm_rope.restype = I
+    lib.thd_qk_norm_rope.argtypes = [P, L, P, L, P, P, I, F, P, P, I, I, I, P, P, P, I, P, P, I, I, I, I, I, P]
+    lib.thd_qk_norm_rope_bwd.restype = I
+    lib.thd_qk_norm_rope_bwd.argtypes = [P, P, P, L, P, L, P, P, I, F, P, P, I, I, I, P, P, P, I, P, L, P, L, P, P, I, I,
+                                         I, I, I, P, SZ, P]
+    lib.thd_qk_norm_rope_bwd_workspace_size.restype = SZ
+    lib.thd_qk_norm_rope_bwd_workspace_size.argtypes = [I]
+    lib.thd_kv_append.restype = I
+    lib.thd_kv_append.argtypes = [P, L, P, L, P, L, P, P, I, F, P, P, I, I, I, P, P, P, P, I, P, P, P, P, I, I, P, L, I, I,
+                                  I, I, I, I, P]
+    lib.thd_attn_paged.restype = I
+    lib.thd_attn_paged.argtypes = [P, P, P, P, I, I, P, L, I, P, P, P, I, I, P, I, F, P, P, I, I, I, I, I, P, SZ, P]
+    lib.thd_attn_paged_workspace_size.restype = SZ
+    lib.thd_attn_paged_workspace_size.argtypes = [I]
     lib.thd_status_string.restype = ctypes.c_char_p
     lib.thd_status_string.argtypes = [I]
     _LIB = lib
@@ -390,3 +406,7 @@ def thd_attn_bwd(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlen
     if st != THD_OK:
         raise ThdError(st, "thd_attn_bwd")
     return dq, dk, dv
+
+
+from .paged import (thd_attn_paged, thd_attn_paged_workspace_size, thd_kv_append, thd_qk_norm_rope,  # noqa: E402
+                    thd_qk_norm_rope_bwd, thd_qk_norm_rope_bwd_workspace_size)

@@ -22,7 +22,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 # content hash of the sources and flags the library was built from, written beside it
 STAMP = LIB + ".sha256"
 
-SOURCES = ["thd_attn.cu", "padding_mask.cu", "attn_noalloc.cu", "attn_merge.cu"]
+SOURCES = ["thd_attn.cu", "padding_mask.cu", "attn_noalloc.cu", "attn_merge.cu", "qk_norm_rope.cu",
+           "attn_paged.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

@@ -1,0 +1,728 @@
+// attn_paged.cu — attention of packed new tokens over a paged key/value cache
+// (thd_attn_paged, include/thd_attn.h): decoding steps, chunks of new tokens, and trees of
+// drafted tokens.
+//
+// For the new token i of a sequence with n new tokens and L cached keys (the new ones among
+// them, last): scores s_j = scale q.k_j over the keys j it sees, out = sum_j softmax(s)_j v_j,
+// lse = log sum_j exp(s_j).  It sees key j < L iff j <= L - n + i, or, with a tree mask, iff
+// j < L - n or bit j - (L - n) of its mask is set.
+//
+// What bounds it is reading the keys and values once (4 d bytes per key and head against
+// 4 d operations per query row), so the work is split along the keys over every SM:
+//  * the query heads that share a key/value head are the rows of one tile (row = token * group
+//    + head of the group), so a key is read once for all of them;
+//  * a unit is kUnit keys of one (sequence, key/value head, row tile); the units of the batch
+//    are laid end to end and every CTA takes an equal share of them, whatever the lengths;
+//  * a CTA whose share ends inside a tile writes an unnormalised partial (at most two per CTA),
+//    and a second kernel, launched to overlap the first one's end, joins them;
+//  * inside a CTA each warp runs alone: it streams its own 16 keys of each unit through its own
+//    ring of shared memory with 16-byte asynchronous copies, keeps a running maximum, sums and
+//    output tile in registers, and meets the other warps only when the tile is done.
+#include <cmath>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/thd_attn.h"
+#include "seq_rows.cuh"
+
+namespace thd {
+namespace {
+
+constexpr int kUnit = 64;            // keys of a unit
+constexpr int kWarps = 4;            // warps of a CTA, 16 keys of the unit each
+constexpr int kWarpKeys = kUnit / kWarps;
+constexpr int kStages = 3;           // units in flight per warp
+constexpr int kMaxCtas = 320;        // CTAs of a launch at most (two on each of up to 160 SMs)
+constexpr int kJoinThreads = 256;
+
+struct PagedArgs {
+  const void* q;
+  const void* kc;
+  const void* vc;
+  const int32_t* table;
+  const int32_t* kv_lens;
+  const int32_t* cu;
+  const int32_t* padded;
+  const long long* tree;
+  void* out;
+  float* lse;
+  float* part_o;       // [ctas * 2][rows][DP]
+  float* part_m;       // [ctas * 2][3][rows]: maximum, sum of the rounded weights, sum of the weights
+  int4* splits;        // [ctas]: (sequence, head, row tile, CTAs of the tile), of the tile that starts in the CTA and ends in another
+  long long table_stride, k_page, k_token, k_head, v_page, v_token, v_head;   // elements
+  int num_pages, page_size, max_pages;
+  int tree_words;
+  int B, T, Hq, Hkv, group, d;
+  float scale_log2;
+};
+
+// One sequence of the batch, clamped to the buffers.
+struct SeqWork {
+  int q_start, q_len, kv_len, tiles, blocks;
+  long long units;
+};
+
+__device__ __forceinline__ SeqWork seq_work(const PagedArgs& p, int b, int rows_per_tile) {
+  SeqWork s;
+  const int c0 = p.cu[b], c1 = p.cu[b + 1];
+  long long qs = p.padded ? p.padded[b] : c0, ql = (long long)c1 - c0;
+  qs = qs < 0 ? 0 : (qs > p.T ? p.T : qs);
+  ql = ql < 0 ? 0 : (ql > p.T - qs ? p.T - qs : ql);
+  const long long room = (long long)p.max_pages * p.page_size;
+  long long kv = p.kv_lens[b];
+  kv = kv < 0 ? 0 : (kv > room ? room : kv);
+  s.q_start = (int)qs;
+  s.q_len = (int)ql;
+  s.kv_len = (int)kv;
+  const long long rows = ql * p.group;
+  s.tiles = (int)((rows + rows_per_tile - 1) / rows_per_tile);
+  s.blocks = (s.kv_len + kUnit - 1) / kUnit;
+  s.units = (long long)s.tiles * s.blocks * p.Hkv;
+  return s;
+}
+
+// The CTA's share of the batch's units, and the sequence its first unit lies in.  Every CTA
+// adds up the whole batch: each thread a run of sequences, then a scan over the threads.
+struct Share {
+  long long begin, end, seq_base;   // units; seq_base: first unit of sequence seq
+  long long total;
+  int ctas;                         // CTAs that have units
+  int seq;
+};
+
+__device__ __forceinline__ long long share_begin(long long total, int ctas, int c) { return total * c / ctas; }
+
+template <int kThreads>
+__device__ void find_share(const PagedArgs& p, int rows_per_tile, Share* out) {
+  __shared__ long long warp_sum[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += seq_work(p, b, rows_per_tile).units;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  const long long excl = before + incl - mine;
+  const int ctas = total < gridDim.x ? (int)total : (int)gridDim.x;
+  if (tid == 0) {
+    out->total = total;
+    out->ctas = ctas;
+    out->begin = out->end = 0;
+    out->seq = 0;
+    out->seq_base = 0;
+  }
+  __syncthreads();
+  if ((int)blockIdx.x < ctas) {
+    const long long begin = share_begin(total, ctas, blockIdx.x);
+    if (begin >= excl && begin < excl + mine) {   // in this thread's run of sequences
+      long long base = excl;
+      int b = b0;
+      for (; b < b1; ++b) {
+        const long long u = seq_work(p, b, rows_per_tile).units;
+        if (begin < base + u) break;
+        base += u;
+      }
+      out->seq = b;
+      out->seq_base = base;
+      out->begin = begin;
+      out->end = share_begin(total, ctas, blockIdx.x + 1);
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <typename DT>
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 2^x, 0 at -inf (the hardware's approximation, 2 ulp)
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Shared memory of a CTA: each warp's ring of key and value tiles (16 rows of DP values,
+// 16-byte chunks XORed with the row so that eight rows of one column of chunks lie in
+// different banks); at a tile's end the warps' sums and outputs take its place.
+template <int DP, int MT>
+struct PagedSmem {
+  static constexpr int kTileBytes = kWarpKeys * DP * 2;
+  static constexpr int kRing = kWarps * kStages * 2 * kTileBytes;
+  static constexpr int kJoin = kWarps * MT * (DP + 3) * 4;
+  static constexpr int kBytes = kRing > kJoin ? kRing : kJoin;
+};
+
+// MT: rows of a tile (16 or 32).
+template <typename DT, int DP, int MT>
+__global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedArgs p) {
+  constexpr int kMF = MT / 16;          // 16-row fragments
+  constexpr int kKSteps = DP / 16;      // of the score product
+  constexpr int kNT = DP / 8;           // 8-column output fragments
+  constexpr int kChunks = DP / 8;       // 16-byte chunks of a key
+  constexpr int kLaneKeys = 32 / kChunks;               // keys one copy instruction covers
+  constexpr int kCopies = kWarpKeys / kLaneKeys;
+  constexpr int kTileBytes = PagedSmem<DP, MT>::kTileBytes;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ Share share;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  find_share<kWarps * 32>(p, MT, &share);
+  const long long begin = share.begin, end = share.end;
+  if (tid == 0) p.splits[blockIdx.x] = make_int4(-1, 0, 0, 0);
+
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * (kStages * 2 * kTileBytes);
+  const int copy_key = lane / kChunks, copy_chunk = lane % kChunks;
+  const bool copy_in = copy_chunk * 8 < p.d;
+  const int ld_row = lane & 7, ld_mat = lane >> 3;   // ldmatrix: this lane's row of matrix ld_mat
+
+  long long u = begin, base = share.seq_base;
+  int b = share.seq;
+  while (u < end) {
+    const SeqWork s = seq_work(p, b, MT);
+    if (u - base >= s.units) {
+      base += s.units;
+      ++b;
+      continue;
+    }
+    const long long item = (u - base) / s.blocks;
+    const int blk0 = (int)(u - base - item * s.blocks);
+    const int nblk = (int)min((long long)(s.blocks - blk0), end - u);
+    const int head = (int)(item / s.tiles), tile = (int)(item - (long long)head * s.tiles);
+    const bool whole = nblk == s.blocks;
+    const int rows = (int)min((long long)MT, (long long)s.q_len * p.group - (long long)tile * MT);
+    const int row0 = tile * MT;           // of the sequence's rows
+    const int past = s.kv_len - s.q_len;  // keys before the new tokens (negative: fewer keys than tokens)
+    // keys that no row of the tile sees need not be read
+    const int last_tok = (row0 + rows - 1) / p.group;
+    const int key_end = p.tree ? s.kv_len : min(s.kv_len, max(0, past + last_tok + 1));
+    const int steps = min(nblk, max(0, (key_end + kUnit - 1) / kUnit - blk0));
+
+    // ---- keys and values: this warp's 16 keys of unit blk0 + i ----
+    const int32_t* table = p.table + (long long)b * p.table_stride;
+    // lane l < 16 holds the element offset of key l, lane 16 + l that of value l
+    auto offset_of = [&](int i) {
+      const int key = (blk0 + i) * kUnit + warp * kWarpKeys + (lane & 15);
+      long long off = 0;
+      if (i < steps && key < key_end) {
+        const int at = key / p.page_size;
+        int page = table[at];
+        page = page < 0 ? 0 : (page >= p.num_pages ? p.num_pages - 1 : page);
+        const int in = key - at * p.page_size;
+        off = lane < 16 ? page * p.k_page + in * p.k_token + head * p.k_head
+                        : page * p.v_page + in * p.v_token + head * p.v_head;
+      }
+      return off;
+    };
+    auto issue = [&](int i, int stage, long long off) {
+      if (i < steps) {
+        const int first = (blk0 + i) * kUnit + warp * kWarpKeys;
+        const uint32_t dst = ring + stage * (2 * kTileBytes);
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c) {
+          const int key = c * kLaneKeys + copy_key;
+          const bool take = copy_in && first + key < key_end;
+          const uint32_t at = key * (DP * 2) + ((copy_chunk ^ (key & 7)) << 4);
+          const long long ko = __shfl_sync(0xffffffffu, off, key), vo = __shfl_sync(0xffffffffu, off, 16 + key);
+          const int col = take ? copy_chunk * 8 : 0;
+          cp_async16(dst + at, static_cast<const DT*>(p.kc) + ko + col, take);
+          cp_async16(dst + kTileBytes + at, static_cast<const DT*>(p.vc) + vo + col, take);
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i, i, offset_of(i));
+    long long next_off = offset_of(kStages - 1);
+
+    // ---- queries: the A fragments of the tile ----
+    uint32_t qf[kMF][kKSteps][4];
+    int limit[kMF][2];            // last key of the row (no tree), -1 past the last row
+    const long long* bits[kMF][2];
+    const int qr = lane >> 2, qc = (lane & 3) * 2;
+#pragma unroll
+    for (int f = 0; f < kMF; ++f) {
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int r = f * 16 + hh * 8 + qr;
+        const int row = row0 + r;
+        const int tok = row / p.group;
+        const bool ok = r < rows;
+        limit[f][hh] = ok ? min(past + tok, s.kv_len - 1) : -1;
+        bits[f][hh] = p.tree && ok ? p.tree + (long long)(s.q_start + tok) * p.tree_words : nullptr;
+        const DT* src = static_cast<const DT*>(p.q) +
+                        ((long long)(s.q_start + tok) * p.Hq + head * p.group + (row - tok * p.group)) * p.d;
+#pragma unroll
+        for (int k = 0; k < kKSteps; ++k) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int col = k * 16 + half * 8 + qc;
+            qf[f][k][half * 2 + hh] = ok && col < p.d ? *reinterpret_cast<const uint32_t*>(src + col) : 0u;
+          }
+        }
+      }
+    }
+
+    float o[kMF][kNT][4], m[kMF][2], l[kMF][2], lr[kMF][2];
+#pragma unroll
+    for (int f = 0; f < kMF; ++f) {
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[f][n][e] = 0.f;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        m[f][hh] = -INFINITY;
+        l[f][hh] = lr[f][hh] = 0.f;
+      }
+    }
+
+    int stage = 0;
+    for (int i = 0; i < steps; ++i) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      {
+        const int fill = stage == 0 ? kStages - 1 : stage - 1;   // the stage read in the step before
+        issue(i + kStages - 1, fill, next_off);
+        next_off = offset_of(i + kStages);
+      }
+      const uint32_t kt = ring + stage * (2 * kTileBytes), vt = kt + kTileBytes;
+      const int first = (blk0 + i) * kUnit + warp * kWarpKeys;
+      // ---- scores ----
+      float c[kMF][2][4];
+#pragma unroll
+      for (int f = 0; f < kMF; ++f)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[f][n][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kKSteps; ++k) {
+        uint32_t kb[4];   // keys 0-7 (both halves of the 16 columns), keys 8-15
+        const int row = ld_row + (ld_mat >> 1) * 8, chunk = 2 * k + (ld_mat & 1);
+        ldsm4(kt + row * (DP * 2) + ((chunk ^ ld_row) << 4), kb);
+#pragma unroll
+        for (int f = 0; f < kMF; ++f) {
+          mma16816<DT>(c[f][0], qf[f][k], kb[0], kb[1]);
+          mma16816<DT>(c[f][1], qf[f][k], kb[2], kb[3]);
+        }
+      }
+      // ---- visibility ----
+      // some key may be hidden from some row
+      const bool cut = first + kWarpKeys > min(p.tree ? past : past + 1, s.kv_len);
+#pragma unroll
+      for (int f = 0; f < kMF; ++f) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[f][n][e] *= p.scale_log2;
+        if (cut) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = first + n * 8 + qc + (e & 1), hh = e >> 1;
+              bool see = key <= limit[f][hh];
+              if (p.tree) {
+                const int j = key - past;
+                see = key < s.kv_len;
+                if (see && j >= 0)
+                  see = bits[f][hh] && j < p.tree_words * 64 && ((bits[f][hh][j >> 6] >> (j & 63)) & 1);
+              }
+              if (!see) c[f][n][e] = -INFINITY;
+            }
+          }
+        }
+      }
+      // ---- running maximum and sums, weights ----
+      uint32_t pf[kMF][4];
+#pragma unroll
+      for (int f = 0; f < kMF; ++f) {
+        float scale[2];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float x = fmaxf(fmaxf(c[f][0][2 * hh], c[f][0][2 * hh + 1]), fmaxf(c[f][1][2 * hh], c[f][1][2 * hh + 1]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          const float top = fmaxf(m[f][hh], x);
+          const float use = top == -INFINITY ? 0.f : top;
+          scale[hh] = exp2_fast(m[f][hh] - use);
+          m[f][hh] = top;
+          float sum = 0.f, sum_r = 0.f;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float p0 = exp2_fast(c[f][n][2 * hh] - use), p1 = exp2_fast(c[f][n][2 * hh + 1] - use);
+            sum += p0 + p1;
+            const uint32_t w = Pair16<DT>::put(p0, p1);
+            const float2 r = Pair16<DT>::get(w);
+            sum_r += r.x + r.y;
+            pf[f][n * 2 + hh] = w;
+          }
+          l[f][hh] = l[f][hh] * scale[hh] + sum;
+          lr[f][hh] = lr[f][hh] * scale[hh] + sum_r;
+        }
+        if (__any_sync(0xffffffffu, scale[0] != 1.f || scale[1] != 1.f)) {
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) {
+            o[f][n][0] *= scale[0];
+            o[f][n][1] *= scale[0];
+            o[f][n][2] *= scale[1];
+            o[f][n][3] *= scale[1];
+          }
+        }
+      }
+      // ---- output ----
+#pragma unroll
+      for (int n = 0; n < kNT; n += 2) {
+        uint32_t vb[4];   // columns n: keys 0-7, 8-15; columns n + 1: the same
+        const int row = ld_row + (ld_mat & 1) * 8, chunk = n + (ld_mat >> 1);
+        ldsm4_trans(vt + row * (DP * 2) + ((chunk ^ ld_row) << 4), vb);
+#pragma unroll
+        for (int f = 0; f < kMF; ++f) {
+          mma16816<DT>(o[f][n], pf[f], vb[0], vb[1]);
+          mma16816<DT>(o[f][n + 1], pf[f], vb[2], vb[3]);
+        }
+      }
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+      __syncwarp();   // every lane has read the stage that the next step's copies fill
+    }
+    cp_async_wait<0>();
+
+    // ---- the warps' results joined ----
+    __syncthreads();   // no warp reads its ring any more
+    float* jo = reinterpret_cast<float*>(smem);                 // [warp][row][DP]
+    float* jm = jo + kWarps * MT * DP;                          // [warp][3][row]
+#pragma unroll
+    for (int f = 0; f < kMF; ++f) {
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int r = f * 16 + hh * 8 + qr;
+        float a = l[f][hh], ar = lr[f][hh];
+        a += __shfl_xor_sync(0xffffffffu, a, 1);
+        a += __shfl_xor_sync(0xffffffffu, a, 2);
+        ar += __shfl_xor_sync(0xffffffffu, ar, 1);
+        ar += __shfl_xor_sync(0xffffffffu, ar, 2);
+        if ((lane & 3) == 0) {
+          jm[(warp * 3 + 0) * MT + r] = m[f][hh];
+          jm[(warp * 3 + 1) * MT + r] = ar;
+          jm[(warp * 3 + 2) * MT + r] = a;
+        }
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+          *reinterpret_cast<float2*>(jo + (warp * MT + r) * DP + n * 8 + qc) =
+              make_float2(o[f][n][2 * hh], o[f][n][2 * hh + 1]);
+      }
+    }
+    __syncthreads();
+    const int part = blockIdx.x * 2 + (u == begin ? 0 : 1);
+    for (int x = tid; x < rows * kChunks; x += kWarps * 32) {
+      const int r = x / kChunks, chunk = x - r * kChunks;
+      float top = -INFINITY, w[kWarps], sr = 0.f, se = 0.f, acc[8];
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) top = fmaxf(top, jm[(k * 3) * MT + r]);
+      const float use = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        w[k] = exp2_fast(jm[(k * 3) * MT + r] - use);
+        sr += w[k] * jm[(k * 3 + 1) * MT + r];
+        se += w[k] * jm[(k * 3 + 2) * MT + r];
+        const float4* src = reinterpret_cast<const float4*>(jo + (k * MT + r) * DP + chunk * 8);
+        const float4 a = src[0], c = src[1];
+        acc[0] += w[k] * a.x, acc[1] += w[k] * a.y, acc[2] += w[k] * a.z, acc[3] += w[k] * a.w;
+        acc[4] += w[k] * c.x, acc[5] += w[k] * c.y, acc[6] += w[k] * c.z, acc[7] += w[k] * c.w;
+      }
+      if (whole) {
+        const int row = row0 + r, tok = row / p.group, hq = head * p.group + (row - tok * p.group);
+        const float inv = sr == 0.f ? 0.f : 1.f / sr;   // a NaN sum stays one
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = sr == 0.f ? 0.f : acc[e] * inv;
+        if (chunk * 8 < p.d)
+          *reinterpret_cast<uint4*>(static_cast<DT*>(p.out) + ((long long)(s.q_start + tok) * p.Hq + hq) * p.d +
+                                    chunk * 8) = pack8<DT>(acc);
+        if (chunk == 0 && p.lse)
+          p.lse[(long long)hq * p.T + s.q_start + tok] =
+              se == 0.f ? -INFINITY : use * 0.69314718055994531f + logf(se);
+      } else {
+        float4* dst = reinterpret_cast<float4*>(p.part_o + ((long long)part * MT + r) * DP + chunk * 8);
+        dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (chunk == 0) {
+          float* pm = p.part_m + (long long)part * 3 * MT;
+          pm[r] = top;
+          pm[MT + r] = sr;
+          pm[2 * MT + r] = se;
+        }
+      }
+    }
+    if (!whole && blk0 == 0 && tid == 0) {
+      // the tile starts here and ends in CTA c: the join goes over blockIdx.x .. c
+      const long long tile_end = base + (item + 1) * s.blocks;
+      int c = blockIdx.x + 1;
+      while (share_begin(share.total, share.ctas, c + 1) < tile_end) ++c;
+      // slot of the first partial in bit 30
+      p.splits[blockIdx.x] = make_int4(b, head, tile, (c - (int)blockIdx.x + 1) | (u == begin ? 0 : 1 << 30));
+    }
+    __syncthreads();   // the ring is filled again
+    u += nblk;
+  }
+}
+
+// Joins the partials of the tiles that several CTAs share (block x: the tile that starts in CTA
+// x; block y its rows y, y + gridDim.y, ...), and writes the rows that have no units: rows of
+// no sequence and of sequences without keys.
+template <typename DT, int DP, int MT>
+__global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const PagedArgs p) {
+  constexpr int kJoinWarps = kJoinThreads / 32;
+  constexpr int kCols = DP / 32;        // columns of a lane
+  __shared__ float weight[kMaxCtas];
+  __shared__ float red[kJoinWarps][3];
+  __shared__ float acc_s[kJoinWarps][DP];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int blocks = gridDim.x * gridDim.y, block = blockIdx.y * gridDim.x + blockIdx.x;
+  for (int t = block * kJoinWarps + warp; t < p.T; t += blocks * kJoinWarps) {
+    const RowPlace at = find_row(p.cu, p.padded, p.B, t);
+    if (at.seq >= 0 && p.kv_lens[at.seq] > 0 && p.max_pages > 0) continue;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<DT*>(p.out) + (long long)t * p.Hq * p.d);
+    for (int i = lane; i < p.Hq * (p.d / 8); i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (p.lse)
+      for (int h = lane; h < p.Hq; h += 32) p.lse[(long long)h * p.T + t] = -INFINITY;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 sp = p.splits[blockIdx.x];
+  if (sp.x < 0) return;
+  const SeqWork s = seq_work(p, sp.x, MT);
+  const int n = sp.w & 0x3fffffff;
+  const int first = blockIdx.x * 2 + (sp.w >> 30);   // partial of the first CTA; the others' slot 0
+  const int rows = (int)min((long long)MT, (long long)s.q_len * p.group - (long long)sp.z * MT);
+  auto part_of = [&](int k) { return k == 0 ? first : ((int)blockIdx.x + k) * 2; };
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    float top = -INFINITY;
+    for (int k = tid; k < n; k += kJoinThreads) top = fmaxf(top, p.part_m[(long long)part_of(k) * 3 * MT + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) red[warp][0] = top;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, red[k][0]);
+    const float use = top == -INFINITY ? 0.f : top;
+    float sr = 0.f, se = 0.f;
+    for (int k = tid; k < n; k += kJoinThreads) {
+      const float* pm = p.part_m + (long long)part_of(k) * 3 * MT;
+      const float w = exp2_fast(pm[r] - use);
+      weight[k] = w;
+      sr += w * pm[MT + r];
+      se += w * pm[2 * MT + r];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      sr += __shfl_xor_sync(0xffffffffu, sr, o);
+      se += __shfl_xor_sync(0xffffffffu, se, o);
+    }
+    if (lane == 0) red[warp][1] = sr, red[warp][2] = se;
+    __syncthreads();
+    float acc[kCols];
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int k = warp; k < n; k += kJoinWarps) {
+      const float w = weight[k];
+      const float* src = p.part_o + ((long long)part_of(k) * MT + r) * DP;
+#pragma unroll
+      for (int e = 0; e < kCols; ++e) acc[e] += w * src[lane + 32 * e];
+    }
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) acc_s[warp][lane + 32 * e] = acc[e];
+    __syncthreads();
+    sr = se = 0.f;
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) sr += red[k][1], se += red[k][2];
+    const int row = sp.z * MT + r, tok = row / p.group, hq = sp.y * p.group + (row - tok * p.group);
+    if (tid < p.d) {
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < kJoinWarps; ++k) v += acc_s[k][tid];
+      static_cast<DT*>(p.out)[((long long)(s.q_start + tok) * p.Hq + hq) * p.d + tid] = DT(sr == 0.f ? 0.f : v / sr);
+    }
+    if (tid == 0 && p.lse)
+      p.lse[(long long)hq * p.T + s.q_start + tok] = se == 0.f ? -INFINITY : use * 0.69314718055994531f + logf(se);
+    __syncthreads();
+  }
+}
+
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+constexpr int kMaxRows = 32;   // rows of a tile at most
+constexpr size_t kSplitBytes = kMaxCtas * sizeof(int4);
+constexpr size_t part_bytes(int dp) { return (size_t)kMaxCtas * 2 * kMaxRows * (dp + 3) * 4; }
+
+template <typename DT, int DP, int MT>
+int launch_paged(PagedArgs& p, long long row_hint, char* ws, int sms, cudaStream_t st) {
+  p.splits = reinterpret_cast<int4*>(ws);
+  p.part_o = reinterpret_cast<float*>(ws + kSplitBytes);
+  p.part_m = p.part_o + (size_t)kMaxCtas * 2 * MT * DP;
+  auto kern = attn_paged_kernel<DT, DP, MT>;
+  constexpr int smem = PagedSmem<DP, MT>::kBytes;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return THD_ERR_CUDA;
+  const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+  kern<<<grid, kWarps * 32, smem, st>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, (unsigned)(row_hint < 8 ? row_hint : 8));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<DT, DP, MT>, static_cast<const PagedArgs>(p)) == cudaSuccess
+             ? THD_OK
+             : THD_ERR_CUDA;
+}
+
+template <typename DT>
+int launch_paged_of(PagedArgs& p, long long row_hint, char* ws, int sms, cudaStream_t st) {
+  if (p.d > 64) {
+    if (row_hint <= 16) return launch_paged<DT, 128, 16>(p, row_hint, ws, sms, st);
+    return launch_paged<DT, 128, 32>(p, row_hint, ws, sms, st);
+  }
+  if (row_hint <= 16) return launch_paged<DT, 64, 16>(p, row_hint, ws, sms, st);
+  return launch_paged<DT, 64, 32>(p, row_hint, ws, sms, st);
+}
+
+}  // namespace
+}  // namespace thd
+
+extern "C" {
+
+size_t thd_attn_paged_workspace_size(int head_dim) {
+  if (head_dim < 8 || head_dim > 128 || head_dim % 8 != 0) return 0;
+  return thd::kSplitBytes + thd::part_bytes(head_dim > 64 ? 128 : 64);
+}
+
+int thd_attn_paged(const void* q, const void* k_cache, const void* v_cache, const int64_t* cache_strides,
+                   int num_pages, int page_size, const int32_t* page_table, int64_t page_table_stride, int max_pages,
+                   const int32_t* kv_lens, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_q_padded,
+                   int batch_size, int max_seqlen_q, const int64_t* tree_mask, int tree_words, float softmax_scale,
+                   void* out, float* lse, int total_tokens, int num_heads_q, int num_heads_kv, int head_dim, int dtype,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace thd;
+  if (batch_size < 0 || max_seqlen_q < 0 || total_tokens < 0) return THD_ERR_ARG;
+  if (num_heads_q < 1 || num_heads_kv < 1 || num_pages < 0 || page_size < 1 || max_pages < 0) return THD_ERR_ARG;
+  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return THD_ERR_ARG;
+  if (dtype != THD_BF16 && dtype != THD_FP16) return THD_ERR_UNSUPPORTED;
+  if (head_dim < 8 || head_dim > 128 || head_dim % 8 != 0) return THD_ERR_UNSUPPORTED;
+  if (num_heads_q % num_heads_kv != 0) return THD_ERR_UNSUPPORTED;
+  const int group = num_heads_q / num_heads_kv;
+  // rows of a sequence and keys of a table are 32-bit
+  if ((long long)total_tokens * group >= (1ll << 30) || (long long)max_pages * page_size >= (1ll << 31) - kUnit)
+    return THD_ERR_UNSUPPORTED;
+  if ((long long)num_heads_q * head_dim >= (1ll << 31)) return THD_ERR_UNSUPPORTED;
+  if (tree_mask && (tree_words < 1 || tree_words > (1 << 20))) return THD_ERR_ARG;
+  if (!cache_strides || page_table_stride < max_pages) return THD_ERR_ARG;
+  for (int i = 0; i < 6; ++i)
+    if (cache_strides[i] < 0 || cache_strides[i] % 8 != 0) return THD_ERR_ARG;
+  if (total_tokens == 0) return THD_OK;
+  if (!q || !out || !on16(q) || !on16(out) || !on4(lse)) return THD_ERR_ARG;
+  if (!on4(page_table) || !on4(kv_lens) || !on4(cu_seqlens_q) || !on4(cu_seqlens_q_padded) ||
+      (reinterpret_cast<uintptr_t>(tree_mask) & 7) != 0)
+    return THD_ERR_ARG;
+  if (batch_size > 0 && (!kv_lens || !cu_seqlens_q)) return THD_ERR_ARG;
+  // without pages no sequence has keys
+  if (num_pages == 0) max_pages = 0;
+  if (batch_size > 0 && max_pages > 0 && (!page_table || !k_cache || !v_cache)) return THD_ERR_ARG;
+  if (!on16(k_cache) || !on16(v_cache)) return THD_ERR_ARG;
+  if (!workspace || !on16(workspace) || workspace_bytes < thd_attn_paged_workspace_size(head_dim))
+    return THD_ERR_WORKSPACE;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+    return THD_ERR_CUDA;
+  PagedArgs p{};
+  p.q = q;
+  p.kc = k_cache;
+  p.vc = v_cache;
+  p.table = page_table;
+  p.kv_lens = kv_lens;
+  p.cu = cu_seqlens_q;
+  p.padded = cu_seqlens_q_padded;
+  p.tree = reinterpret_cast<const long long*>(tree_mask);
+  p.out = out;
+  p.lse = lse;
+  p.table_stride = page_table_stride;
+  p.k_page = cache_strides[0];
+  p.k_token = cache_strides[1];
+  p.k_head = cache_strides[2];
+  p.v_page = cache_strides[3];
+  p.v_token = cache_strides[4];
+  p.v_head = cache_strides[5];
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  p.tree_words = tree_mask ? tree_words : 0;
+  p.B = batch_size;
+  p.T = total_tokens;
+  p.Hq = num_heads_q;
+  p.Hkv = num_heads_kv;
+  p.group = group;
+  p.d = head_dim;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  long long longest = max_seqlen_q > 0 && max_seqlen_q < total_tokens ? max_seqlen_q : total_tokens;
+  return dtype == THD_BF16
+             ? launch_paged_of<__nv_bfloat16>(p, longest * group, static_cast<char*>(workspace), sms,
+                                              static_cast<cudaStream_t>(stream))
+             : launch_paged_of<__half>(p, longest * group, static_cast<char*>(workspace), sms,
+                                       static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,96 @@
+// seq_rows.cuh — what the row operators share: the sequence a packed row belongs to,
+// and 16-bit element conversion.
+//
+// Packed rows, cu_seqlens and slot starts as everywhere in this library: sequence b holds rows
+// [start_b, start_b + cu[b+1] - cu[b]), start_b = padded[b] or cu[b], starts ascending.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace thd {
+
+// The sequence of row t and the row's place in it, found by the whole warp (every lane passes
+// the same t and gets the same answer); seq -1 for a row of no sequence.  Each step probes 32
+// starts at once, so 4096 sequences take three dependent loads instead of the twelve of a
+// bisection.  The answer is checked against the sequence's length, so metadata that does not
+// ascend gives rows of no sequence, never a place outside one.
+struct RowPlace {
+  int seq, pos;
+};
+
+__device__ __forceinline__ RowPlace find_row(const int32_t* __restrict__ cu, const int32_t* __restrict__ padded, int B,
+                                             int t) {
+  const int32_t* starts = padded ? padded : cu;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;   // the last start <= t lies in [lo, lo + n)
+  if (B <= 0) return {-1, 0};
+  for (;;) {
+    const int step = (n + 31) >> 5;
+    const int at = lane * step;
+    const bool le = at < n && starts[lo + at] <= t;
+    const int cnt = __popc(__ballot_sync(0xffffffffu, le));
+    if (cnt == 0) return {-1, 0};
+    lo += (cnt - 1) * step;
+    n = min(step, n - (cnt - 1) * step);
+    if (n <= 1) break;
+  }
+  // sequences without rows may share a start with the one before them
+  int b = lo;
+  int len = cu[b + 1] - cu[b];
+  while (len <= 0) {
+    const int back = b - 1 - lane;
+    const uint32_t some = __ballot_sync(0xffffffffu, back >= 0 && cu[max(back, 0) + 1] - cu[max(back, 0)] > 0);
+    if (some) {
+      b -= __ffs(some);
+      len = cu[b + 1] - cu[b];
+      break;
+    }
+    b -= 32;
+    if (b <= 0) return {-1, 0};
+  }
+  const long long pos = (long long)t - starts[b];
+  if (pos < 0 || pos >= len) return {-1, 0};
+  return {b, (int)pos};
+}
+
+template <typename DT>
+struct Pair16;
+template <>
+struct Pair16<__nv_bfloat16> {
+  __device__ static __forceinline__ float2 get(uint32_t x) {
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+  }
+  __device__ static __forceinline__ uint32_t put(float a, float b) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+};
+template <>
+struct Pair16<__half> {
+  __device__ static __forceinline__ float2 get(uint32_t x) {
+    return __half22float2(*reinterpret_cast<__half2*>(&x));
+  }
+  __device__ static __forceinline__ uint32_t put(float a, float b) {
+    __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+};
+
+template <typename DT>
+__device__ __forceinline__ void unpack8(const uint4& x, float* f) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = Pair16<DT>::get(u[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+template <typename DT>
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  return make_uint4(Pair16<DT>::put(f[0], f[1]), Pair16<DT>::put(f[2], f[3]), Pair16<DT>::put(f[4], f[5]),
+                    Pair16<DT>::put(f[6], f[7]));
+}
+
+}  // namespace thd
