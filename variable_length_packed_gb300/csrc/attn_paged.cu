@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int blocks = gridDim.x * gridDim.y, block = blockIdx.y * gridDim.x + blockIdx.x;
   for (int t = block * kJoinWarps + warp; t < p.T; t += blocks * kJoinWarps) {
-    const RowPlace at = find_row(p.cu, p.padded, p.B, t);
+    const RowSpan at = find_span(p.cu, p.padded, p.B, t);
     if (at.seq >= 0 && p.kv_lens[at.seq] > 0 && p.max_pages > 0) continue;
     uint4* dst = reinterpret_cast<uint4*>(static_cast<DT*>(p.out) + (long long)t * p.Hq * p.d);
     for (int i = lane; i < p.Hq * (p.d / 8); i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);

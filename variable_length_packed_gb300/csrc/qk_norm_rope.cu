@@ -53,6 +53,7 @@ struct RowArgs {
   int interleaved, weight_fp32;
   int q_items, k_items;      // blocks of heads per row
   int row_items;             // of all kinds
+  unsigned run;              // items of a warp
   // cache
   void* k_cache;
   void* v_cache;
@@ -63,48 +64,156 @@ struct RowArgs {
 
 constexpr int kRowWarps = 4;      // warps of a block
 constexpr int kRowPasses = 4;     // 32 / lanes-per-head heads in each
+constexpr int kRowStages = 2;     // the item worked on and one on the way
+constexpr int kRowBlocksPerSm = 4;
+constexpr int kRowRun = 6;        // items of a warp at most
 
-// cos / sin of a lane's two chunks.  Half-split: element e of both chunks turns by angle
-// 8 s + e.  Interleaved: pair e of the first chunk by 4 s + e, of the second by
-// 4 (s + rotary / 16) + e.
-struct Angles {
-  float c[8], s[8];
-};
-
-__device__ __forceinline__ void load_angles(Angles& a, const RowArgs& p, int slot, long long pos) {
-  const long long row = pos < 0 ? 0 : (pos >= p.rope_rows ? p.rope_rows - 1 : pos);
-  const int half = p.rotary >> 1;
-  const int at0 = p.interleaved ? 4 * slot : 8 * slot;
-  const int at1 = p.interleaved ? 4 * (slot + (p.rotary >> 4)) : 8 * slot + 4;
-  const float4 c0 = *reinterpret_cast<const float4*>(p.cos + row * half + at0);
-  const float4 c1 = *reinterpret_cast<const float4*>(p.cos + row * half + at1);
-  const float4 s0 = *reinterpret_cast<const float4*>(p.sin + row * half + at0);
-  const float4 s1 = *reinterpret_cast<const float4*>(p.sin + row * half + at1);
-  a.c[0] = c0.x, a.c[1] = c0.y, a.c[2] = c0.z, a.c[3] = c0.w;
-  a.c[4] = c1.x, a.c[5] = c1.y, a.c[6] = c1.z, a.c[7] = c1.w;
-  a.s[0] = s0.x, a.s[1] = s0.y, a.s[2] = s0.z, a.s[3] = s0.w;
-  a.s[4] = s1.x, a.s[5] = s1.y, a.s[6] = s1.z, a.s[7] = s1.w;
+// Two fp32 values in one 64-bit register: multiplied and added by one instruction.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split(f2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f2 swapped(f2 x) {
+  const float2 v = split(x);
+  return pair(v.y, v.x);
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+template <typename DT>
+__device__ __forceinline__ void unpack4(const uint4& x, f2* f) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = Pair16<DT>::get(u[i]);
+    f[i] = pair(v.x, v.y);
+  }
+}
+template <typename DT>
+__device__ __forceinline__ uint4 pack4(const f2* f) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = split(f[i]);
+    u[i] = Pair16<DT>::put(v.x, v.y);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// Turns a lane's two chunks; sign -1 turns back.
-__device__ __forceinline__ void turn(float* x0, float* x1, const Angles& a, int interleaved, float sign) {
-  if (interleaved) {
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The turn of a lane's two chunks by its angles, with a factor for each value before it:
+// y0 = a0 x0 + b0 z0, y1 = a1 x1 + b1 z1, where z is the other chunk (half-split) or the same one with
+// neighbours swapped (interleaved).  Half-split: value e of both chunks turns by angle 8 slot + e.
+// Interleaved: pair e of the first chunk by 4 slot + e, of the second by 4 (slot + rotary / 16) + e.
+struct Turn {
+  f2 a0[4], b0[4], a1[4], b1[4];
+};
+
+// A lane's angles from its tables' row: cos 0-3, cos 4-7, sin 0-3, sin 4-7, into four 16-byte places
+// that lie `apart` uint4s from one another.
+__device__ __forceinline__ void fetch_angles(uint4* dst, int apart, const RowArgs& p, int slot, long long pos) {
+  const long long row = pos < 0 ? 0 : (pos >= p.rope_rows ? p.rope_rows - 1 : pos);
+  const int half = p.rotary >> 1;
+  const long long at0 = row * half + (p.interleaved ? 4 * slot : 8 * slot);
+  const long long at1 = row * half + (p.interleaved ? 4 * (slot + (p.rotary >> 4)) : 8 * slot + 4);
+  copy16(dst, p.cos + at0);
+  copy16(dst + apart, p.cos + at1);
+  copy16(dst + 2 * apart, p.sin + at0);
+  copy16(dst + 3 * apart, p.sin + at1);
+}
+
+__device__ __forceinline__ void read_angles(const uint4* src, int apart, f2* c, f2* s) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float s0 = sign * a.s[e], s1 = sign * a.s[4 + e];
-      const float u0 = x0[2 * e], w0 = x0[2 * e + 1], u1 = x1[2 * e], w1 = x1[2 * e + 1];
-      x0[2 * e] = u0 * a.c[e] - w0 * s0;
-      x0[2 * e + 1] = w0 * a.c[e] + u0 * s0;
-      x1[2 * e] = u1 * a.c[4 + e] - w1 * s1;
-      x1[2 * e + 1] = w1 * a.c[4 + e] + u1 * s1;
+  for (int i = 0; i < 2; ++i) {
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(src + i * apart);
+    const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(src + (2 + i) * apart);
+    c[2 * i] = a.x, c[2 * i + 1] = a.y;
+    s[2 * i] = b.x, s[2 * i + 1] = b.y;
+  }
+}
+
+__device__ __forceinline__ f2 negated(f2 x) { return x ^ 0x8000000080000000ull; }
+
+__device__ __forceinline__ void make_turn(Turn& t, const f2* c, const f2* s, const f2* w0, const f2* w1, bool rot,
+                                          int interleaved) {
+  if (!rot) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t.a0[i] = w0[i];
+      t.a1[i] = w1[i];
+      t.b0[i] = t.b1[i] = 0ull;
+    }
+  } else if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 cl = split(c[i >> 1]), sl = split(s[i >> 1]), ch = split(c[2 + (i >> 1)]), sh = split(s[2 + (i >> 1)]);
+      const float c0 = i & 1 ? cl.y : cl.x, s0 = i & 1 ? sl.y : sl.x, c1 = i & 1 ? ch.y : ch.x, s1 = i & 1 ? sh.y : sh.x;
+      t.a0[i] = mul2(pair(c0, c0), w0[i]);
+      t.b0[i] = mul2(pair(-s0, s0), swapped(w0[i]));
+      t.a1[i] = mul2(pair(c1, c1), w1[i]);
+      t.b1[i] = mul2(pair(-s1, s1), swapped(w1[i]));
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float s = sign * a.s[e];
-      const float u = x0[e], w = x1[e];
-      x0[e] = u * a.c[e] - w * s;
-      x1[e] = w * a.c[e] + u * s;
+    for (int i = 0; i < 4; ++i) {
+      t.a0[i] = mul2(c[i], w0[i]);
+      t.b0[i] = mul2(negated(s[i]), w1[i]);
+      t.a1[i] = mul2(c[i], w1[i]);
+      t.b1[i] = mul2(s[i], w0[i]);
+    }
+  }
+}
+
+// A lane that holds no rotated values leaves out the other chunk, which need not be finite.
+__device__ __forceinline__ void apply_turn(const Turn& t, const f2* x0, const f2* x1, f2* y0, f2* y1, bool rot,
+                                           int interleaved) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y0[i] = mul2(x0[i], t.a0[i]);
+    y1[i] = mul2(x1[i], t.a1[i]);
+  }
+  if (rot) {
+    if (interleaved) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y0[i] = fma2(swapped(x0[i]), t.b0[i], y0[i]);
+        y1[i] = fma2(swapped(x1[i]), t.b1[i], y1[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y0[i] = fma2(x1[i], t.b0[i], y0[i]);
+        y1[i] = fma2(x0[i], t.b1[i], y1[i]);
+      }
     }
   }
 }
@@ -122,122 +231,257 @@ __device__ __forceinline__ void lane_chunks(int slot, int rotary, int& c0, int& 
 }
 
 template <typename DT>
-__device__ __forceinline__ void load_weight(const void* w, int fp32, int chunk, float* f) {
+__device__ __forceinline__ void load_weight(const void* w, int fp32, int chunk, f2* f) {
   if (fp32) {
-    const float4 a = reinterpret_cast<const float4*>(w)[2 * chunk], b = reinterpret_cast<const float4*>(w)[2 * chunk + 1];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    const ulonglong2 a = reinterpret_cast<const ulonglong2*>(w)[2 * chunk];
+    const ulonglong2 b = reinterpret_cast<const ulonglong2*>(w)[2 * chunk + 1];
+    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
   } else {
-    unpack8<DT>(reinterpret_cast<const uint4*>(w)[chunk], f);
+    unpack4<DT>(reinterpret_cast<const uint4*>(w)[chunk], f);
   }
 }
 
-template <int LPH>
-__device__ __forceinline__ float head_sum(float x) {
-#pragma unroll
-  for (int o = LPH / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
+// The items of a warp: a run of them.  More blocks than fit at once, each with short runs, beat a grid
+// of warps that stay (one long run each, or strided ones): the GPU's reads and writes then move
+// through memory as one front, and an SM that is slower takes fewer blocks.  Packed batch of 65536 rows of
+// 32 + 8 heads of 128, normed: 205 us against 225 (strided) and 255 (long runs); 131072 rows of
+// 16 + 16 without a norm: 322 us against 379 and 374.
+struct ItemWalk {
+  unsigned item, end, row_items, t, part;
 
-// LPH lanes per head (a power of two >= d / 16).
+  __device__ __forceinline__ ItemWalk(unsigned total, unsigned row_items_, unsigned warp, unsigned run)
+      : row_items(row_items_) {
+    const unsigned long long first = (unsigned long long)warp * run;
+    item = first < total ? (unsigned)first : total;
+    end = total - item < run ? total : item + run;
+    t = item / row_items;
+    part = item - t * row_items;
+  }
+  __device__ __forceinline__ bool more() const { return item < end; }
+  __device__ __forceinline__ void next() {
+    ++item;
+    if (++part == row_items) part = 0, ++t;
+  }
+};
+
+// Shared memory of a warp: kRowStages items, each its heads' chunks ([pass][chunk][lane]) and the
+// row's angles ([part][slot]).
+template <int kPasses, int kChunks, int LPH>
+struct alignas(16) RowStage {
+  uint4 x[kPasses][kChunks][32];
+  uint4 angle[4][LPH];
+};
+
+// LPH lanes per head (a power of two >= d / 16).  An item is a block of one row's heads of one
+// kind; a warp takes an equal run of items.  Two items ahead of the one it works on it looks up the
+// row and copies the heads and angles into shared memory, so that only arithmetic is left
+// when their turn comes; rows of no sequence are not read.
 template <typename DT, int LPH, bool kCache>
-__global__ void __launch_bounds__(kRowWarps * 32) head_rows_kernel(const RowArgs p) {
+__global__ void __launch_bounds__(kRowWarps * 32, kRowBlocksPerSm) head_rows_kernel(const RowArgs p) {
   constexpr int kPerPass = 32 / LPH;
-  const int lane = threadIdx.x & 31;
-  const unsigned item = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  const unsigned t = item / (unsigned)p.row_items;
-  if (t >= (unsigned)p.T) return;
-  int part = (int)(item - t * (unsigned)p.row_items);
-  int kind = 0;   // 0 queries, 1 keys, 2 values
-  HeadRows h = p.q;
-  if (part >= p.q_items) {
-    part -= p.q_items;
-    kind = 1;
-    h = p.k;
-    if (kCache && part >= p.k_items) {
-      part -= p.k_items;
-      kind = 2;
-      h = p.v;
-    }
-  }
+  constexpr int kAhead = kRowStages - 1;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto* ring = reinterpret_cast<RowStage<kRowPasses, 2, LPH>*>(smem) + warp * kRowStages;
+  ItemWalk ahead((unsigned)p.T * (unsigned)p.row_items, (unsigned)p.row_items, blockIdx.x * kRowWarps + warp,
+                 p.run);
+  ItemWalk now = ahead;
   const int slot = lane % LPH;
-  const int head0 = part * (kRowPasses * kPerPass) + lane / LPH;
   const bool mine = slot < (p.d >> 4);
   int c0, c1;
   lane_chunks(slot, p.rotary, c0, c1);
 
-  uint4 raw[kRowPasses][2];
-  const DT* src = static_cast<const DT*>(h.src) + (long long)t * h.src_stride;
-#pragma unroll
-  for (int i = 0; i < kRowPasses; ++i) {
-    const int head = head0 + i * kPerPass;
-    raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
-    if (mine && head < h.heads) {
-      raw[i][0] = *reinterpret_cast<const uint4*>(src + (long long)head * p.d + 8 * c0);
-      raw[i][1] = *reinterpret_cast<const uint4*>(src + (long long)head * p.d + 8 * c1);
+  auto kind_of = [&](int part, int& block) {   // 0 queries, 1 keys, 2 values
+    if (part < p.q_items) {
+      block = part;
+      return 0;
     }
-  }
-  const bool norm = kind != 2 && h.weight != nullptr;
-  float w0[8], w1[8];
-  if (norm && mine) {
-    load_weight<DT>(h.weight, p.weight_fp32, c0, w0);
-    load_weight<DT>(h.weight, p.weight_fp32, c1, w1);
-  }
-  const RowPlace at = find_row(p.cu, p.padded, p.B, (int)t);
-  long long pos = at.pos;
-  DT* dst;
-  long long dst_head = p.d;
-  if (at.seq >= 0) pos += p.offsets ? p.offsets[at.seq] : 0;
-  if (kCache && kind != 0) {
-    if (at.seq < 0 || pos < 0) return;
-    const long long page_at = pos / p.page_size;
-    if (page_at >= p.max_pages) return;
-    const int page = p.table[(long long)at.seq * p.table_stride + page_at];
-    if (page < 0 || page >= p.num_pages) return;
-    const long long off = pos - page_at * p.page_size;
-    dst = kind == 1 ? static_cast<DT*>(p.k_cache) + page * p.k_page + off * p.k_token
-                    : static_cast<DT*>(p.v_cache) + page * p.v_page + off * p.v_token;
-    dst_head = kind == 1 ? p.k_head : p.v_head;
-  } else {
-    dst = static_cast<DT*>(h.dst) + (long long)t * h.dst_stride;
-  }
-  const bool rot = kind != 2 && slot < (p.rotary >> 4);
-  Angles a;
-  if (at.seq >= 0 && rot) load_angles(a, p, slot, kCache && p.positions ? (long long)p.positions[t] : pos);
+    block = part - p.q_items;
+    if (!kCache || block < p.k_items) return 1;
+    block -= p.k_items;
+    return 2;
+  };
+  auto rows_of = [&](int kind) -> const HeadRows& { return kind == 0 ? p.q : (kCache && kind == 2 ? p.v : p.k); };
+
+  // What is known of an item when it is fetched: whether its row is of a sequence, and (cache) its
+  // place: page (-1: none) and token in it.
+  struct Item {
+    int seq, page, in;
+  };
+  Item items[kAhead + 1];
+  RowCursor cursor;
+  auto fetch_next = [&](int stage) {
+    Item it{-1, -1, 0};
+    if (ahead.more()) {
+      const unsigned ft = ahead.t, fpart = ahead.part;
+      int block;
+      const int kind = kind_of((int)fpart, block);
+      const HeadRows& h = rows_of(kind);
+      cursor.move(p.cu, p.padded, p.B, (int)ft);
+      it.seq = cursor.span.seq;
+      bool read = it.seq >= 0;
+      if (read) {
+        long long pos = (long long)ft - cursor.span.from + (p.offsets ? p.offsets[it.seq] : 0);
+        if (kCache && kind != 0) {
+          const long long page_at = pos / p.page_size;
+          if (pos >= 0 && page_at < p.max_pages) {
+            it.page = p.table[(long long)it.seq * p.table_stride + page_at];
+            it.in = (int)(pos - page_at * p.page_size);
+          }
+          read = it.page >= 0 && it.page < p.num_pages;
+          if (!read) it.page = -1;
+        }
+        if (read && kind != 2 && lane < (p.rotary >> 4))
+          fetch_angles(&ring[stage].angle[0][lane], LPH, p, lane, kCache && p.positions ? (long long)p.positions[ft] : pos);
+      }
+      if (read && mine) {
+        const DT* src = static_cast<const DT*>(h.src) + (long long)ft * h.src_stride;
+        const int head0 = block * (kRowPasses * kPerPass) + lane / LPH;
 #pragma unroll
-  for (int i = 0; i < kRowPasses; ++i) {
-    const int head = head0 + i * kPerPass;
-    uint4 o0 = make_uint4(0u, 0u, 0u, 0u), o1 = o0;   // a row of no sequence
-    if (at.seq >= 0) {
-      if (norm || rot) {
-        float x0[8], x1[8];
-        unpack8<DT>(raw[i][0], x0);
-        unpack8<DT>(raw[i][1], x1);
-        if (norm) {
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss += x0[e] * x0[e] + x1[e] * x1[e];
-          const float r = rsqrtf(head_sum<LPH>(ss) * p.inv_d + p.eps);
-          if (mine) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              x0[e] *= r * w0[e];
-              x1[e] *= r * w1[e];
-            }
+        for (int i = 0; i < kRowPasses; ++i) {
+          const int head = head0 + i * kPerPass;
+          if (head < h.heads) {
+            copy16(&ring[stage].x[i][0][lane], src + (long long)head * p.d + 8 * c0);
+            copy16(&ring[stage].x[i][1][lane], src + (long long)head * p.d + 8 * c1);
           }
         }
-        if (rot) turn(x0, x1, a, p.interleaved, p.sin_sign);
-        o0 = pack8<DT>(x0);
-        o1 = pack8<DT>(x1);
-      } else {
-        o0 = raw[i][0];
-        o1 = raw[i][1];
+      }
+      ahead.next();
+    }
+    copy_commit();
+    items[kAhead] = it;
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    fetch_next(i);
+    items[i] = items[kAhead];
+  }
+  int stage = 0, turn_kind = -1;
+  Turn turn;
+  for (; now.more(); now.next()) {
+    const unsigned t = now.t, part = now.part;
+    __syncwarp();   // the stage filled now was read by every lane
+    fetch_next(stage == 0 ? kRowStages - 1 : stage - 1);
+    int block;
+    const int kind = kind_of((int)part, block);
+    const HeadRows& h = rows_of(kind);
+    const Item it = items[0];
+    DT* dst;
+    long long dst_head = p.d;
+    bool store = true;
+    if (kCache && kind != 0) {   // a row without a page is not written
+      store = it.page >= 0;
+      dst = kind == 1 ? static_cast<DT*>(p.k_cache) + it.page * p.k_page + it.in * p.k_token
+                      : static_cast<DT*>(p.v_cache) + it.page * p.v_page + it.in * p.v_token;
+      dst_head = kind == 1 ? p.k_head : p.v_head;
+    } else {
+      dst = static_cast<DT*>(h.dst) + (long long)t * h.dst_stride;
+    }
+    const bool norm = kind != 2 && h.weight != nullptr;
+    const bool turns = kind != 2 && p.rotary > 0;
+    const bool rot = turns && slot < (p.rotary >> 4);
+    const int head0 = block * (kRowPasses * kPerPass);
+    DT* out = dst + (head0 + lane / LPH) * dst_head;
+    copy_wait<kAhead>();
+    __syncwarp();
+    if (store && it.seq < 0) {
+#pragma unroll
+      for (int i = 0; i < kRowPasses; ++i) {
+        if (mine && head0 + i * kPerPass + lane / LPH < h.heads) {
+          *reinterpret_cast<uint4*>(out + i * kPerPass * dst_head + 8 * c0) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(out + i * kPerPass * dst_head + 8 * c1) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    } else if (store) {
+      const auto& st = ring[stage];
+      if ((norm || turns) && (block == 0 || turn_kind != kind)) {   // a row's blocks of one kind turn alike
+        f2 c[4], s[4], w0[4], w1[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w0[e] = w1[e] = pair(1.f, 1.f);
+        if (norm && mine) {
+          load_weight<DT>(h.weight, p.weight_fp32, c0, w0);
+          load_weight<DT>(h.weight, p.weight_fp32, c1, w1);
+        }
+        if (rot) {
+          read_angles(&st.angle[0][slot], LPH, c, s);
+          if (p.sin_sign < 0.f) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] = negated(s[e]);
+          }
+        }
+        make_turn(turn, c, s, w0, w1, rot, p.interleaved);
+        turn_kind = kind;
+      }
+      // two passes at a time, side by side
+#pragma unroll
+      for (int i = 0; i < kRowPasses; i += 2) {
+        if (head0 + i * kPerPass >= h.heads) break;
+        uint4 v[2][2];
+        bool have[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          have[k] = mine && head0 + (i + k) * kPerPass + lane / LPH < h.heads;
+          v[k][0] = v[k][1] = make_uint4(0u, 0u, 0u, 0u);
+          if (have[k]) {
+            v[k][0] = st.x[i + k][0][lane];
+            v[k][1] = st.x[i + k][1][lane];
+          }
+        }
+        if (norm || turns) {
+          f2 y[2][2][4];
+          float sum[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            f2 x0[4], x1[4];
+            unpack4<DT>(v[k][0], x0);
+            unpack4<DT>(v[k][1], x1);
+            apply_turn(turn, x0, x1, y[k][0], y[k][1], rot, p.interleaved);
+            f2 sq = mul2(x0[0], x0[0]), sq1 = mul2(x1[0], x1[0]);
+#pragma unroll
+            for (int e = 1; e < 4; ++e) {
+              sq = fma2(x0[e], x0[e], sq);
+              sq1 = fma2(x1[e], x1[e], sq1);
+            }
+            const float2 sqs = split(add2(sq, sq1));
+            sum[k] = sqs.x + sqs.y;
+          }
+          if (norm) {
+#pragma unroll
+            for (int o = LPH / 2; o > 0; o >>= 1) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float r = rsqrtf(sum[k] * p.inv_d + p.eps);
+              const f2 rr = pair(r, r);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                y[k][0][e] = mul2(y[k][0][e], rr);
+                y[k][1][e] = mul2(y[k][1][e], rr);
+              }
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            v[k][0] = pack4<DT>(y[k][0]);
+            v[k][1] = pack4<DT>(y[k][1]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (have[k]) {
+            *reinterpret_cast<uint4*>(out + (i + k) * kPerPass * dst_head + 8 * c0) = v[k][0];
+            *reinterpret_cast<uint4*>(out + (i + k) * kPerPass * dst_head + 8 * c1) = v[k][1];
+          }
+        }
       }
     }
-    if (mine && head < h.heads) {
-      *reinterpret_cast<uint4*>(dst + head * dst_head + 8 * c0) = o0;
-      *reinterpret_cast<uint4*>(dst + head * dst_head + 8 * c1) = o1;
-    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) items[i] = items[i + 1];
+    stage = stage == kRowStages - 1 ? 0 : stage + 1;
   }
+  copy_wait<0>();
 }
 
 // ---------------------------------------------------------------------------- backward
@@ -247,129 +491,226 @@ struct NormBwdArgs {
   const void* gk;
   float* partial;            // [blocks][d]
   int q_blocks, k_blocks;
+  unsigned run;              // items of a warp
 };
 
 constexpr int kBwdPasses = 2;
 constexpr int kBwdWarps = 4;
-constexpr int kBwdBlocksPerSm = 4;
-constexpr int kBwdMaxBlocks = 1024;
+constexpr int kBwdStages = 3;
+constexpr int kBwdRun = 6;        // items of a warp, more where that would give over kBwdMaxBlocks blocks
+constexpr int kBwdBlocksPerSm = 3;
+constexpr int kBwdMaxBlocks = 4096;
 
+// A block works on one kind (queries or keys), so that a lane keeps one sum for dw.  Copies ahead as
+// the forward does: gradients in chunks 0 and 1 of a stage, inputs in 2 and 3.
 template <typename DT, int LPH>
-__global__ void __launch_bounds__(kBwdWarps * 32) head_rows_bwd_kernel(const NormBwdArgs b) {
+__global__ void __launch_bounds__(kBwdWarps * 32, kBwdBlocksPerSm) head_rows_bwd_kernel(const NormBwdArgs b) {
   constexpr int kPerPass = 32 / LPH;
+  constexpr int kAhead = kBwdStages - 1;
+  extern __shared__ __align__(16) unsigned char smem[];
   const RowArgs& p = b.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto* ring = reinterpret_cast<RowStage<kBwdPasses, 4, LPH>*>(smem) + warp * kBwdStages;
   const bool is_q = (int)blockIdx.x < b.q_blocks;
-  const HeadRows h = is_q ? p.q : p.k;
+  const HeadRows& h = is_q ? p.q : p.k;
   const DT* grad = static_cast<const DT*>(is_q ? b.gq : b.gk);
-  const unsigned items = (unsigned)(is_q ? p.q_items : p.k_items);
-  const unsigned blocks = (unsigned)(is_q ? b.q_blocks : b.k_blocks);
-  const unsigned first = (unsigned)(is_q ? blockIdx.x : blockIdx.x - b.q_blocks) * kBwdWarps + warp;
+  const unsigned row_items = (unsigned)(is_q ? p.q_items : p.k_items);
+  ItemWalk ahead((unsigned)p.T * row_items, row_items, (is_q ? blockIdx.x : blockIdx.x - b.q_blocks) * kBwdWarps + warp,
+                 b.run);
+  ItemWalk now = ahead;
   const int slot = lane % LPH;
   const bool mine = slot < (p.d >> 4);
   const bool norm = h.weight != nullptr;
+  const bool rot = slot < (p.rotary >> 4);
   int c0, c1;
   lane_chunks(slot, p.rotary, c0, c1);
-  float w0[8], w1[8], dw0[8], dw1[8];
+  f2 w0[4], w1[4], dw0[4], dw1[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w0[e] = w1[e] = dw0[e] = dw1[e] = 0.f;
+  for (int e = 0; e < 4; ++e) w0[e] = w1[e] = dw0[e] = dw1[e] = 0ull;
   if (norm && mine) {
     load_weight<DT>(h.weight, p.weight_fp32, c0, w0);
     load_weight<DT>(h.weight, p.weight_fp32, c1, w1);
   }
-  const bool rot = slot < (p.rotary >> 4);
-  const unsigned total = (unsigned)p.T * items;
-  for (unsigned item = first; item < total; item += blocks * kBwdWarps) {
-    const unsigned t = item / items;
-    const int head0 = (int)(item - t * items) * (kBwdPasses * kPerPass) + lane / LPH;
-    const DT* src = static_cast<const DT*>(h.src) + (long long)t * h.src_stride;
-    const DT* gsrc = grad + (long long)t * h.heads * p.d;
-    DT* dst = static_cast<DT*>(h.dst) + (long long)t * h.dst_stride;
-    uint4 rx[kBwdPasses][2], rg[kBwdPasses][2];
+  RowCursor cursor;
+  bool inside[kAhead + 1];   // whether the item's row is of a sequence
+  auto fetch_next = [&](int stage) {
+    bool in = false;
+    if (ahead.more()) {
+      const unsigned ft = ahead.t, fpart = ahead.part;
+      cursor.move(p.cu, p.padded, p.B, (int)ft);
+      in = cursor.span.seq >= 0;
+      if (in) {
+        if (lane < (p.rotary >> 4))
+          fetch_angles(&ring[stage].angle[0][lane], LPH, p, lane,
+                       (long long)ft - cursor.span.from + (p.offsets ? p.offsets[cursor.span.seq] : 0));
+        const DT* src = static_cast<const DT*>(h.src) + (long long)ft * h.src_stride;
+        const DT* gsrc = grad + (long long)ft * h.heads * p.d;
 #pragma unroll
-    for (int i = 0; i < kBwdPasses; ++i) {
-      const int head = head0 + i * kPerPass;
-      rx[i][0] = rx[i][1] = rg[i][0] = rg[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (mine && head < h.heads) {
-        const long long at = (long long)head * p.d;
-        rg[i][0] = *reinterpret_cast<const uint4*>(gsrc + at + 8 * c0);
-        rg[i][1] = *reinterpret_cast<const uint4*>(gsrc + at + 8 * c1);
-        if (norm) {
-          rx[i][0] = *reinterpret_cast<const uint4*>(src + at + 8 * c0);
-          rx[i][1] = *reinterpret_cast<const uint4*>(src + at + 8 * c1);
-        }
-      }
-    }
-    const RowPlace at = find_row(p.cu, p.padded, p.B, (int)t);
-    Angles a;
-    if (at.seq >= 0 && rot) load_angles(a, p, slot, (long long)at.pos + (p.offsets ? p.offsets[at.seq] : 0));
-#pragma unroll
-    for (int i = 0; i < kBwdPasses; ++i) {
-      const int head = head0 + i * kPerPass;
-      uint4 o0 = make_uint4(0u, 0u, 0u, 0u), o1 = o0;
-      if (at.seq >= 0) {
-        float g0[8], g1[8];
-        unpack8<DT>(rg[i][0], g0);
-        unpack8<DT>(rg[i][1], g1);
-        if (rot) turn(g0, g1, a, p.interleaved, -1.f);
-        if (norm) {
-          float x0[8], x1[8];
-          unpack8<DT>(rx[i][0], x0);
-          unpack8<DT>(rx[i][1], x1);
-          float ss = 0.f, dot = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            ss += x0[e] * x0[e] + x1[e] * x1[e];
-            dot += g0[e] * w0[e] * x0[e] + g1[e] * w1[e] * x1[e];
-          }
-          ss = head_sum<LPH>(ss);
-          dot = head_sum<LPH>(dot);
-          // past the last head there is nothing, and with eps = 0 its 1 / rms has no value
-          const float r = head < h.heads ? rsqrtf(ss * p.inv_d + p.eps) : 0.f;
-          const float m = dot * p.inv_d * r * r;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            dw0[e] += g0[e] * x0[e] * r;
-            dw1[e] += g1[e] * x1[e] * r;
-            g0[e] = r * (g0[e] * w0[e] - x0[e] * m);
-            g1[e] = r * (g1[e] * w1[e] - x1[e] * m);
+        for (int i = 0; i < kBwdPasses; ++i) {
+          const int head = ((int)fpart * kBwdPasses + i) * kPerPass + lane / LPH;
+          if (mine && head < h.heads) {
+            const long long at = (long long)head * p.d;
+            copy16(&ring[stage].x[i][0][lane], gsrc + at + 8 * c0);
+            copy16(&ring[stage].x[i][1][lane], gsrc + at + 8 * c1);
+            if (norm) {
+              copy16(&ring[stage].x[i][2][lane], src + at + 8 * c0);
+              copy16(&ring[stage].x[i][3][lane], src + at + 8 * c1);
+            }
           }
         }
-        o0 = pack8<DT>(g0);
-        o1 = pack8<DT>(g1);
       }
-      if (mine && head < h.heads) {
-        *reinterpret_cast<uint4*>(dst + (long long)head * p.d + 8 * c0) = o0;
-        *reinterpret_cast<uint4*>(dst + (long long)head * p.d + 8 * c1) = o1;
-      }
+      ahead.next();
     }
+    copy_commit();
+    inside[kAhead] = in;
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    fetch_next(i);
+    inside[i] = inside[kAhead];
   }
+  int stage = 0;
+  for (; now.more(); now.next()) {
+    const unsigned t = now.t, part = now.part;
+    __syncwarp();   // the stage filled now was read by every lane
+    fetch_next(stage == 0 ? kBwdStages - 1 : stage - 1);
+    const int head0 = (int)part * (kBwdPasses * kPerPass);
+    DT* out = static_cast<DT*>(h.dst) + (long long)t * h.dst_stride + (long long)(head0 + lane / LPH) * p.d;
+    copy_wait<kAhead>();
+    __syncwarp();
+    if (!inside[0]) {
+#pragma unroll
+      for (int i = 0; i < kBwdPasses; ++i) {
+        if (mine && head0 + i * kPerPass + lane / LPH < h.heads) {
+          *reinterpret_cast<uint4*>(out + (long long)i * kPerPass * p.d + 8 * c0) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(out + (long long)i * kPerPass * p.d + 8 * c1) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    } else {
+      const auto& st = ring[stage];
+      f2 c[4], s[4];
+      if (rot) read_angles(&st.angle[0][slot], LPH, c, s);
+      f2 h0[kBwdPasses][4], h1[kBwdPasses][4], x0[kBwdPasses][4], x1[kBwdPasses][4];
+      float sum[kBwdPasses], along[kBwdPasses];
+      bool have[kBwdPasses];
+#pragma unroll
+      for (int i = 0; i < kBwdPasses; ++i) {
+        have[i] = mine && head0 + i * kPerPass + lane / LPH < h.heads;
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (have[i] && (k < 2 || norm)) v[k] = st.x[i][k][lane];
+        }
+        f2 g0[4], g1[4];
+        unpack4<DT>(v[0], g0);
+        unpack4<DT>(v[1], g1);
+        unpack4<DT>(v[2], x0[i]);
+        unpack4<DT>(v[3], x1[i]);
+        if (rot) {   // turned back
+          if (p.interleaved) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 cl = split(c[e >> 1]), sl = split(s[e >> 1]);
+              const float2 ch = split(c[2 + (e >> 1)]), sh = split(s[2 + (e >> 1)]);
+              const float ca = e & 1 ? cl.y : cl.x, sa = e & 1 ? sl.y : sl.x;
+              const float cb = e & 1 ? ch.y : ch.x, sb = e & 1 ? sh.y : sh.x;
+              h0[i][e] = fma2(swapped(g0[e]), pair(sa, -sa), mul2(g0[e], pair(ca, ca)));
+              h1[i][e] = fma2(swapped(g1[e]), pair(sb, -sb), mul2(g1[e], pair(cb, cb)));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              h0[i][e] = fma2(g1[e], s[e], mul2(g0[e], c[e]));
+              h1[i][e] = fma2(negated(g0[e]), s[e], mul2(g1[e], c[e]));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h0[i][e] = g0[e], h1[i][e] = g1[e];
+        }
+        f2 sq0 = 0ull, sq1 = 0ull, dot0 = 0ull, dot1 = 0ull;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sq0 = fma2(x0[i][e], x0[i][e], sq0);
+          sq1 = fma2(x1[i][e], x1[i][e], sq1);
+          dot0 = fma2(mul2(h0[i][e], w0[e]), x0[i][e], dot0);
+          dot1 = fma2(mul2(h1[i][e], w1[e]), x1[i][e], dot1);
+        }
+        const float2 sqs = split(add2(sq0, sq1)), dots = split(add2(dot0, dot1));
+        sum[i] = sqs.x + sqs.y;
+        along[i] = dots.x + dots.y;
+      }
+      if (norm) {
+#pragma unroll
+        for (int o = LPH / 2; o > 0; o >>= 1) {
+#pragma unroll
+          for (int i = 0; i < kBwdPasses; ++i) {
+            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+            along[i] += __shfl_xor_sync(0xffffffffu, along[i], o);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBwdPasses; ++i) {
+          // past the last head there is nothing, and with eps = 0 its 1 / rms has no value
+          const float r = head0 + i * kPerPass + lane / LPH < h.heads ? rsqrtf(sum[i] * p.inv_d + p.eps) : 0.f;
+          const float m = -(along[i] * p.inv_d * r) * r * r;   // in an order that stays in range for tiny heads
+          const f2 rr = pair(r, r), mm = pair(m, m);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const f2 hr0 = mul2(h0[i][e], rr), hr1 = mul2(h1[i][e], rr);
+            dw0[e] = fma2(hr0, x0[i][e], dw0[e]);
+            dw1[e] = fma2(hr1, x1[i][e], dw1[e]);
+            h0[i][e] = fma2(hr0, w0[e], mul2(x0[i][e], mm));
+            h1[i][e] = fma2(hr1, w1[e], mul2(x1[i][e], mm));
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBwdPasses; ++i) {
+        if (have[i]) {
+          *reinterpret_cast<uint4*>(out + (long long)i * kPerPass * p.d + 8 * c0) = pack4<DT>(h0[i]);
+          *reinterpret_cast<uint4*>(out + (long long)i * kPerPass * p.d + 8 * c1) = pack4<DT>(h1[i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) inside[i] = inside[i + 1];
+    stage = stage == kBwdStages - 1 ? 0 : stage + 1;
+  }
+  copy_wait<0>();
   if (!norm) return;
   // the block's share of dw: over the warp's heads, then over the warps
-  __shared__ float sum[kBwdWarps][128];
+  __syncthreads();
+  float(*sum)[128] = reinterpret_cast<float(*)[128]>(smem);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < 4; ++e) {
+    float2 a = split(dw0[e]), c = split(dw1[e]);
 #pragma unroll
     for (int o = LPH; o < 32; o <<= 1) {
-      dw0[e] += __shfl_xor_sync(0xffffffffu, dw0[e], o);
-      dw1[e] += __shfl_xor_sync(0xffffffffu, dw1[e], o);
+      a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+      a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+      c.x += __shfl_xor_sync(0xffffffffu, c.x, o);
+      c.y += __shfl_xor_sync(0xffffffffu, c.y, o);
     }
     if (lane < LPH && mine) {
-      sum[warp][8 * c0 + e] = dw0[e];
-      sum[warp][8 * c1 + e] = dw1[e];
+      sum[warp][8 * c0 + 2 * e] = a.x;
+      sum[warp][8 * c0 + 2 * e + 1] = a.y;
+      sum[warp][8 * c1 + 2 * e] = c.x;
+      sum[warp][8 * c1 + 2 * e + 1] = c.y;
     }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < p.d; i += blockDim.x) {
-    float s = 0.f;
+    float total = 0.f;
 #pragma unroll
-    for (int k = 0; k < kBwdWarps; ++k) s += sum[k][i];
-    b.partial[(long long)blockIdx.x * p.d + i] = s;
+    for (int k = 0; k < kBwdWarps; ++k) total += sum[k][i];
+    b.partial[(long long)blockIdx.x * p.d + i] = total;
   }
 }
 
 // dw = the blocks' shares summed in a fixed order; a block takes 8 columns of one kind.
-constexpr int kSumRows = 32;
+constexpr int kSumRows = 128;
 __global__ void __launch_bounds__(kSumRows * 8) weight_sum_kernel(const float* __restrict__ partial, int q_blocks,
                                                                   int k_blocks, int d, float* dwq, float* dwk) {
   const int kind = blockIdx.y;
@@ -379,15 +720,16 @@ __global__ void __launch_bounds__(kSumRows * 8) weight_sum_kernel(const float* _
   const int begin = kind == 0 ? 0 : q_blocks, n = kind == 0 ? q_blocks : k_blocks;
   __shared__ float part[kSumRows][9];
   float s = 0.f;
+#pragma unroll 8
   for (int i = row; i < n; i += kSumRows) s += partial[(long long)(begin + i) * d + col];
   part[row][threadIdx.x & 7] = s;
   __syncthreads();
-  if (row == 0) {
-    s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kSumRows; ++i) s += part[i][threadIdx.x];
-    dst[col] = s;
+  for (int half = kSumRows / 2; half > 0; half >>= 1) {
+    if (row < half) part[row][threadIdx.x & 7] += part[row + half][threadIdx.x & 7];
+    __syncthreads();
   }
+  if (row == 0) dst[col] = part[0][threadIdx.x];
 }
 
 // ---------------------------------------------------------------------------- host
@@ -443,16 +785,36 @@ void fill_common(RowArgs& p, int B, int T, int d, float eps, int weight_fp32, co
   p.weight_fp32 = weight_fp32;
 }
 
+template <typename Args>
+int launch_with_smem(void (*kern)(const Args), const Args& args, unsigned grid, int warps, size_t smem, cudaStream_t st) {
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return THD_ERR_CUDA;
+  kern<<<grid, warps * 32, smem, st>>>(args);
+  return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
+}
+
+template <typename DT, int LPH, bool kCache>
+int launch_rows_at(const RowArgs& p, unsigned grid, cudaStream_t st) {
+  return launch_with_smem<RowArgs>(head_rows_kernel<DT, LPH, kCache>, p, grid, kRowWarps,
+                                   kRowWarps * kRowStages * sizeof(RowStage<kRowPasses, 2, LPH>), st);
+}
+
 template <typename DT, bool kCache>
 int launch_rows_of(const RowArgs& p, unsigned grid, cudaStream_t st) {
-  const dim3 block(kRowWarps * 32);
   switch (lanes_per_head(p.d)) {
-    case 1: head_rows_kernel<DT, 1, kCache><<<grid, block, 0, st>>>(p); break;
-    case 2: head_rows_kernel<DT, 2, kCache><<<grid, block, 0, st>>>(p); break;
-    case 4: head_rows_kernel<DT, 4, kCache><<<grid, block, 0, st>>>(p); break;
-    default: head_rows_kernel<DT, 8, kCache><<<grid, block, 0, st>>>(p); break;
+    case 1: return launch_rows_at<DT, 1, kCache>(p, grid, st);
+    case 2: return launch_rows_at<DT, 2, kCache>(p, grid, st);
+    case 4: return launch_rows_at<DT, 4, kCache>(p, grid, st);
+    default: return launch_rows_at<DT, 8, kCache>(p, grid, st);
   }
-  return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
+}
+
+int num_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
 }
 
 template <bool kCache>
@@ -465,21 +827,30 @@ int launch_rows(RowArgs& p, int dtype, cudaStream_t st) {
   const long long items = row_items * p.T;
   if (items >= (1ll << 31)) return THD_ERR_UNSUPPORTED;   // item numbers are 32-bit
   p.row_items = (int)row_items;
-  const unsigned grid = (unsigned)((items + kRowWarps - 1) / kRowWarps);
+  const int sms = num_sms();
+  if (sms <= 0) return THD_ERR_CUDA;
+  // as many items for a warp as leave all that fit at once one, kRowRun at most
+  const long long per_warp = items / ((long long)sms * kRowBlocksPerSm * kRowWarps);
+  p.run = per_warp < 1 ? 1u : (per_warp > kRowRun ? (unsigned)kRowRun : (unsigned)per_warp);
+  const unsigned grid = (unsigned)((items + (long long)kRowWarps * p.run - 1) / ((long long)kRowWarps * p.run));
   return dtype == THD_BF16 ? launch_rows_of<__nv_bfloat16, kCache>(p, grid, st)
                            : launch_rows_of<__half, kCache>(p, grid, st);
 }
 
+template <typename DT, int LPH>
+int launch_bwd_at(const NormBwdArgs& b, unsigned grid, cudaStream_t st) {
+  return launch_with_smem<NormBwdArgs>(head_rows_bwd_kernel<DT, LPH>, b, grid, kBwdWarps,
+                                       kBwdWarps * kBwdStages * sizeof(RowStage<kBwdPasses, 4, LPH>), st);
+}
+
 template <typename DT>
 int launch_bwd_of(const NormBwdArgs& b, unsigned grid, cudaStream_t st) {
-  const dim3 block(kBwdWarps * 32);
   switch (lanes_per_head(b.a.d)) {
-    case 1: head_rows_bwd_kernel<DT, 1><<<grid, block, 0, st>>>(b); break;
-    case 2: head_rows_bwd_kernel<DT, 2><<<grid, block, 0, st>>>(b); break;
-    case 4: head_rows_bwd_kernel<DT, 4><<<grid, block, 0, st>>>(b); break;
-    default: head_rows_bwd_kernel<DT, 8><<<grid, block, 0, st>>>(b); break;
+    case 1: return launch_bwd_at<DT, 1>(b, grid, st);
+    case 2: return launch_bwd_at<DT, 2>(b, grid, st);
+    case 4: return launch_bwd_at<DT, 4>(b, grid, st);
+    default: return launch_bwd_at<DT, 8>(b, grid, st);
   }
-  return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
 }
 
 }  // namespace
@@ -555,10 +926,8 @@ int thd_qk_norm_rope_bwd(const void* grad_q, const void* grad_k, const void* q, 
   }
   if (!workspace || !on16(workspace) || workspace_bytes < thd_qk_norm_rope_bwd_workspace_size(head_dim))
     return THD_ERR_WORKSPACE;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-    return THD_ERR_CUDA;
+  const int sms = num_sms();
+  if (sms <= 0) return THD_ERR_CUDA;
   const int per = kBwdPasses * (32 / lanes_per_head(head_dim));
   NormBwdArgs b{};
   p.q = HeadRows{q, dq, q_weight, q_stride, dq_stride, num_heads_q};
@@ -566,19 +935,17 @@ int thd_qk_norm_rope_bwd(const void* grad_q, const void* grad_k, const void* q, 
   p.q_items = blocks_of_heads(num_heads_q, per);
   p.k_items = blocks_of_heads(num_heads_kv, per);
   const long long qi = (long long)p.q_items * total_tokens, ki = (long long)p.k_items * total_tokens;
-  // item numbers are 32-bit, and the loop adds one stride of the grid past the last
-  if (qi >= (1ll << 31) || ki >= (1ll << 31)) return THD_ERR_UNSUPPORTED;
-  // blocks in proportion to the items of each kind, at most one item's worth of warps each
-  long long blocks = (long long)sms * kBwdBlocksPerSm;
-  if (blocks > kBwdMaxBlocks) blocks = kBwdMaxBlocks;
-  const long long want_q = (qi + kBwdWarps - 1) / kBwdWarps, want_k = (ki + kBwdWarps - 1) / kBwdWarps;
-  long long qb = want_q, kb = want_k;
-  if (want_q + want_k > blocks) {
-    qb = blocks * want_q / (want_q + want_k);
-    if (want_q > 0 && qb < 1) qb = 1;
-    if (want_k > 0 && qb > blocks - 1) qb = blocks - 1;
-    kb = want_k < blocks - qb ? want_k : blocks - qb;
-  }
+  if (qi >= (1ll << 31) || ki >= (1ll << 31)) return THD_ERR_UNSUPPORTED;   // item numbers are 32-bit
+  // runs as in launch_rows, but of such a length that there are at most kBwdMaxBlocks blocks: each
+  // leaves a share of dw to be summed
+  const long long resident = (long long)sms * kBwdBlocksPerSm * kBwdWarps;
+  const long long most = (long long)(kBwdMaxBlocks - 2) * kBwdWarps, least = (qi + ki + most - 1) / most;
+  long long run = (qi + ki) / resident;
+  run = run < 1 ? 1 : (run > kBwdRun ? kBwdRun : run);
+  if (run < least) run = least;
+  const long long per_block = run * kBwdWarps;
+  const long long qb = (qi + per_block - 1) / per_block, kb = (ki + per_block - 1) / per_block;
+  b.run = (unsigned)run;
   b.a = p;
   b.gq = grad_q;
   b.gk = grad_k;

@@ -10,31 +10,39 @@
 
 namespace thd {
 
-// The sequence of row t and the row's place in it, found by the whole warp (every lane passes
-// the same t and gets the same answer); seq -1 for a row of no sequence.  Each step probes 32
-// starts at once, so 4096 sequences take three dependent loads instead of the twelve of a
-// bisection.  The answer is checked against the sequence's length, so metadata that does not
-// ascend gives rows of no sequence, never a place outside one.
-struct RowPlace {
-  int seq, pos;
+// Where row t lies, found by the whole warp (every lane passes the same t and gets the same
+// answer): its sequence and the rows [from, to) of it, or seq -1 and rows after t that are
+// certainly of no sequence.  Each step probes 32 starts at once, so 4096 sequences take three
+// dependent loads instead of the twelve of a bisection.  The answer is checked against the
+// sequence's length, so metadata that does not ascend gives rows of no sequence, never a place
+// outside one.
+struct RowSpan {
+  int seq;
+  long long from, to;
 };
 
-__device__ __forceinline__ RowPlace find_row(const int32_t* __restrict__ cu, const int32_t* __restrict__ padded, int B,
+__device__ __forceinline__ RowSpan find_span(const int32_t* __restrict__ cu, const int32_t* __restrict__ padded, int B,
                                              int t) {
   const int32_t* starts = padded ? padded : cu;
   const int lane = threadIdx.x & 31;
+  const long long none = 1ll << 40;
+  if (B <= 0) return {-1, t, none};
   int lo = 0, n = B;   // the last start <= t lies in [lo, lo + n)
-  if (B <= 0) return {-1, 0};
   for (;;) {
     const int step = (n + 31) >> 5;
     const int at = lane * step;
     const bool le = at < n && starts[lo + at] <= t;
     const int cnt = __popc(__ballot_sync(0xffffffffu, le));
-    if (cnt == 0) return {-1, 0};
+    if (cnt == 0) {
+      const long long first = starts[lo];
+      return {-1, t, first > t ? first : t + 1ll};
+    }
     lo += (cnt - 1) * step;
     n = min(step, n - (cnt - 1) * step);
     if (n <= 1) break;
   }
+  long long next = lo + 1 < B ? (long long)starts[lo + 1] : none;
+  if (next <= t) next = t + 1ll;
   // sequences without rows may share a start with the one before them
   int b = lo;
   int len = cu[b + 1] - cu[b];
@@ -47,12 +55,22 @@ __device__ __forceinline__ RowPlace find_row(const int32_t* __restrict__ cu, con
       break;
     }
     b -= 32;
-    if (b <= 0) return {-1, 0};
+    if (b <= 0) return {-1, t, next};
   }
-  const long long pos = (long long)t - starts[b];
-  if (pos < 0 || pos >= len) return {-1, 0};
-  return {b, (int)pos};
+  const long long from = starts[b], to = from + len;
+  if (t < from || t >= to) return {-1, t, next};
+  return {b, from, to};
 }
+
+// The places of rows that a warp visits in ascending order: the span of the last one is kept and
+// looked up again only when a row leaves it.
+struct RowCursor {
+  RowSpan span{-1, 0, 0};
+
+  __device__ __forceinline__ void move(const int32_t* cu, const int32_t* padded, int B, int t) {
+    if (t < span.from || t >= span.to) span = find_span(cu, padded, B, t);
+  }
+};
 
 template <typename DT>
 struct Pair16;
