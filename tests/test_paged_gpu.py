@@ -329,3 +329,24 @@ def test_binding_refusals():
         with pytest.raises(error):
             call()
             pytest.fail(f"call {i} was not refused")
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """Wide tiles wait on barriers: with an injected wait and a short limit the call comes back with the
+    status bit set, and the next call is as if nothing had been."""
+    x = make([300, 500], [40, 33], 16, 8, 2, 128, BF16, words=1)
+    work = torch.zeros(vlp.thd_attn_paged_workspace_size(128), dtype=torch.uint8, device="cuda")
+    want = run(x, workspace=work, max_seqlen_q=40)
+    status = lambda: int(work[8:12].view(torch.int32).item())
+    assert status() == 0
+    vlp.thd_set_wait_limit_ns(1)
+    vlp.thd_set_wait_injection(True)
+    try:
+        run(x, workspace=work, max_seqlen_q=40)
+        assert status() == vlp.STATUS_WAIT_TIMEOUT
+    finally:
+        vlp.thd_set_wait_injection(False)
+        vlp.thd_set_wait_limit_ns(0)
+    got = run(x, workspace=work, max_seqlen_q=40)
+    assert status() == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    check(x, got)

@@ -25,134 +25,21 @@
 #include <cuda_runtime.h>
 
 #include "../../include/thd_attn.h"
-#include "seq_rows.cuh"
+#include "attn_paged_common.cuh"
+#include "attn_paged_wide.cuh"
 
 namespace thd {
+
+// the library's settings of waits inside kernels (thd_attn.cu)
+void wait_settings(uint64_t* limit_ns, uint32_t* check_mask, uint32_t* inject);
+
 namespace {
 
-constexpr int kUnit = 64;            // keys of a unit
 constexpr int kWarps = 4;            // warps of a CTA, 16 keys of the unit each
 constexpr int kWarpKeys = kUnit / kWarps;
 constexpr int kStages = 3;           // units in flight per warp
-constexpr int kMaxCtas = 320;        // CTAs of a launch at most (two on each of up to 160 SMs)
 constexpr int kJoinThreads = 256;
 
-struct PagedArgs {
-  const void* q;
-  const void* kc;
-  const void* vc;
-  const int32_t* table;
-  const int32_t* kv_lens;
-  const int32_t* cu;
-  const int32_t* padded;
-  const long long* tree;
-  void* out;
-  float* lse;
-  float* part_o;       // [ctas * 2][rows][DP]
-  float* part_m;       // [ctas * 2][3][rows]: maximum, sum of the rounded weights, sum of the weights
-  int4* splits;        // [ctas]: (sequence, head, row tile, CTAs of the tile), of the tile that starts in the CTA and ends in another
-  long long table_stride, k_page, k_token, k_head, v_page, v_token, v_head;   // elements
-  int num_pages, page_size, max_pages;
-  int tree_words;
-  int B, T, Hq, Hkv, group, d;
-  float scale_log2;
-};
-
-// One sequence of the batch, clamped to the buffers.
-struct SeqWork {
-  int q_start, q_len, kv_len, tiles, blocks;
-  long long units;
-};
-
-__device__ __forceinline__ SeqWork seq_work(const PagedArgs& p, int b, int rows_per_tile) {
-  SeqWork s;
-  const int c0 = p.cu[b], c1 = p.cu[b + 1];
-  long long qs = p.padded ? p.padded[b] : c0, ql = (long long)c1 - c0;
-  qs = qs < 0 ? 0 : (qs > p.T ? p.T : qs);
-  ql = ql < 0 ? 0 : (ql > p.T - qs ? p.T - qs : ql);
-  const long long room = (long long)p.max_pages * p.page_size;
-  long long kv = p.kv_lens[b];
-  kv = kv < 0 ? 0 : (kv > room ? room : kv);
-  s.q_start = (int)qs;
-  s.q_len = (int)ql;
-  s.kv_len = (int)kv;
-  const long long rows = ql * p.group;
-  s.tiles = (int)((rows + rows_per_tile - 1) / rows_per_tile);
-  s.blocks = (s.kv_len + kUnit - 1) / kUnit;
-  s.units = (long long)s.tiles * s.blocks * p.Hkv;
-  return s;
-}
-
-// The CTA's share of the batch's units, and the sequence its first unit lies in.  Every CTA
-// adds up the whole batch: each thread a run of sequences, then a scan over the threads.
-struct Share {
-  long long begin, end, seq_base;   // units; seq_base: first unit of sequence seq
-  long long total;
-  int ctas;                         // CTAs that have units
-  int seq;
-};
-
-__device__ __forceinline__ long long share_begin(long long total, int ctas, int c) { return total * c / ctas; }
-
-template <int kThreads>
-__device__ void find_share(const PagedArgs& p, int rows_per_tile, Share* out) {
-  __shared__ long long warp_sum[kThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_work(p, b, rows_per_tile).units;
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  long long before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
-  }
-  const long long excl = before + incl - mine;
-  const int ctas = total < gridDim.x ? (int)total : (int)gridDim.x;
-  if (tid == 0) {
-    out->total = total;
-    out->ctas = ctas;
-    out->begin = out->end = 0;
-    out->seq = 0;
-    out->seq_base = 0;
-  }
-  __syncthreads();
-  if ((int)blockIdx.x < ctas) {
-    const long long begin = share_begin(total, ctas, blockIdx.x);
-    if (begin >= excl && begin < excl + mine) {   // in this thread's run of sequences
-      long long base = excl;
-      int b = b0;
-      for (; b < b1; ++b) {
-        const long long u = seq_work(p, b, rows_per_tile).units;
-        if (begin < base + u) break;
-        base += u;
-      }
-      out->seq = b;
-      out->seq_base = base;
-      out->begin = begin;
-      out->end = share_begin(total, ctas, blockIdx.x + 1);
-    }
-  }
-  __syncthreads();
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -181,13 +68,6 @@ __device__ __forceinline__ void mma16816<__half>(float* c, const uint32_t* a, ui
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// 2^x, 0 at -inf (the hardware's approximation, 2 ulp)
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Shared memory of a CTA: each warp's ring of key and value tiles (16 rows of DP values,
 // 16-byte chunks XORed with the row so that eight rows of one column of chunks lie in
 // different banks); at a tile's end the warps' sums and outputs take its place.
@@ -215,60 +95,34 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   find_share<kWarps * 32>(p, MT, &share);
-  const long long begin = share.begin, end = share.end;
-  if (tid == 0) p.splits[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (tid == 0) {
+    p.splits[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    p.status[blockIdx.x] = 0u;
+  }
 
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * (kStages * 2 * kTileBytes);
   const int copy_key = lane / kChunks, copy_chunk = lane % kChunks;
   const bool copy_in = copy_chunk * 8 < p.d;
   const int ld_row = lane & 7, ld_mat = lane >> 3;   // ldmatrix: this lane's row of matrix ld_mat
 
-  long long u = begin, base = share.seq_base;
-  int b = share.seq;
-  while (u < end) {
-    const SeqWork s = seq_work(p, b, MT);
-    if (u - base >= s.units) {
-      base += s.units;
-      ++b;
-      continue;
-    }
-    const long long item = (u - base) / s.blocks;
-    const int blk0 = (int)(u - base - item * s.blocks);
-    const int nblk = (int)min((long long)(s.blocks - blk0), end - u);
-    const int head = (int)(item / s.tiles), tile = (int)(item - (long long)head * s.tiles);
-    const bool whole = nblk == s.blocks;
-    const int rows = (int)min((long long)MT, (long long)s.q_len * p.group - (long long)tile * MT);
-    const int row0 = tile * MT;           // of the sequence's rows
-    const int past = s.kv_len - s.q_len;  // keys before the new tokens (negative: fewer keys than tokens)
-    // keys that no row of the tile sees need not be read
-    const int last_tok = (row0 + rows - 1) / p.group;
-    const int key_end = p.tree ? s.kv_len : min(s.kv_len, max(0, past + last_tok + 1));
-    const int steps = min(nblk, max(0, (key_end + kUnit - 1) / kUnit - blk0));
-
+  PieceWalk walk(share);
+  Piece x;
+  while (walk.next<MT>(p, x)) {
     // ---- keys and values: this warp's 16 keys of unit blk0 + i ----
-    const int32_t* table = p.table + (long long)b * p.table_stride;
-    // lane l < 16 holds the element offset of key l, lane 16 + l that of value l
+    const int32_t* table = p.table + (long long)x.seq * p.table_stride;
+    // lane l < 16 holds the offset of key l, lane 16 + l that of value l
     auto offset_of = [&](int i) {
-      const int key = (blk0 + i) * kUnit + warp * kWarpKeys + (lane & 15);
-      long long off = 0;
-      if (i < steps && key < key_end) {
-        const int at = key / p.page_size;
-        int page = table[at];
-        page = page < 0 ? 0 : (page >= p.num_pages ? p.num_pages - 1 : page);
-        const int in = key - at * p.page_size;
-        off = lane < 16 ? page * p.k_page + in * p.k_token + head * p.k_head
-                        : page * p.v_page + in * p.v_token + head * p.v_head;
-      }
-      return off;
+      return i < x.steps ? cache_offset(p, x, table, (x.blk0 + i) * kUnit + warp * kWarpKeys + (lane & 15), lane >= 16)
+                         : 0ll;
     };
     auto issue = [&](int i, int stage, long long off) {
-      if (i < steps) {
-        const int first = (blk0 + i) * kUnit + warp * kWarpKeys;
+      if (i < x.steps) {
+        const int first = (x.blk0 + i) * kUnit + warp * kWarpKeys;
         const uint32_t dst = ring + stage * (2 * kTileBytes);
 #pragma unroll
         for (int c = 0; c < kCopies; ++c) {
           const int key = c * kLaneKeys + copy_key;
-          const bool take = copy_in && first + key < key_end;
+          const bool take = copy_in && first + key < x.key_end;
           const uint32_t at = key * (DP * 2) + ((copy_chunk ^ (key & 7)) << 4);
           const long long ko = __shfl_sync(0xffffffffu, off, key), vo = __shfl_sync(0xffffffffu, off, 16 + key);
           const int col = take ? copy_chunk * 8 : 0;
@@ -284,21 +138,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
 
     // ---- queries: the A fragments of the tile ----
     uint32_t qf[kMF][kKSteps][4];
-    int limit[kMF][2];            // last key of the row (no tree), -1 past the last row
-    const long long* bits[kMF][2];
+    int token[kMF][2];            // of the row, -1 past the last row
     const int qr = lane >> 2, qc = (lane & 3) * 2;
 #pragma unroll
     for (int f = 0; f < kMF; ++f) {
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const int r = f * 16 + hh * 8 + qr;
-        const int row = row0 + r;
+        const int row = x.row0 + r;
         const int tok = row / p.group;
-        const bool ok = r < rows;
-        limit[f][hh] = ok ? min(past + tok, s.kv_len - 1) : -1;
-        bits[f][hh] = p.tree && ok ? p.tree + (long long)(s.q_start + tok) * p.tree_words : nullptr;
+        const bool ok = r < x.rows;
+        token[f][hh] = ok ? tok : -1;
         const DT* src = static_cast<const DT*>(p.q) +
-                        ((long long)(s.q_start + tok) * p.Hq + head * p.group + (row - tok * p.group)) * p.d;
+                        ((long long)(x.s.q_start + tok) * p.Hq + x.head * p.group + (row - tok * p.group)) * p.d;
 #pragma unroll
         for (int k = 0; k < kKSteps; ++k) {
 #pragma unroll
@@ -325,7 +177,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
     }
 
     int stage = 0;
-    for (int i = 0; i < steps; ++i) {
+    for (int i = 0; i < x.steps; ++i) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
       {
@@ -334,7 +186,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
         next_off = offset_of(i + kStages);
       }
       const uint32_t kt = ring + stage * (2 * kTileBytes), vt = kt + kTileBytes;
-      const int first = (blk0 + i) * kUnit + warp * kWarpKeys;
+      const int unit0 = (x.blk0 + i) * kUnit;
       // ---- scores ----
       float c[kMF][2][4];
 #pragma unroll
@@ -355,8 +207,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
         }
       }
       // ---- visibility ----
-      // some key may be hidden from some row
-      const bool cut = first + kWarpKeys > min(p.tree ? past : past + 1, s.kv_len);
+      // some key of the unit may be hidden from some row
+      const bool cut = unit0 + kUnit > min(p.tree ? x.past : x.past + 1, x.s.kv_len);
 #pragma unroll
       for (int f = 0; f < kMF; ++f) {
 #pragma unroll
@@ -365,19 +217,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
           for (int e = 0; e < 4; ++e) c[f][n][e] *= p.scale_log2;
         if (cut) {
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = first + n * 8 + qc + (e & 1), hh = e >> 1;
-              bool see = key <= limit[f][hh];
-              if (p.tree) {
-                const int j = key - past;
-                see = key < s.kv_len;
-                if (see && j >= 0)
-                  see = bits[f][hh] && j < p.tree_words * 64 && ((bits[f][hh][j >> 6] >> (j & 63)) & 1);
-              }
-              if (!see) c[f][n][e] = -INFINITY;
-            }
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint64_t all = token[f][hh] >= 0 ? seen_keys(p, x, token[f][hh], unit0) : 0ull;
+            const uint32_t seen = (uint32_t)(all >> (warp * kWarpKeys)) >> qc;   // this lane's: bits 0, 1, 8, 9
+            if (!(seen & 1)) c[f][0][2 * hh] = -INFINITY;
+            if (!(seen & 2)) c[f][0][2 * hh + 1] = -INFINITY;
+            if (!(seen & 256)) c[f][1][2 * hh] = -INFINITY;
+            if (!(seen & 512)) c[f][1][2 * hh + 1] = -INFINITY;
           }
         }
       }
@@ -393,12 +239,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
           const float top = fmaxf(m[f][hh], x);
           const float use = top == -INFINITY ? 0.f : top;
-          scale[hh] = exp2_fast(m[f][hh] - use);
+          scale[hh] = ex2_approx(m[f][hh] - use);
           m[f][hh] = top;
           float sum = 0.f, sum_r = 0.f;
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const float p0 = exp2_fast(c[f][n][2 * hh] - use), p1 = exp2_fast(c[f][n][2 * hh + 1] - use);
+            const float p0 = ex2_approx(c[f][n][2 * hh] - use), p1 = ex2_approx(c[f][n][2 * hh + 1] - use);
             sum += p0 + p1;
             const uint32_t w = Pair16<DT>::put(p0, p1);
             const float2 r = Pair16<DT>::get(w);
@@ -461,9 +307,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
       }
     }
     __syncthreads();
-    const int part = blockIdx.x * 2 + (u == begin ? 0 : 1);
-    for (int x = tid; x < rows * kChunks; x += kWarps * 32) {
-      const int r = x / kChunks, chunk = x - r * kChunks;
+    const int part = part_of_piece(x);
+    for (int i = tid; i < x.rows * kChunks; i += kWarps * 32) {
+      const int r = i / kChunks, chunk = i - r * kChunks;
       float top = -INFINITY, w[kWarps], sr = 0.f, se = 0.f, acc[8];
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) top = fmaxf(top, jm[(k * 3) * MT + r]);
@@ -472,7 +318,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
       for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
-        w[k] = exp2_fast(jm[(k * 3) * MT + r] - use);
+        w[k] = ex2_approx(jm[(k * 3) * MT + r] - use);
         sr += w[k] * jm[(k * 3 + 1) * MT + r];
         se += w[k] * jm[(k * 3 + 2) * MT + r];
         const float4* src = reinterpret_cast<const float4*>(jo + (k * MT + r) * DP + chunk * 8);
@@ -480,16 +326,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
         acc[0] += w[k] * a.x, acc[1] += w[k] * a.y, acc[2] += w[k] * a.z, acc[3] += w[k] * a.w;
         acc[4] += w[k] * c.x, acc[5] += w[k] * c.y, acc[6] += w[k] * c.z, acc[7] += w[k] * c.w;
       }
-      if (whole) {
-        const int row = row0 + r, tok = row / p.group, hq = head * p.group + (row - tok * p.group);
+      if (x.whole) {
+        const int row = x.row0 + r, tok = row / p.group, hq = x.head * p.group + (row - tok * p.group);
         const float inv = sr == 0.f ? 0.f : 1.f / sr;   // a NaN sum stays one
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = sr == 0.f ? 0.f : acc[e] * inv;
         if (chunk * 8 < p.d)
-          *reinterpret_cast<uint4*>(static_cast<DT*>(p.out) + ((long long)(s.q_start + tok) * p.Hq + hq) * p.d +
+          *reinterpret_cast<uint4*>(static_cast<DT*>(p.out) + ((long long)(x.s.q_start + tok) * p.Hq + hq) * p.d +
                                     chunk * 8) = pack8<DT>(acc);
         if (chunk == 0 && p.lse)
-          p.lse[(long long)hq * p.T + s.q_start + tok] =
+          p.lse[(long long)hq * p.T + x.s.q_start + tok] =
               se == 0.f ? -INFINITY : use * 0.69314718055994531f + logf(se);
       } else {
         float4* dst = reinterpret_cast<float4*>(p.part_o + ((long long)part * MT + r) * DP + chunk * 8);
@@ -503,16 +349,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
         }
       }
     }
-    if (!whole && blk0 == 0 && tid == 0) {
-      // the tile starts here and ends in CTA c: the join goes over blockIdx.x .. c
-      const long long tile_end = base + (item + 1) * s.blocks;
-      int c = blockIdx.x + 1;
-      while (share_begin(share.total, share.ctas, c + 1) < tile_end) ++c;
-      // slot of the first partial in bit 30
-      p.splits[blockIdx.x] = make_int4(b, head, tile, (c - (int)blockIdx.x + 1) | (u == begin ? 0 : 1 << 30));
-    }
+    if (tid == 0) note_split(p, x, share);
     __syncthreads();   // the ring is filled again
-    u += nblk;
   }
 }
 
@@ -537,6 +375,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
       for (int h = lane; h < p.Hq; h += 32) p.lse[(long long)h * p.T + t] = -INFINITY;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (block == 0) {   // the call's status word, from the CTAs'
+    uint32_t bits = 0u;
+    for (int i = tid; i < (int)gridDim.x; i += kJoinThreads) bits |= p.status[i];
+    bits = __syncthreads_or(bits != 0u) ? THD_STATUS_WAIT_TIMEOUT : 0u;
+    if (tid == 0) *p.call_status = bits;
+  }
   const int4 sp = p.splits[blockIdx.x];
   if (sp.x < 0) return;
   const SeqWork s = seq_work(p, sp.x, MT);
@@ -557,7 +401,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
     float sr = 0.f, se = 0.f;
     for (int k = tid; k < n; k += kJoinThreads) {
       const float* pm = p.part_m + (long long)part_of(k) * 3 * MT;
-      const float w = exp2_fast(pm[r] - use);
+      const float w = ex2_approx(pm[r] - use);
       weight[k] = w;
       sr += w * pm[MT + r];
       se += w * pm[2 * MT + r];
@@ -601,20 +445,34 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
-constexpr int kMaxRows = 32;   // rows of a tile at most
-constexpr size_t kSplitBytes = kMaxCtas * sizeof(int4);
+// Workspace: the call's status word (byte 8), the CTAs' status words and split tiles, then the
+// partial results (outputs, then maxima and sums).
+constexpr int kMaxRows = 128;   // rows of a tile at most
+constexpr size_t kStatusAt = 256, kSplitAt = kStatusAt + kMaxCtas * sizeof(uint32_t);
+constexpr size_t kPartAt = kSplitAt + kMaxCtas * sizeof(int4);
 constexpr size_t part_bytes(int dp) { return (size_t)kMaxCtas * 2 * kMaxRows * (dp + 3) * 4; }
 
 template <typename DT, int DP, int MT>
 int launch_paged(PagedArgs& p, long long row_hint, char* ws, int sms, cudaStream_t st) {
-  p.splits = reinterpret_cast<int4*>(ws);
-  p.part_o = reinterpret_cast<float*>(ws + kSplitBytes);
+  p.call_status = reinterpret_cast<uint32_t*>(ws + 8);
+  p.status = reinterpret_cast<uint32_t*>(ws + kStatusAt);
+  p.splits = reinterpret_cast<int4*>(ws + kSplitAt);
+  p.part_o = reinterpret_cast<float*>(ws + kPartAt);
   p.part_m = p.part_o + (size_t)kMaxCtas * 2 * MT * DP;
-  auto kern = attn_paged_kernel<DT, DP, MT>;
-  constexpr int smem = PagedSmem<DP, MT>::kBytes;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return THD_ERR_CUDA;
   const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
-  kern<<<grid, kWarps * 32, smem, st>>>(p);
+  if constexpr (MT == kWideRows) {
+    auto kern = attn_paged_wide_kernel<DT, DP>;
+    constexpr int smem = (int)sizeof(WideSmem<DP>) + 1024;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return THD_ERR_CUDA;
+    kern<<<grid, kWideThreads, smem, st>>>(p);
+  } else {
+    auto kern = attn_paged_kernel<DT, DP, MT>;
+    constexpr int smem = PagedSmem<DP, MT>::kBytes;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return THD_ERR_CUDA;
+    kern<<<grid, kWarps * 32, smem, st>>>(p);
+  }
   if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, (unsigned)(row_hint < 8 ? row_hint : 8));
@@ -634,10 +492,12 @@ template <typename DT>
 int launch_paged_of(PagedArgs& p, long long row_hint, char* ws, int sms, cudaStream_t st) {
   if (p.d > 64) {
     if (row_hint <= 16) return launch_paged<DT, 128, 16>(p, row_hint, ws, sms, st);
-    return launch_paged<DT, 128, 32>(p, row_hint, ws, sms, st);
+    if (row_hint <= 32) return launch_paged<DT, 128, 32>(p, row_hint, ws, sms, st);
+    return launch_paged<DT, 128, kWideRows>(p, row_hint, ws, sms, st);
   }
   if (row_hint <= 16) return launch_paged<DT, 64, 16>(p, row_hint, ws, sms, st);
-  return launch_paged<DT, 64, 32>(p, row_hint, ws, sms, st);
+  if (row_hint <= 32) return launch_paged<DT, 64, 32>(p, row_hint, ws, sms, st);
+  return launch_paged<DT, 64, kWideRows>(p, row_hint, ws, sms, st);
 }
 
 }  // namespace
@@ -647,7 +507,7 @@ extern "C" {
 
 size_t thd_attn_paged_workspace_size(int head_dim) {
   if (head_dim < 8 || head_dim > 128 || head_dim % 8 != 0) return 0;
-  return thd::kSplitBytes + thd::part_bytes(head_dim > 64 ? 128 : 64);
+  return thd::kPartAt + thd::part_bytes(head_dim > 64 ? 128 : 64);
 }
 
 int thd_attn_paged(const void* q, const void* k_cache, const void* v_cache, const int64_t* cache_strides,
@@ -717,6 +577,7 @@ int thd_attn_paged(const void* q, const void* k_cache, const void* v_cache, cons
   p.group = group;
   p.d = head_dim;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  wait_settings(&p.wait_limit_ns, &p.wait_check_mask, &p.inject_wait);
   long long longest = max_seqlen_q > 0 && max_seqlen_q < total_tokens ? max_seqlen_q : total_tokens;
   return dtype == THD_BF16
              ? launch_paged_of<__nv_bfloat16>(p, longest * group, static_cast<char*>(workspace), sms,

@@ -76,6 +76,7 @@ template <typename DT>
 struct Pair16;
 template <>
 struct Pair16<__nv_bfloat16> {
+  static constexpr bool kBF16 = true;
   __device__ static __forceinline__ float2 get(uint32_t x) {
     return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
   }
@@ -86,6 +87,7 @@ struct Pair16<__nv_bfloat16> {
 };
 template <>
 struct Pair16<__half> {
+  static constexpr bool kBF16 = false;
   __device__ static __forceinline__ float2 get(uint32_t x) {
     return __half22float2(*reinterpret_cast<__half2*>(&x));
   }

@@ -44,6 +44,22 @@ void set_wait_fields(thd::AttnParams& p) {
   p.inject_wait = g_inject_wait.load(std::memory_order_relaxed);
 }
 
+}  // namespace
+
+namespace thd {
+// The settings for the kernels of other translation units.
+void wait_settings(uint64_t* limit_ns, uint32_t* check_mask, uint32_t* inject) {
+  AttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  set_wait_fields(p);
+  *limit_ns = p.wait_limit_ns;
+  *check_mask = p.wait_check_mask;
+  *inject = p.inject_wait;
+}
+}  // namespace thd
+
+namespace {
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
