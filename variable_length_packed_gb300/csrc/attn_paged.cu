@@ -354,9 +354,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
   }
 }
 
-// Joins the partials of the tiles that several CTAs share (block x: the tile that starts in CTA
-// x; block y its rows y, y + gridDim.y, ...), and writes the rows that have no units: rows of
-// no sequence and of sequences without keys.
+// Joins the partials of the tiles that several CTAs share (block x: the tile that starts in CTA x;
+// block y a part of its rows), and writes the rows that have no units: rows of no sequence and of
+// sequences without keys.  A tile of few partials takes a warp for a row, one of many (a long
+// sequence alone) a block.
+constexpr int kWarpJoin = 32;   // partials that one warp joins at most
+
 template <typename DT, int DP, int MT>
 __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const PagedArgs p) {
   constexpr int kJoinWarps = kJoinThreads / 32;
@@ -388,6 +391,55 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
   const int first = blockIdx.x * 2 + (sp.w >> 30);   // partial of the first CTA; the others' slot 0
   const int rows = (int)min((long long)MT, (long long)s.q_len * p.group - (long long)sp.z * MT);
   auto part_of = [&](int k) { return k == 0 ? first : ((int)blockIdx.x + k) * 2; };
+  auto place = [&](int r, int& t) {   // output row of the tile's row r: buffer row t, query head
+    const int row = sp.z * MT + r, tok = row / p.group;
+    t = s.q_start + tok;
+    return sp.y * p.group + (row - tok * p.group);
+  };
+  if (n <= kWarpJoin) {
+    for (int r = blockIdx.y * kJoinWarps + warp; r < rows; r += gridDim.y * kJoinWarps) {
+      const float* pm = p.part_m + (long long)part_of(lane < n ? lane : 0) * 3 * MT + r;
+      const float mine = lane < n ? pm[0] : -INFINITY;
+      float sr = pm[MT], se = pm[2 * MT];
+      float top = mine;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float use = top == -INFINITY ? 0.f : top;
+      const float w = lane < n ? ex2_approx(mine - use) : 0.f;
+      sr = lane < n ? w * sr : 0.f;
+      se = lane < n ? w * se : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        sr += __shfl_xor_sync(0xffffffffu, sr, o);
+        se += __shfl_xor_sync(0xffffffffu, se, o);
+      }
+      float acc[kCols];
+#pragma unroll
+      for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < n; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const float* src = p.part_o + ((long long)part_of(k) * MT + r) * DP + kCols * lane;
+#pragma unroll
+        for (int e = 0; e < kCols; e += 2) {
+          const float2 v = *reinterpret_cast<const float2*>(src + e);
+          acc[e] += wk * v.x;
+          acc[e + 1] += wk * v.y;
+        }
+      }
+      int t;
+      const int hq = place(r, t);
+      DT* dst = static_cast<DT*>(p.out) + ((long long)t * p.Hq + hq) * p.d + kCols * lane;
+#pragma unroll
+      for (int e = 0; e < kCols; e += 2) {
+        const float a = sr == 0.f ? 0.f : acc[e] / sr, b = sr == 0.f ? 0.f : acc[e + 1] / sr;
+        if (kCols * lane + e < p.d) *reinterpret_cast<uint32_t*>(dst + e) = Pair16<DT>::put(a, b);
+      }
+      if (lane == 0 && p.lse)
+        p.lse[(long long)hq * p.T + t] = se == 0.f ? -INFINITY : use * 0.69314718055994531f + logf(se);
+    }
+    return;
+  }
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {
     float top = -INFINITY;
     for (int k = tid; k < n; k += kJoinThreads) top = fmaxf(top, p.part_m[(long long)part_of(k) * 3 * MT + r]);
@@ -416,7 +468,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
     float acc[kCols];
 #pragma unroll
     for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int k = warp; k < n; k += kJoinWarps) {
       const float w = weight[k];
       const float* src = p.part_o + ((long long)part_of(k) * MT + r) * DP;
@@ -429,15 +481,16 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
     sr = se = 0.f;
 #pragma unroll
     for (int k = 0; k < kJoinWarps; ++k) sr += red[k][1], se += red[k][2];
-    const int row = sp.z * MT + r, tok = row / p.group, hq = sp.y * p.group + (row - tok * p.group);
+    int t;
+    const int hq = place(r, t);
     if (tid < p.d) {
       float v = 0.f;
 #pragma unroll
       for (int k = 0; k < kJoinWarps; ++k) v += acc_s[k][tid];
-      static_cast<DT*>(p.out)[((long long)(s.q_start + tok) * p.Hq + hq) * p.d + tid] = DT(sr == 0.f ? 0.f : v / sr);
+      static_cast<DT*>(p.out)[((long long)t * p.Hq + hq) * p.d + tid] = DT(sr == 0.f ? 0.f : v / sr);
     }
     if (tid == 0 && p.lse)
-      p.lse[(long long)hq * p.T + s.q_start + tok] = se == 0.f ? -INFINITY : use * 0.69314718055994531f + logf(se);
+      p.lse[(long long)hq * p.T + t] = se == 0.f ? -INFINITY : use * 0.69314718055994531f + logf(se);
     __syncthreads();
   }
 }
@@ -460,17 +513,16 @@ int launch_paged(PagedArgs& p, long long row_hint, char* ws, int sms, cudaStream
   p.part_o = reinterpret_cast<float*>(ws + kPartAt);
   p.part_m = p.part_o + (size_t)kMaxCtas * 2 * MT * DP;
   const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+  static SmemGrant grant;
   if constexpr (MT == kWideRows) {
     auto kern = attn_paged_wide_kernel<DT, DP>;
     constexpr int smem = (int)sizeof(WideSmem<DP>) + 1024;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-      return THD_ERR_CUDA;
+    if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
     kern<<<grid, kWideThreads, smem, st>>>(p);
   } else {
     auto kern = attn_paged_kernel<DT, DP, MT>;
     constexpr int smem = PagedSmem<DP, MT>::kBytes;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-      return THD_ERR_CUDA;
+    if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
     kern<<<grid, kWarps * 32, smem, st>>>(p);
   }
   if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;
@@ -544,10 +596,8 @@ int thd_attn_paged(const void* q, const void* k_cache, const void* v_cache, cons
   if (!on16(k_cache) || !on16(v_cache)) return THD_ERR_ARG;
   if (!workspace || !on16(workspace) || workspace_bytes < thd_attn_paged_workspace_size(head_dim))
     return THD_ERR_WORKSPACE;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-    return THD_ERR_CUDA;
+  const int sms = device_sms();
+  if (sms <= 0) return THD_ERR_CUDA;
   PagedArgs p{};
   p.q = q;
   p.kc = k_cache;

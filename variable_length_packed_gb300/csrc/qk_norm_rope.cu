@@ -785,18 +785,13 @@ void fill_common(RowArgs& p, int B, int T, int d, float eps, int weight_fp32, co
   p.weight_fp32 = weight_fp32;
 }
 
-template <typename Args>
-int launch_with_smem(void (*kern)(const Args), const Args& args, unsigned grid, int warps, size_t smem, cudaStream_t st) {
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return THD_ERR_CUDA;
-  kern<<<grid, warps * 32, smem, st>>>(args);
-  return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
-}
-
 template <typename DT, int LPH, bool kCache>
 int launch_rows_at(const RowArgs& p, unsigned grid, cudaStream_t st) {
-  return launch_with_smem<RowArgs>(head_rows_kernel<DT, LPH, kCache>, p, grid, kRowWarps,
-                                   kRowWarps * kRowStages * sizeof(RowStage<kRowPasses, 2, LPH>), st);
+  static SmemGrant grant;
+  constexpr size_t smem = kRowWarps * kRowStages * sizeof(RowStage<kRowPasses, 2, LPH>);
+  if (!grant.ask(head_rows_kernel<DT, LPH, kCache>, smem)) return THD_ERR_CUDA;
+  head_rows_kernel<DT, LPH, kCache><<<grid, kRowWarps * 32, smem, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
 }
 
 template <typename DT, bool kCache>
@@ -809,14 +804,6 @@ int launch_rows_of(const RowArgs& p, unsigned grid, cudaStream_t st) {
   }
 }
 
-int num_sms() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return sms;
-}
-
 template <bool kCache>
 int launch_rows(RowArgs& p, int dtype, cudaStream_t st) {
   const int per = kRowPasses * (32 / lanes_per_head(p.d));
@@ -827,7 +814,7 @@ int launch_rows(RowArgs& p, int dtype, cudaStream_t st) {
   const long long items = row_items * p.T;
   if (items >= (1ll << 31)) return THD_ERR_UNSUPPORTED;   // item numbers are 32-bit
   p.row_items = (int)row_items;
-  const int sms = num_sms();
+  const int sms = device_sms();
   if (sms <= 0) return THD_ERR_CUDA;
   // as many items for a warp as leave all that fit at once one, kRowRun at most
   const long long per_warp = items / ((long long)sms * kRowBlocksPerSm * kRowWarps);
@@ -839,8 +826,11 @@ int launch_rows(RowArgs& p, int dtype, cudaStream_t st) {
 
 template <typename DT, int LPH>
 int launch_bwd_at(const NormBwdArgs& b, unsigned grid, cudaStream_t st) {
-  return launch_with_smem<NormBwdArgs>(head_rows_bwd_kernel<DT, LPH>, b, grid, kBwdWarps,
-                                       kBwdWarps * kBwdStages * sizeof(RowStage<kBwdPasses, 4, LPH>), st);
+  static SmemGrant grant;
+  constexpr size_t smem = kBwdWarps * kBwdStages * sizeof(RowStage<kBwdPasses, 4, LPH>);
+  if (!grant.ask(head_rows_bwd_kernel<DT, LPH>, smem)) return THD_ERR_CUDA;
+  head_rows_bwd_kernel<DT, LPH><<<grid, kBwdWarps * 32, smem, st>>>(b);
+  return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
 }
 
 template <typename DT>
@@ -926,7 +916,7 @@ int thd_qk_norm_rope_bwd(const void* grad_q, const void* grad_k, const void* q, 
   }
   if (!workspace || !on16(workspace) || workspace_bytes < thd_qk_norm_rope_bwd_workspace_size(head_dim))
     return THD_ERR_WORKSPACE;
-  const int sms = num_sms();
+  const int sms = device_sms();
   if (sms <= 0) return THD_ERR_CUDA;
   const int per = kBwdPasses * (32 / lanes_per_head(head_dim));
   NormBwdArgs b{};

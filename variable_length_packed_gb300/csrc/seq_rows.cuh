@@ -4,11 +4,42 @@
 // Packed rows, cu_seqlens and slot starts as everywhere in this library: sequence b holds rows
 // [start_b, start_b + cu[b+1] - cu[b]), start_b = padded[b] or cu[b], starts ascending.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_runtime.h>
 
 namespace thd {
+
+// SM count of the current device, 0 on an error (looked up once per device).
+inline int device_sms() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < kDevices && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < kDevices) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
+
+// Lets a kernel take `smem` bytes of dynamic shared memory on the current device.  One instance per
+// kernel: what it has set is not set again (the call costs about a microsecond).
+struct SmemGrant {
+  std::atomic<uint64_t> granted{0};   // bit per device
+
+  template <typename Kernel>
+  bool ask(Kernel kern, size_t smem) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (granted.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
+    granted.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+  }
+};
 
 // Where row t lies, found by the whole warp (every lane passes the same t and gets the same
 // answer): its sequence and the rows [from, to) of it, or seq -1 and rows after t that are

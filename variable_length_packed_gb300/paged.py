@@ -7,12 +7,17 @@ the work is in the library's kernels (include/thd_attn.h states each operator).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
 
 from . import THD_BF16, THD_FP16, THD_OK, ThdError, _check_metadata, load_library
 
+# the current stream's handle without the Stream object around it (2 us a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_Places = ctypes.c_int64 * 6
 _CODES = {torch.bfloat16: THD_BF16, torch.float16: THD_FP16}
 
 
@@ -22,6 +27,11 @@ def thd_qk_norm_rope_bwd_workspace_size(head_dim):
 
 def thd_attn_paged_workspace_size(head_dim):
     return int(load_library().thd_attn_paged_workspace_size(int(head_dim)))
+
+
+@functools.lru_cache(maxsize=None)
+def _workspace_size(name, head_dim):
+    return int(getattr(load_library(), name)(head_dim))
 
 
 def _addr(t):
@@ -40,6 +50,9 @@ def _whole(t, name, device, dtype, shape=None):
     """A contiguous tensor of one dtype (and shape) on `device`; None passes."""
     if t is None:
         return
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.device == device and t.is_contiguous()
+            and device.type == "cuda" and (shape is None or t.shape == shape)):
+        return
     _on(t, name, device)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
@@ -51,13 +64,14 @@ def _whole(t, name, device, dtype, shape=None):
 
 def _rows(t, name, device, dtype, shape=None):
     """Row stride of a [T, heads, head_dim] tensor whose rows are whole but may lie apart."""
-    _on(t, name, device)
+    if type(t) is not torch.Tensor or t.device != device or device.type != "cuda":
+        _on(t, name, device)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, heads, head_dim]")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     T, h, d = t.shape
-    if shape is not None and (T, h, d) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     row, head, one = t.stride()
     if (d > 1 and one != 1) or (h > 1 and head != d):
@@ -78,20 +92,23 @@ def _dtype_code(t, name):
     return code
 
 
-def _meta(device, batch_size, cu, padded, per_seq=()):
-    """Batch size and checks of the int32 metadata; per_seq: (name, tensor) of >= batch_size entries."""
-    _whole(cu, "cu_seqlens", device, torch.int32)
+def _meta(device, batch_size, cu, padded, name, per_seq):
+    """Batch size and checks of the int32 metadata; per_seq: a tensor of >= batch_size entries, or None."""
     if cu is None:
         raise TypeError("cu_seqlens must be an int32 tensor")
-    _whole(padded, "cu_seqlens_padded", device, torch.int32)
+    _whole(cu, "cu_seqlens", device, torch.int32)
     if batch_size is None:
         batch_size = cu.numel() - 1
-    _check_metadata(batch_size, cu, None, padded)
-    for name, t in per_seq:
-        _whole(t, name, device, torch.int32)
-        if t is not None and t.numel() < batch_size:
-            raise ValueError(f"{name} holds {t.numel()} entries, batch_size {batch_size} needs as many")
-    return int(batch_size)
+    batch_size = int(batch_size)
+    if padded is not None:
+        _whole(padded, "cu_seqlens_padded", device, torch.int32)
+    if batch_size < 0 or cu.numel() <= batch_size or (padded is not None and padded.numel() < batch_size):
+        _check_metadata(batch_size, cu, None, padded)
+    if per_seq is not None:
+        _whole(per_seq, name, device, torch.int32)
+        if per_seq.numel() < batch_size:
+            raise ValueError(f"{name} holds {per_seq.numel()} entries, batch_size {batch_size} needs as many")
+    return batch_size
 
 
 def _tables(cos, sin, device, d):
@@ -112,13 +129,15 @@ def _tables(cos, sin, device, d):
 def _weights(wq, wk, device, d, dtype):
     """1 if the norm weights are fp32, 0 if they are of the rows' dtype."""
     fp32 = 0
+    if wq is None and wk is None:
+        return fp32
     for name, w in (("q_weight", wq), ("k_weight", wk)):
         if w is not None:
-            if not isinstance(w, torch.Tensor) or w.dtype not in (dtype, torch.float32):
+            if not isinstance(w, torch.Tensor) or (w.dtype is not dtype and w.dtype is not torch.float32):
                 raise TypeError(f"{name} must be a float32 or {dtype} tensor")
             _whole(w, name, device, w.dtype, (d,))
-            fp32 = int(w.dtype == torch.float32)
-    if wq is not None and wk is not None and wq.dtype != wk.dtype:
+            fp32 = int(w.dtype is torch.float32)
+    if wq is not None and wk is not None and wq.dtype is not wk.dtype:
         raise TypeError("q_weight and k_weight must share a dtype")
     return fp32
 
@@ -127,10 +146,10 @@ def _call(name, device, *args):
     """The library's entry point on the current stream of `device`."""
     fn = getattr(load_library(), name)
     if torch.cuda.current_device() == device.index:
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        st = fn(*args, _raw_stream(device.index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            st = fn(*args, _raw_stream(device.index))
     if st != THD_OK:
         raise ThdError(st, name)
 
@@ -159,7 +178,7 @@ def thd_qk_norm_rope(q, k, cu_seqlens, rope_cos=None, rope_sin=None, cu_seqlens_
             raise ValueError("k must be [T, Hkv, head_dim] with q's T and head_dim")
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out and k_weight need k")
-    B = _meta(dev, batch_size, cu_seqlens, cu_seqlens_padded, (("position_offsets", position_offsets),))
+    B = _meta(dev, batch_size, cu_seqlens, cu_seqlens_padded, "position_offsets", position_offsets)
     rows, rot = _tables(rope_cos, rope_sin, dev, d)
     fp32 = _weights(q_weight, k_weight, dev, d, dtype)
     if q_out is None:
@@ -204,7 +223,7 @@ def thd_qk_norm_rope_bwd(grad_q, grad_k, q, k, cu_seqlens, rope_cos=None, rope_s
         qs = _rows(q, "q", dev, dtype, grad_q.shape)
     if k_weight is not None:
         ks = _rows(k, "k", dev, dtype, grad_k.shape)
-    B = _meta(dev, batch_size, cu_seqlens, cu_seqlens_padded, (("position_offsets", position_offsets),))
+    B = _meta(dev, batch_size, cu_seqlens, cu_seqlens_padded, "position_offsets", position_offsets)
     rows, rot = _tables(rope_cos, rope_sin, dev, d)
     if dq is None:
         dq = torch.empty((T, hq, d), dtype=dtype, device=dev)
@@ -225,7 +244,8 @@ def thd_qk_norm_rope_bwd(grad_q, grad_k, q, k, cu_seqlens, rope_cos=None, rope_s
     size = 0
     if q_weight is not None or k_weight is not None:
         if workspace is None:
-            workspace = torch.empty(thd_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(_workspace_size("thd_qk_norm_rope_bwd_workspace_size", d), dtype=torch.uint8,
+                                    device=dev)
         else:
             _whole(workspace, "workspace", dev, torch.uint8)
         size = workspace.numel()
@@ -238,27 +258,29 @@ def thd_qk_norm_rope_bwd(grad_q, grad_k, q, k, cu_seqlens, rope_cos=None, rope_s
 
 def _caches(k_cache, v_cache, device, dtype, page_table, batch_size, writes):
     """Strides of the two caches (ctypes int64[6]: page, token, head of each), and the table's."""
-    shape, strides = None, []
+    shape = k_cache.shape if isinstance(k_cache, torch.Tensor) else None
+    places = []
     for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _on(c, name, device)
-        if c.dtype != dtype:
+        if type(c) is not torch.Tensor or c.device != device:
+            _on(c, name, device)
+        if c.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}")
-        if c.dim() != 4 or (shape is not None and c.shape != shape):
+        if c.dim() != 4 or c.shape != shape:
             raise ValueError("k_cache and v_cache must both be [pages, page_size, Hkv, head_dim]")
-        shape = c.shape
-        st = c.stride()
-        if shape[3] > 1 and st[3] != 1:
+        pages, size, heads, d = shape
+        page, token, head, one = c.stride()
+        if d > 1 and one != 1:
             raise ValueError(f"{name}: the values of a head must be contiguous")
-        apart = [(st[i], shape[i]) for i in range(3) if shape[i] > 1]
-        if writes:
-            need = shape[3]
-            for step, n in sorted(apart):
+        if writes and not c.is_contiguous():
+            need = d
+            for step, n in sorted((s, n) for s, n in ((page, pages), (token, size), (head, heads)) if n > 1):
                 if step < need:
                     raise ValueError(f"{name}: places overlap")
                 need = step * n
-        strides += [st[i] if shape[i] > 1 else 0 for i in range(3)]
-    _on(page_table, "page_table", device)
-    if page_table.dtype != torch.int32:
+        places += (page if pages > 1 else 0, token if size > 1 else 0, head if heads > 1 else 0)
+    if type(page_table) is not torch.Tensor or page_table.device != device:
+        _on(page_table, "page_table", device)
+    if page_table.dtype is not torch.int32:
         raise TypeError("page_table must be int32")
     if page_table.dim() != 2 or page_table.shape[0] < batch_size:
         raise ValueError("page_table must be [>= batch_size, pages]")
@@ -268,7 +290,7 @@ def _caches(k_cache, v_cache, device, dtype, page_table, batch_size, writes):
     step = page_table.stride(0) if page_table.shape[0] > 1 else wide
     if step < wide:
         raise ValueError("page_table: rows overlap")
-    return shape, (ctypes.c_int64 * 6)(*strides), wide, step
+    return shape, _Places(*places), wide, step
 
 
 def thd_kv_append(k, v, k_cache, v_cache, page_table, cache_lens, cu_seqlens, cu_seqlens_padded=None,
@@ -299,7 +321,7 @@ def thd_kv_append(k, v, k_cache, v_cache, page_table, cache_lens, cu_seqlens, cu
         raise ValueError("q_out and q_weight need q")
     if cache_lens is None:
         raise TypeError("cache_lens must be an int32 tensor")
-    B = _meta(dev, batch_size, cu_seqlens, cu_seqlens_padded, (("cache_lens", cache_lens),))
+    B = _meta(dev, batch_size, cu_seqlens, cu_seqlens_padded, "cache_lens", cache_lens)
     rows, rot = _tables(rope_cos, rope_sin, dev, d)
     fp32 = _weights(q_weight, k_weight, dev, d, dtype)
     if positions is not None:
@@ -341,7 +363,7 @@ def thd_attn_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q, cu_se
     T, hq, d = q.shape
     if kv_lens is None:
         raise TypeError("kv_lens must be an int32 tensor")
-    B = _meta(dev, batch_size, cu_seqlens_q, cu_seqlens_q_padded, (("kv_lens", kv_lens),))
+    B = _meta(dev, batch_size, cu_seqlens_q, cu_seqlens_q_padded, "kv_lens", kv_lens)
     shape, strides, wide, step = _caches(k_cache, v_cache, dev, dtype, page_table, B, False)
     if shape[3] != d:
         raise ValueError("the caches must have q's head_dim")
@@ -362,7 +384,7 @@ def thd_attn_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q, cu_se
     else:
         _whole(lse, "lse", dev, torch.float32, (hq, T))
     if workspace is None:
-        workspace = torch.empty(thd_attn_paged_workspace_size(d), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(_workspace_size("thd_attn_paged_workspace_size", d), dtype=torch.uint8, device=dev)
     else:
         _whole(workspace, "workspace", dev, torch.uint8)
     _call("thd_attn_paged", dev, _addr(q), _addr(k_cache), _addr(v_cache), strides, shape[0], shape[1],
