@@ -38,7 +38,7 @@ namespace {
 constexpr int kWarps = 4;            // warps of a CTA, 16 keys of the unit each
 constexpr int kWarpKeys = kUnit / kWarps;
 constexpr int kStages = 3;           // units in flight per warp
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   find_share<kWarps * 32>(p, MT, &share);
   if (tid == 0) {
-    p.splits[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    p.splits[blockIdx.x].n = 0;
     p.status[blockIdx.x] = 0u;
   }
 
@@ -338,9 +338,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
           p.lse[(long long)hq * p.T + x.s.q_start + tok] =
               se == 0.f ? -INFINITY : use * 0.69314718055994531f + logf(se);
       } else {
-        float4* dst = reinterpret_cast<float4*>(p.part_o + ((long long)part * MT + r) * DP + chunk * 8);
-        dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        float* dst = p.part_o + (long long)part * MT * DP + (2 * chunk * MT + r) * 4;
+        *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        *reinterpret_cast<float4*>(dst + MT * 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
         if (chunk == 0) {
           float* pm = p.part_m + (long long)part * 3 * MT;
           pm[r] = top;
@@ -354,22 +354,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
   }
 }
 
-// Joins the partials of the tiles that several CTAs share (block x: the tile that starts in CTA x;
-// block y a part of its rows), and writes the rows that have no units: rows of no sequence and of
-// sequences without keys.  A tile of few partials takes a warp for a row, one of many (a long
-// sequence alone) a block.
-constexpr int kWarpJoin = 32;   // partials that one warp joins at most
-
+// Joins the partials of the tiles that several CTAs share, and writes the rows that have no units: rows
+// of no sequence and of sequences without keys.  Block x works on the tile that goes on from CTA x to
+// the next, so a tile of n partials has n - 1 blocks.  They share its tasks of 32 rows (a lane each:
+// partials lie rows side by side) and 16 columns; a warp takes a task, or, of many partials (a
+// long sequence alone), a block does, its warps a part of the partials each.  The time is that of a
+// few dependent loads, so four partials are read at once and weighed against the maximum so far.
 template <typename DT, int DP, int MT>
 __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const PagedArgs p) {
   constexpr int kJoinWarps = kJoinThreads / 32;
-  constexpr int kCols = DP / 32;        // columns of a lane
-  __shared__ float weight[kMaxCtas];
-  __shared__ float red[kJoinWarps][3];
-  __shared__ float acc_s[kJoinWarps][DP];
+  constexpr int kColumnGroups = DP / 16;
+  __shared__ float shared[kJoinWarps][32][19];   // 19: rows in different banks
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int blocks = gridDim.x * gridDim.y, block = blockIdx.y * gridDim.x + blockIdx.x;
-  for (int t = block * kJoinWarps + warp; t < p.T; t += blocks * kJoinWarps) {
+  // from the last block on: the first ones have tiles to join
+  for (int t = ((int)gridDim.x - 1 - (int)blockIdx.x) * kJoinWarps + warp; t < p.T; t += gridDim.x * kJoinWarps) {
     const RowSpan at = find_span(p.cu, p.padded, p.B, t);
     if (at.seq >= 0 && p.kv_lens[at.seq] > 0 && p.max_pages > 0) continue;
     uint4* dst = reinterpret_cast<uint4*>(static_cast<DT*>(p.out) + (long long)t * p.Hq * p.d);
@@ -378,120 +376,105 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
       for (int h = lane; h < p.Hq; h += 32) p.lse[(long long)h * p.T + t] = -INFINITY;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (block == 0) {   // the call's status word, from the CTAs'
+  if (blockIdx.x == gridDim.x - 1) {   // the call's status word, from the CTAs'
     uint32_t bits = 0u;
     for (int i = tid; i < (int)gridDim.x; i += kJoinThreads) bits |= p.status[i];
     bits = __syncthreads_or(bits != 0u) ? THD_STATUS_WAIT_TIMEOUT : 0u;
     if (tid == 0) *p.call_status = bits;
   }
-  const int4 sp = p.splits[blockIdx.x];
-  if (sp.x < 0) return;
-  const SeqWork s = seq_work(p, sp.x, MT);
-  const int n = sp.w & 0x3fffffff;
-  const int first = blockIdx.x * 2 + (sp.w >> 30);   // partial of the first CTA; the others' slot 0
-  const int rows = (int)min((long long)MT, (long long)s.q_len * p.group - (long long)sp.z * MT);
-  auto part_of = [&](int k) { return k == 0 ? first : ((int)blockIdx.x + k) * 2; };
-  auto place = [&](int r, int& t) {   // output row of the tile's row r: buffer row t, query head
-    const int row = sp.z * MT + r, tok = row / p.group;
-    t = s.q_start + tok;
-    return sp.y * p.group + (row - tok * p.group);
-  };
-  if (n <= kWarpJoin) {
-    for (int r = blockIdx.y * kJoinWarps + warp; r < rows; r += gridDim.y * kJoinWarps) {
-      const float* pm = p.part_m + (long long)part_of(lane < n ? lane : 0) * 3 * MT + r;
-      const float mine = lane < n ? pm[0] : -INFINITY;
-      float sr = pm[MT], se = pm[2 * MT];
-      float top = mine;
+  const Split sp = p.splits[blockIdx.x];
+  if (sp.n == 0) return;
+  const int tasks = (sp.rows + 31) / 32 * kColumnGroups, mine = (int)blockIdx.x - sp.first, others = sp.n - 1;
+  // a warp takes a task alone where that means fewer rounds of reads one after another
+  const bool alone = (tasks + others * kJoinWarps - 1) / (others * kJoinWarps) * ((sp.n + 3) / 4) <=
+                     (tasks + others - 1) / others * ((sp.n + 4 * kJoinWarps - 1) / (4 * kJoinWarps));
+  const int k0 = alone ? 0 : warp, step = alone ? 1 : kJoinWarps;
+  for (int task = alone ? mine * kJoinWarps + warp : mine; task < tasks; task += alone ? others * kJoinWarps : others) {
+    const int cg = task % kColumnGroups, r = task / kColumnGroups * 32 + lane;
+    const bool have = r < sp.rows;
+    float top = -INFINITY, sr = 0.f, se = 0.f, acc[16];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float use = top == -INFINITY ? 0.f : top;
-      const float w = lane < n ? ex2_approx(mine - use) : 0.f;
-      sr = lane < n ? w * sr : 0.f;
-      se = lane < n ? w * se : 0.f;
+    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+    if (have) {
+      for (int k = k0; k < sp.n; k += 4 * step) {
+        float m[4], lr[4], le[4];
+        float4 v[4][4];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        sr += __shfl_xor_sync(0xffffffffu, sr, o);
-        se += __shfl_xor_sync(0xffffffffu, se, o);
-      }
-      float acc[kCols];
+        for (int i = 0; i < 4; ++i) {
+          const int kk = k + i * step;
+          m[i] = -INFINITY;
+          if (kk < sp.n) {
+            const long long part = (sp.first + kk) * 2 + (kk == 0 ? sp.second : 0);
+            const float* pm = p.part_m + part * 3 * MT + r;
+            const float* src = p.part_o + part * MT * DP + (cg * 4 * MT + r) * 4;
+            m[i] = pm[0];
+            lr[i] = pm[MT];
+            le[i] = pm[2 * MT];
 #pragma unroll
-      for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
-#pragma unroll 4
-      for (int k = 0; k < n; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const float* src = p.part_o + ((long long)part_of(k) * MT + r) * DP + kCols * lane;
+            for (int e = 0; e < 4; ++e) v[i][e] = *reinterpret_cast<const float4*>(src + e * MT * 4);
+          }
+        }
+        const float next = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), top);
+        const float use = next == -INFINITY ? 0.f : next;
+        const float old = ex2_approx(top - use);
+        top = next;
+        sr *= old, se *= old;
 #pragma unroll
-        for (int e = 0; e < kCols; e += 2) {
-          const float2 v = *reinterpret_cast<const float2*>(src + e);
-          acc[e] += wk * v.x;
-          acc[e + 1] += wk * v.y;
+        for (int e = 0; e < 16; ++e) acc[e] *= old;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (k + i * step < sp.n) {
+            const float w = ex2_approx(m[i] - use);
+            sr += w * lr[i];
+            se += w * le[i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              acc[4 * e] += w * v[i][e].x, acc[4 * e + 1] += w * v[i][e].y;
+              acc[4 * e + 2] += w * v[i][e].z, acc[4 * e + 3] += w * v[i][e].w;
+            }
+          }
         }
       }
-      int t;
-      const int hq = place(r, t);
-      DT* dst = static_cast<DT*>(p.out) + ((long long)t * p.Hq + hq) * p.d + kCols * lane;
+    }
+    if (!alone) {   // over the warps, in their order
+      float* own = shared[warp][lane];
+      own[0] = top, own[1] = sr, own[2] = se;
 #pragma unroll
-      for (int e = 0; e < kCols; e += 2) {
-        const float a = sr == 0.f ? 0.f : acc[e] / sr, b = sr == 0.f ? 0.f : acc[e + 1] / sr;
-        if (kCols * lane + e < p.d) *reinterpret_cast<uint32_t*>(dst + e) = Pair16<DT>::put(a, b);
+      for (int e = 0; e < 16; ++e) own[3 + e] = acc[e];
+      __syncthreads();
+      if (warp == 0 && have) {
+#pragma unroll
+        for (int k = 1; k < kJoinWarps; ++k) top = fmaxf(top, shared[k][lane][0]);
+        const float use = top == -INFINITY ? 0.f : top;
+        const float w0 = ex2_approx(own[0] - use);
+        sr *= w0, se *= w0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[e] *= w0;
+        for (int k = 1; k < kJoinWarps; ++k) {
+          const float* from = shared[k][lane];
+          const float w = ex2_approx(from[0] - use);
+          sr += w * from[1];
+          se += w * from[2];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[e] += w * from[3 + e];
+        }
       }
-      if (lane == 0 && p.lse)
-        p.lse[(long long)hq * p.T + t] = se == 0.f ? -INFINITY : use * 0.69314718055994531f + logf(se);
+      __syncthreads();
     }
-    return;
-  }
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    float top = -INFINITY;
-    for (int k = tid; k < n; k += kJoinThreads) top = fmaxf(top, p.part_m[(long long)part_of(k) * 3 * MT + r]);
+    if (have && (alone || warp == 0)) {
+      const int row = sp.row0 + r, tok = row / p.group, hq = sp.head * p.group + (row - tok * p.group);
+      const long long t = sp.q_start + tok;
+      DT* dst = static_cast<DT*>(p.out) + (t * p.Hq + hq) * p.d + cg * 16;
+      const float inv = 1.f / sr;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) red[warp][0] = top;
-    __syncthreads();
+      for (int e = 0; e < 16; ++e) acc[e] = sr == 0.f ? 0.f : acc[e] * inv;
 #pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, red[k][0]);
-    const float use = top == -INFINITY ? 0.f : top;
-    float sr = 0.f, se = 0.f;
-    for (int k = tid; k < n; k += kJoinThreads) {
-      const float* pm = p.part_m + (long long)part_of(k) * 3 * MT;
-      const float w = ex2_approx(pm[r] - use);
-      weight[k] = w;
-      sr += w * pm[MT + r];
-      se += w * pm[2 * MT + r];
+      for (int e = 0; e < 16; e += 8)
+        if (cg * 16 + e < p.d) *reinterpret_cast<uint4*>(dst + e) = pack8<DT>(acc + e);
+      if (cg == 0 && p.lse)
+        p.lse[(long long)hq * p.T + t] =
+            se == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) * 0.69314718055994531f + logf(se);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      sr += __shfl_xor_sync(0xffffffffu, sr, o);
-      se += __shfl_xor_sync(0xffffffffu, se, o);
-    }
-    if (lane == 0) red[warp][1] = sr, red[warp][2] = se;
-    __syncthreads();
-    float acc[kCols];
-#pragma unroll
-    for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
-#pragma unroll 8
-    for (int k = warp; k < n; k += kJoinWarps) {
-      const float w = weight[k];
-      const float* src = p.part_o + ((long long)part_of(k) * MT + r) * DP;
-#pragma unroll
-      for (int e = 0; e < kCols; ++e) acc[e] += w * src[lane + 32 * e];
-    }
-#pragma unroll
-    for (int e = 0; e < kCols; ++e) acc_s[warp][lane + 32 * e] = acc[e];
-    __syncthreads();
-    sr = se = 0.f;
-#pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) sr += red[k][1], se += red[k][2];
-    int t;
-    const int hq = place(r, t);
-    if (tid < p.d) {
-      float v = 0.f;
-#pragma unroll
-      for (int k = 0; k < kJoinWarps; ++k) v += acc_s[k][tid];
-      static_cast<DT*>(p.out)[((long long)t * p.Hq + hq) * p.d + tid] = DT(sr == 0.f ? 0.f : v / sr);
-    }
-    if (tid == 0 && p.lse)
-      p.lse[(long long)hq * p.T + t] = se == 0.f ? -INFINITY : use * 0.69314718055994531f + logf(se);
-    __syncthreads();
   }
 }
 
@@ -502,14 +485,14 @@ bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 // partial results (outputs, then maxima and sums).
 constexpr int kMaxRows = 128;   // rows of a tile at most
 constexpr size_t kStatusAt = 256, kSplitAt = kStatusAt + kMaxCtas * sizeof(uint32_t);
-constexpr size_t kPartAt = kSplitAt + kMaxCtas * sizeof(int4);
+constexpr size_t kPartAt = kSplitAt + kMaxCtas * sizeof(Split);
 constexpr size_t part_bytes(int dp) { return (size_t)kMaxCtas * 2 * kMaxRows * (dp + 3) * 4; }
 
 template <typename DT, int DP, int MT>
-int launch_paged(PagedArgs& p, long long row_hint, char* ws, int sms, cudaStream_t st) {
+int launch_paged(PagedArgs& p, char* ws, int sms, cudaStream_t st) {
   p.call_status = reinterpret_cast<uint32_t*>(ws + 8);
   p.status = reinterpret_cast<uint32_t*>(ws + kStatusAt);
-  p.splits = reinterpret_cast<int4*>(ws + kSplitAt);
+  p.splits = reinterpret_cast<Split*>(ws + kSplitAt);
   p.part_o = reinterpret_cast<float*>(ws + kPartAt);
   p.part_m = p.part_o + (size_t)kMaxCtas * 2 * MT * DP;
   const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
@@ -527,7 +510,7 @@ int launch_paged(PagedArgs& p, long long row_hint, char* ws, int sms, cudaStream
   }
   if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, (unsigned)(row_hint < 8 ? row_hint : 8));
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
@@ -543,13 +526,13 @@ int launch_paged(PagedArgs& p, long long row_hint, char* ws, int sms, cudaStream
 template <typename DT>
 int launch_paged_of(PagedArgs& p, long long row_hint, char* ws, int sms, cudaStream_t st) {
   if (p.d > 64) {
-    if (row_hint <= 16) return launch_paged<DT, 128, 16>(p, row_hint, ws, sms, st);
-    if (row_hint <= 32) return launch_paged<DT, 128, 32>(p, row_hint, ws, sms, st);
-    return launch_paged<DT, 128, kWideRows>(p, row_hint, ws, sms, st);
+    if (row_hint <= 16) return launch_paged<DT, 128, 16>(p, ws, sms, st);
+    if (row_hint <= 32) return launch_paged<DT, 128, 32>(p, ws, sms, st);
+    return launch_paged<DT, 128, kWideRows>(p, ws, sms, st);
   }
-  if (row_hint <= 16) return launch_paged<DT, 64, 16>(p, row_hint, ws, sms, st);
-  if (row_hint <= 32) return launch_paged<DT, 64, 32>(p, row_hint, ws, sms, st);
-  return launch_paged<DT, 64, kWideRows>(p, row_hint, ws, sms, st);
+  if (row_hint <= 16) return launch_paged<DT, 64, 16>(p, ws, sms, st);
+  if (row_hint <= 32) return launch_paged<DT, 64, 32>(p, ws, sms, st);
+  return launch_paged<DT, 64, kWideRows>(p, ws, sms, st);
 }
 
 }  // namespace

@@ -14,6 +14,15 @@ namespace {
 constexpr int kUnit = 64;            // keys of a unit
 constexpr int kMaxCtas = 320;        // CTAs of a launch at most (two on each of up to 160 SMs)
 
+// A tile that goes on from one CTA to the next: its rows, and the CTAs that share it.
+struct alignas(16) Split {
+  int n;        // CTAs (0: no such tile)
+  int first;    // the first of them
+  int second;   // whether the first one's partial is its second
+  int q_start, row0, rows, head;
+  int unused;
+};
+
 struct PagedArgs {
   const void* q;
   const void* kc;
@@ -25,13 +34,13 @@ struct PagedArgs {
   const long long* tree;
   void* out;
   float* lse;
-  float* part_o;       // [ctas * 2][rows][DP]
+  float* part_o;       // [ctas * 2][DP / 4][rows][4]
   float* part_m;       // [ctas * 2][3][rows]: maximum, sum of the rounded weights, sum of the weights
   uint32_t* call_status;
   uint32_t* status;    // [ctas]: THD_STATUS_* bits of each CTA
   uint64_t wait_limit_ns;
   uint32_t wait_check_mask, inject_wait;
-  int4* splits;        // [ctas]: (sequence, head, row tile, CTAs of the tile), of the tile that starts in the CTA and ends in another
+  Split* splits;       // [ctas]
   long long table_stride, k_page, k_token, k_head, v_page, v_token, v_head;   // elements
   int num_pages, page_size, max_pages;
   int tree_words;
@@ -199,12 +208,25 @@ __device__ __forceinline__ uint64_t seen_keys(const PagedArgs& p, const Piece& x
   return m;
 }
 
-// A tile that starts in this CTA and ends in another: noted for the join.
+// The CTA whose share unit u lies in.
+__device__ __forceinline__ int cta_of(const Share& s, long long u) {
+  return (int)(((u + 1) * s.ctas - 1) / s.total);
+}
+
+// A tile that goes on in the next CTA: noted for the join.
 __device__ __forceinline__ void note_split(const PagedArgs& p, const Piece& x, const Share& share) {
-  if (x.whole || x.blk0 != 0) return;
-  int c = blockIdx.x + 1;
-  while (share_begin(share.total, share.ctas, c + 1) < x.tile_end) ++c;
-  p.splits[blockIdx.x] = make_int4(x.seq, x.head, x.tile, (c - (int)blockIdx.x + 1) | (x.first ? 0 : 1 << 30));
+  if (x.tile_end <= share.end) return;
+  const long long tile_begin = x.tile_end - x.s.blocks;
+  Split sp;
+  sp.first = cta_of(share, tile_begin);
+  sp.n = cta_of(share, x.tile_end - 1) - sp.first + 1;
+  sp.second = share_begin(share.total, share.ctas, sp.first) == tile_begin ? 0 : 1;
+  sp.q_start = x.s.q_start;
+  sp.row0 = x.row0;
+  sp.rows = x.rows;
+  sp.head = x.head;
+  sp.unused = 0;
+  p.splits[blockIdx.x] = sp;
 }
 // Place of the piece's partial result.
 __device__ __forceinline__ int part_of_piece(const Piece& x) { return blockIdx.x * 2 + (x.first ? 0 : 1); }

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
     mbar_init(&sm.never, 1);
     fence_mbar_init();
     sm.abort = 0u;
-    p.splits[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    p.splits[blockIdx.x].n = 0;
     p.status[blockIdx.x] = 0u;
   }
   if (warp == 6) {
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
       const int part = part_of_piece(x);
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
       DT* dst = static_cast<DT*>(p.out) + ((long long)(x.s.q_start + (valid ? tok : 0)) * p.Hq + (valid ? hq : 0)) * p.d;
-      float* pdst = p.part_o + ((long long)part * kWideRows + r) * DP;
+      float* pdst = p.part_o + (long long)part * kWideRows * DP + r * 4;
 #pragma unroll
       for (int c = 0; c < DP / 32; ++c) {
         uint32_t o[32];
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
           } else {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(pdst + 32 * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              *reinterpret_cast<uint4*>(pdst + (8 * c + e / 4) * (kWideRows * 4)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         }
       }
