@@ -186,6 +186,20 @@ def test_one_long_sequence_sampled():
     assert torch.all((lse[:, 0].double() - s.logsumexp(-1)).abs() <= e + 1024 * 2.0 ** -24)
 
 
+@pytest.mark.parametrize("keys,new,hq,hkv,d,words", [
+    ([40000], [16], 32, 8, 64, 1),                        # over 30 units of one tile for each CTA
+    ([900 + 37 * i for i in range(40)], [10] * 40, 16, 4, 128, 0),   # several tiles for each CTA, two rows of blocks
+    ([70] * 300, [9] * 300, 16, 4, 64, 1),                # tiles of one or two units, many for each CTA
+    ([5000, 4000], [300, 5], 4, 1, 128, 0),               # ten tiles over the same keys
+])
+def test_many_units_for_each_cta(keys, new, hq, hkv, d, words):
+    x = make(keys, new, 16, hq, hkv, d, BF16, words=words)
+    work = torch.zeros(vlp.thd_attn_paged_workspace_size(d), dtype=torch.uint8, device="cuda")
+    got = run(x, max_seqlen_q=max(new), workspace=work)
+    assert int(work[8:12].view(torch.int32).item()) == 0
+    check(x, got)
+
+
 def test_rows_of_no_sequence_and_no_pages():
     x = make([5], [2], 4, 4, 2, 64, BF16, gap=6)
     out = torch.full_like(x["q"], 9.0)

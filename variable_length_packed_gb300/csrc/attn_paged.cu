@@ -20,6 +20,8 @@
 //    output tile in registers, and meets the other warps only when the tile is done.
 #include <cmath>
 #include <cstdint>
+#include <cstring>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -32,6 +34,8 @@ namespace thd {
 
 // the library's settings of waits inside kernels (thd_attn.cu)
 void wait_settings(uint64_t* limit_ns, uint32_t* check_mask, uint32_t* inject);
+bool encode_cache_map(CUtensorMap* map, const void* base, int d, int heads, int page_size, int pages, int box,
+                      const int64_t* strides, bool bf16);
 
 namespace {
 
@@ -488,6 +492,36 @@ constexpr size_t kStatusAt = 256, kSplitAt = kStatusAt + kMaxCtas * sizeof(uint3
 constexpr size_t kPartAt = kSplitAt + kMaxCtas * sizeof(Split);
 constexpr size_t part_bytes(int dp) { return (size_t)kMaxCtas * 2 * kMaxRows * (dp + 3) * 4; }
 
+// The wide kernel's boxes of tokens, or 0 where its rows go one by one: head_dim other than 64 or 128,
+// pages that are no multiple of 8 tokens (a box starts on a whole 8-row pattern of the layout), or
+// a cache that the tensor copies cannot describe.
+int cache_boxes(const PagedArgs& p, bool bf16, CUtensorMap* key_map, CUtensorMap* value_map) {
+  int box = kUnit;
+  while (box > 1 && p.page_size % box != 0) box /= 2;
+  if (box < 8 || p.num_pages < 1 || (p.d != 64 && p.d != 128)) return 0;
+  auto encode = [&](CUtensorMap* map, const void* base, long long page, long long token, long long head) {
+    // the stride of a dimension of one place means nothing
+    const int64_t strides[3] = {p.num_pages > 1 ? 2 * page : 2ll * p.d, p.page_size > 1 ? 2 * token : 2ll * p.d,
+                                p.Hkv > 1 ? 2 * head : 2ll * p.d};
+    return encode_cache_map(map, base, p.d, p.Hkv, p.page_size, p.num_pages, box, strides, bf16);
+  };
+  return encode(key_map, p.kc, p.k_page, p.k_token, p.k_head) && encode(value_map, p.vc, p.v_page, p.v_token, p.v_head)
+             ? box
+             : 0;
+}
+
+template <typename DT, int DP, bool kBoxes>
+int launch_wide(const PagedArgs& p, const CUtensorMap& key_map, const CUtensorMap& value_map, int box, int grid,
+                cudaStream_t st) {
+  static SmemGrant grant;
+  auto kern = attn_paged_wide_kernel<DT, DP, kBoxes>;
+  // over half of an SM's shared memory: two CTAs on one SM would wait for each other's tensor memory
+  constexpr size_t need = sizeof(WideSmem<DP>) + 1024, half = 120 * 1024, smem = need > half ? need : half;
+  if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
+  kern<<<grid, kWideThreads, smem, st>>>(p, key_map, value_map, box);
+  return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
+}
+
 template <typename DT, int DP, int MT>
 int launch_paged(PagedArgs& p, char* ws, int sms, cudaStream_t st) {
   p.call_status = reinterpret_cast<uint32_t*>(ws + 8);
@@ -495,20 +529,24 @@ int launch_paged(PagedArgs& p, char* ws, int sms, cudaStream_t st) {
   p.splits = reinterpret_cast<Split*>(ws + kSplitAt);
   p.part_o = reinterpret_cast<float*>(ws + kPartAt);
   p.part_m = p.part_o + (size_t)kMaxCtas * 2 * MT * DP;
-  const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
-  static SmemGrant grant;
+  const int most = MT == kWideRows ? sms : 2 * sms;   // CTAs that fit at once
+  const int grid = most < kMaxCtas ? most : kMaxCtas;
   if constexpr (MT == kWideRows) {
-    auto kern = attn_paged_wide_kernel<DT, DP>;
-    constexpr int smem = (int)sizeof(WideSmem<DP>) + 1024;
-    if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
-    kern<<<grid, kWideThreads, smem, st>>>(p);
+    CUtensorMap key_map, value_map;
+    std::memset(&key_map, 0, sizeof(key_map));
+    std::memset(&value_map, 0, sizeof(value_map));
+    const int box = cache_boxes(p, Pair16<DT>::kBF16, &key_map, &value_map);
+    const int got = box ? launch_wide<DT, DP, true>(p, key_map, value_map, box, grid, st)
+                        : launch_wide<DT, DP, false>(p, key_map, value_map, 0, grid, st);
+    if (got != THD_OK) return got;
   } else {
+    static SmemGrant grant;
     auto kern = attn_paged_kernel<DT, DP, MT>;
     constexpr int smem = PagedSmem<DP, MT>::kBytes;
     if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
     kern<<<grid, kWarps * 32, smem, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;
   }
-  if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kJoinThreads);

@@ -240,16 +240,32 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Element offset of a piece's key or value in its cache: 0 for one that is not read.
-__device__ __forceinline__ long long cache_offset(const PagedArgs& p, const Piece& x, const int32_t* table, int key,
-                                                  bool values) {
+// Box of a four-dimensional tensor (columns, heads, tokens, pages) into shared memory.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// Page of a piece's key, clamped to the cache (0 for a key that is not read), and the element offset of the
+// key or its value there.
+__device__ __forceinline__ int cache_page(const PagedArgs& p, const Piece& x, const int32_t* table, int key) {
+  return key < x.key_end ? table[key / p.page_size] : 0;
+}
+__device__ __forceinline__ long long place_in_cache(const PagedArgs& p, const Piece& x, int page, int key,
+                                                    bool values) {
   if (key >= x.key_end) return 0;
-  const int at = key / p.page_size;
-  int page = table[at];
   page = page < 0 ? 0 : (page >= p.num_pages ? p.num_pages - 1 : page);
-  const int in = key - at * p.page_size;
+  const int in = key % p.page_size;
   return values ? page * p.v_page + in * p.v_token + x.head * p.v_head
                 : page * p.k_page + in * p.k_token + x.head * p.k_head;
+}
+__device__ __forceinline__ long long cache_offset(const PagedArgs& p, const Piece& x, const int32_t* table, int key,
+                                                  bool values) {
+  return place_in_cache(p, x, cache_page(p, x, table, key), key, values);
 }
 
 }  // namespace

@@ -50,8 +50,8 @@ def _whole(t, name, device, dtype, shape=None):
     """A contiguous tensor of one dtype (and shape) on `device`; None passes."""
     if t is None:
         return
-    if (type(t) is torch.Tensor and t.dtype is dtype and t.device == device and t.is_contiguous()
-            and device.type == "cuda" and (shape is None or t.shape == shape)):
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == device.index and t.is_contiguous()
+            and (shape is None or t.shape == shape)):   # the usual case, without building devices to compare
         return
     _on(t, name, device)
     if t.dtype != dtype:
@@ -64,7 +64,7 @@ def _whole(t, name, device, dtype, shape=None):
 
 def _rows(t, name, device, dtype, shape=None):
     """Row stride of a [T, heads, head_dim] tensor whose rows are whole but may lie apart."""
-    if type(t) is not torch.Tensor or t.device != device or device.type != "cuda":
+    if type(t) is not torch.Tensor or t.get_device() != device.index:
         _on(t, name, device)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, heads, head_dim]")
@@ -182,16 +182,16 @@ def thd_qk_norm_rope(q, k, cu_seqlens, rope_cos=None, rope_sin=None, cu_seqlens_
     rows, rot = _tables(rope_cos, rope_sin, dev, d)
     fp32 = _weights(q_weight, k_weight, dev, d, dtype)
     if q_out is None:
-        q_out = torch.empty((T, hq, d), dtype=dtype, device=dev)
+        q_out = q.new_empty((T, hq, d))
     else:
         _whole(q_out, "q_out", dev, dtype, q.shape)
     if k is not None:
         if k_out is None:
-            k_out = torch.empty((T, hkv, d), dtype=dtype, device=dev)
+            k_out = q.new_empty((T, hkv, d))
         else:
             _whole(k_out, "k_out", dev, dtype, k.shape)
     _call("thd_qk_norm_rope", dev, _addr(q), qs, _addr(k), ks, _addr(q_weight), _addr(k_weight), fp32, float(eps),
-          _addr(rope_cos), _addr(rope_sin), rows, rot, int(bool(interleaved)), _addr(cu_seqlens),
+          _addr(rope_cos), _addr(rope_sin), rows, rot, int(bool(interleaved)), cu_seqlens.data_ptr(),
           _addr(cu_seqlens_padded), _addr(position_offsets), B, _addr(q_out), _addr(k_out), T, hq, hkv, d, code)
     return q_out, k_out
 
@@ -226,19 +226,19 @@ def thd_qk_norm_rope_bwd(grad_q, grad_k, q, k, cu_seqlens, rope_cos=None, rope_s
     B = _meta(dev, batch_size, cu_seqlens, cu_seqlens_padded, "position_offsets", position_offsets)
     rows, rot = _tables(rope_cos, rope_sin, dev, d)
     if dq is None:
-        dq = torch.empty((T, hq, d), dtype=dtype, device=dev)
+        dq = grad_q.new_empty((T, hq, d))
     dqs = _rows(dq, "dq", dev, dtype, grad_q.shape)
     dks = 0
     if grad_k is not None:
         if dk is None:
-            dk = torch.empty((T, hkv, d), dtype=dtype, device=dev)
+            dk = grad_q.new_empty((T, hkv, d))
         dks = _rows(dk, "dk", dev, dtype, grad_k.shape)
     grads = []
     for name, w, g in (("dq_weight", q_weight, dq_weight), ("dk_weight", k_weight, dk_weight)):
         if w is None and g is not None:
             raise ValueError(f"{name} needs its weight")
         if w is not None and g is None:
-            g = torch.empty(d, dtype=torch.float32, device=dev)
+            g = grad_q.new_empty(d, dtype=torch.float32)
         _whole(g, name, dev, torch.float32, (d,))
         grads.append(g)
     size = 0
@@ -249,9 +249,9 @@ def thd_qk_norm_rope_bwd(grad_q, grad_k, q, k, cu_seqlens, rope_cos=None, rope_s
         else:
             _whole(workspace, "workspace", dev, torch.uint8)
         size = workspace.numel()
-    _call("thd_qk_norm_rope_bwd", dev, _addr(grad_q), _addr(grad_k), _addr(q), qs, _addr(k), ks, _addr(q_weight),
+    _call("thd_qk_norm_rope_bwd", dev, grad_q.data_ptr(), _addr(grad_k), _addr(q), qs, _addr(k), ks, _addr(q_weight),
           _addr(k_weight), fp32, float(eps), _addr(rope_cos), _addr(rope_sin), rows, rot, int(bool(interleaved)),
-          _addr(cu_seqlens), _addr(cu_seqlens_padded), _addr(position_offsets), B, _addr(dq), dqs, _addr(dk), dks,
+          cu_seqlens.data_ptr(), _addr(cu_seqlens_padded), _addr(position_offsets), B, dq.data_ptr(), dqs, _addr(dk), dks,
           _addr(grads[0]), _addr(grads[1]), T, hq, hkv, d, code, _addr(workspace), size)
     return dq, dk, grads[0], grads[1]
 
@@ -261,7 +261,7 @@ def _caches(k_cache, v_cache, device, dtype, page_table, batch_size, writes):
     shape = k_cache.shape if isinstance(k_cache, torch.Tensor) else None
     places = []
     for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if type(c) is not torch.Tensor or c.device != device:
+        if type(c) is not torch.Tensor or c.get_device() != device.index:
             _on(c, name, device)
         if c.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}")
@@ -278,7 +278,7 @@ def _caches(k_cache, v_cache, device, dtype, page_table, batch_size, writes):
                     raise ValueError(f"{name}: places overlap")
                 need = step * n
         places += (page if pages > 1 else 0, token if size > 1 else 0, head if heads > 1 else 0)
-    if type(page_table) is not torch.Tensor or page_table.device != device:
+    if type(page_table) is not torch.Tensor or page_table.get_device() != device.index:
         _on(page_table, "page_table", device)
     if page_table.dtype is not torch.int32:
         raise TypeError("page_table must be int32")
@@ -333,13 +333,13 @@ def thd_kv_append(k, v, k_cache, v_cache, page_table, cache_lens, cu_seqlens, cu
         raise ValueError("a page must hold a token")
     if q is not None:
         if q_out is None:
-            q_out = torch.empty((T, hq, d), dtype=dtype, device=dev)
+            q_out = k.new_empty((T, hq, d))
         else:
             _whole(q_out, "q_out", dev, dtype, q.shape)
-    _call("thd_kv_append", dev, _addr(q), qs, _addr(k), ks, _addr(v), vs, _addr(q_weight), _addr(k_weight), fp32,
+    _call("thd_kv_append", dev, _addr(q), qs, _addr(k), ks, v.data_ptr(), vs, _addr(q_weight), _addr(k_weight), fp32,
           float(eps), _addr(rope_cos), _addr(rope_sin), rows, rot, int(bool(interleaved)), _addr(positions),
-          _addr(cu_seqlens), _addr(cu_seqlens_padded), _addr(cache_lens), B, _addr(q_out), _addr(k_cache),
-          _addr(v_cache), strides, shape[0], shape[1], _addr(page_table), step, wide, T, hq, hkv, d, code)
+          cu_seqlens.data_ptr(), _addr(cu_seqlens_padded), cache_lens.data_ptr(), B, _addr(q_out), k_cache.data_ptr(),
+          v_cache.data_ptr(), strides, shape[0], shape[1], page_table.data_ptr(), step, wide, T, hq, hkv, d, code)
     return q_out
 
 
@@ -376,19 +376,19 @@ def thd_attn_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q, cu_se
             raise ValueError("tree_mask must be [T, words]")
         words = tree_mask.shape[1]
     if out is None:
-        out = torch.empty((T, hq, d), dtype=dtype, device=dev)
+        out = q.new_empty((T, hq, d))
     else:
         _whole(out, "out", dev, dtype, q.shape)
     if lse is None and return_lse:
-        lse = torch.empty((hq, T), dtype=torch.float32, device=dev)
+        lse = q.new_empty((hq, T), dtype=torch.float32)
     else:
         _whole(lse, "lse", dev, torch.float32, (hq, T))
     if workspace is None:
         workspace = torch.empty(_workspace_size("thd_attn_paged_workspace_size", d), dtype=torch.uint8, device=dev)
     else:
         _whole(workspace, "workspace", dev, torch.uint8)
-    _call("thd_attn_paged", dev, _addr(q), _addr(k_cache), _addr(v_cache), strides, shape[0], shape[1],
-          _addr(page_table), step, wide, _addr(kv_lens), _addr(cu_seqlens_q), _addr(cu_seqlens_q_padded), B,
+    _call("thd_attn_paged", dev, _addr(q), k_cache.data_ptr(), v_cache.data_ptr(), strides, shape[0], shape[1],
+          page_table.data_ptr(), step, wide, kv_lens.data_ptr(), cu_seqlens_q.data_ptr(), _addr(cu_seqlens_q_padded), B,
           int(max_seqlen_q), _addr(tree_mask), words, 1.0 / math.sqrt(d) if softmax_scale is None else
-          float(softmax_scale), _addr(out), _addr(lse), T, hq, shape[2], d, code, _addr(workspace), workspace.numel())
+          float(softmax_scale), out.data_ptr(), _addr(lse), T, hq, shape[2], d, code, _addr(workspace), workspace.numel())
     return out, lse
