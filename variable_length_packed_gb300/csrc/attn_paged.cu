@@ -20,8 +20,6 @@
 //    output tile in registers, and meets the other warps only when the tile is done.
 #include <cmath>
 #include <cstdint>
-#include <cstring>
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -34,15 +32,14 @@ namespace thd {
 
 // the library's settings of waits inside kernels (thd_attn.cu)
 void wait_settings(uint64_t* limit_ns, uint32_t* check_mask, uint32_t* inject);
-bool encode_cache_map(CUtensorMap* map, const void* base, int d, int heads, int page_size, int pages, int box,
-                      const int64_t* strides, bool bf16);
 
 namespace {
 
 constexpr int kWarps = 4;            // warps of a CTA, 16 keys of the unit each
 constexpr int kWarpKeys = kUnit / kWarps;
 constexpr int kStages = 3;           // units in flight per warp
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 256;
+constexpr int kJoinAhead = 4;        // partials read at once
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -222,7 +219,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
         if (cut) {
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
-            const uint64_t all = token[f][hh] >= 0 ? seen_keys(p, x, token[f][hh], unit0) : 0ull;
+            const uint64_t all = token[f][hh] >= 0 ? seen_keys(p, x, token[f][hh], unit0, tree_word(p, x, token[f][hh])) : 0ull;
             const uint32_t seen = (uint32_t)(all >> (warp * kWarpKeys)) >> qc;   // this lane's: bits 0, 1, 8, 9
             if (!(seen & 1)) c[f][0][2 * hh] = -INFINITY;
             if (!(seen & 2)) c[f][0][2 * hh + 1] = -INFINITY;
@@ -363,7 +360,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
 // the next, so a tile of n partials has n - 1 blocks.  They share its tasks of 32 rows (a lane each:
 // partials lie rows side by side) and 16 columns; a warp takes a task, or, of many partials (a
 // long sequence alone), a block does, its warps a part of the partials each.  The time is that of a
-// few dependent loads, so four partials are read at once and weighed against the maximum so far.
+// few dependent loads, so kJoinAhead partials are read at once and weighed against the maximum so far.
 template <typename DT, int DP, int MT>
 __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const PagedArgs p) {
   constexpr int kJoinWarps = kJoinThreads / 32;
@@ -390,8 +387,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
   if (sp.n == 0) return;
   const int tasks = (sp.rows + 31) / 32 * kColumnGroups, mine = (int)blockIdx.x - sp.first, others = sp.n - 1;
   // a warp takes a task alone where that means fewer rounds of reads one after another
-  const bool alone = (tasks + others * kJoinWarps - 1) / (others * kJoinWarps) * ((sp.n + 3) / 4) <=
-                     (tasks + others - 1) / others * ((sp.n + 4 * kJoinWarps - 1) / (4 * kJoinWarps));
+  const bool alone = (tasks + others * kJoinWarps - 1) / (others * kJoinWarps) * ((sp.n + kJoinAhead - 1) / kJoinAhead) <=
+                     (tasks + others - 1) / others * ((sp.n + kJoinAhead * kJoinWarps - 1) / (kJoinAhead * kJoinWarps));
   const int k0 = alone ? 0 : warp, step = alone ? 1 : kJoinWarps;
   for (int task = alone ? mine * kJoinWarps + warp : mine; task < tasks; task += alone ? others * kJoinWarps : others) {
     const int cg = task % kColumnGroups, r = task / kColumnGroups * 32 + lane;
@@ -400,11 +397,11 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.f;
     if (have) {
-      for (int k = k0; k < sp.n; k += 4 * step) {
-        float m[4], lr[4], le[4];
-        float4 v[4][4];
+      for (int k = k0; k < sp.n; k += kJoinAhead * step) {
+        float m[kJoinAhead], lr[kJoinAhead], le[kJoinAhead];
+        float4 v[kJoinAhead][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kJoinAhead; ++i) {
           const int kk = k + i * step;
           m[i] = -INFINITY;
           if (kk < sp.n) {
@@ -418,7 +415,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
             for (int e = 0; e < 4; ++e) v[i][e] = *reinterpret_cast<const float4*>(src + e * MT * 4);
           }
         }
-        const float next = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), top);
+        float next = top;
+#pragma unroll
+        for (int i = 0; i < kJoinAhead; ++i) next = fmaxf(next, m[i]);
         const float use = next == -INFINITY ? 0.f : next;
         const float old = ex2_approx(top - use);
         top = next;
@@ -426,7 +425,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[e] *= old;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kJoinAhead; ++i) {
           if (k + i * step < sp.n) {
             const float w = ex2_approx(m[i] - use);
             sr += w * lr[i];
@@ -492,36 +491,6 @@ constexpr size_t kStatusAt = 256, kSplitAt = kStatusAt + kMaxCtas * sizeof(uint3
 constexpr size_t kPartAt = kSplitAt + kMaxCtas * sizeof(Split);
 constexpr size_t part_bytes(int dp) { return (size_t)kMaxCtas * 2 * kMaxRows * (dp + 3) * 4; }
 
-// The wide kernel's boxes of tokens, or 0 where its rows go one by one: head_dim other than 64 or 128,
-// pages that are no multiple of 8 tokens (a box starts on a whole 8-row pattern of the layout), or
-// a cache that the tensor copies cannot describe.
-int cache_boxes(const PagedArgs& p, bool bf16, CUtensorMap* key_map, CUtensorMap* value_map) {
-  int box = kUnit;
-  while (box > 1 && p.page_size % box != 0) box /= 2;
-  if (box < 8 || p.num_pages < 1 || (p.d != 64 && p.d != 128)) return 0;
-  auto encode = [&](CUtensorMap* map, const void* base, long long page, long long token, long long head) {
-    // the stride of a dimension of one place means nothing
-    const int64_t strides[3] = {p.num_pages > 1 ? 2 * page : 2ll * p.d, p.page_size > 1 ? 2 * token : 2ll * p.d,
-                                p.Hkv > 1 ? 2 * head : 2ll * p.d};
-    return encode_cache_map(map, base, p.d, p.Hkv, p.page_size, p.num_pages, box, strides, bf16);
-  };
-  return encode(key_map, p.kc, p.k_page, p.k_token, p.k_head) && encode(value_map, p.vc, p.v_page, p.v_token, p.v_head)
-             ? box
-             : 0;
-}
-
-template <typename DT, int DP, bool kBoxes>
-int launch_wide(const PagedArgs& p, const CUtensorMap& key_map, const CUtensorMap& value_map, int box, int grid,
-                cudaStream_t st) {
-  static SmemGrant grant;
-  auto kern = attn_paged_wide_kernel<DT, DP, kBoxes>;
-  // over half of an SM's shared memory: two CTAs on one SM would wait for each other's tensor memory
-  constexpr size_t need = sizeof(WideSmem<DP>) + 1024, half = 120 * 1024, smem = need > half ? need : half;
-  if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
-  kern<<<grid, kWideThreads, smem, st>>>(p, key_map, value_map, box);
-  return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
-}
-
 template <typename DT, int DP, int MT>
 int launch_paged(PagedArgs& p, char* ws, int sms, cudaStream_t st) {
   p.call_status = reinterpret_cast<uint32_t*>(ws + 8);
@@ -529,24 +498,20 @@ int launch_paged(PagedArgs& p, char* ws, int sms, cudaStream_t st) {
   p.splits = reinterpret_cast<Split*>(ws + kSplitAt);
   p.part_o = reinterpret_cast<float*>(ws + kPartAt);
   p.part_m = p.part_o + (size_t)kMaxCtas * 2 * MT * DP;
-  const int most = MT == kWideRows ? sms : 2 * sms;   // CTAs that fit at once
-  const int grid = most < kMaxCtas ? most : kMaxCtas;
+  const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+  static SmemGrant grant;
   if constexpr (MT == kWideRows) {
-    CUtensorMap key_map, value_map;
-    std::memset(&key_map, 0, sizeof(key_map));
-    std::memset(&value_map, 0, sizeof(value_map));
-    const int box = cache_boxes(p, Pair16<DT>::kBF16, &key_map, &value_map);
-    const int got = box ? launch_wide<DT, DP, true>(p, key_map, value_map, box, grid, st)
-                        : launch_wide<DT, DP, false>(p, key_map, value_map, 0, grid, st);
-    if (got != THD_OK) return got;
+    auto kern = attn_paged_wide_kernel<DT, DP>;
+    constexpr int smem = (int)sizeof(WideSmem<DP>) + 1024;
+    if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
+    kern<<<grid, kWideThreads, smem, st>>>(p);
   } else {
-    static SmemGrant grant;
     auto kern = attn_paged_kernel<DT, DP, MT>;
     constexpr int smem = PagedSmem<DP, MT>::kBytes;
     if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
     kern<<<grid, kWarps * 32, smem, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;
   }
+  if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kJoinThreads);

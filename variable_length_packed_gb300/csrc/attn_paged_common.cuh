@@ -135,6 +135,11 @@ __device__ void find_share(const PagedArgs& p, int rows_per_tile, Share* out) {
   __syncthreads();
 }
 
+// a / b for a >= 0, b > 0: in 32 bits where both fit, several times faster than in 64.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // One piece of a CTA's share: keys of units [blk0, blk0 + steps) of one row tile of one key/value head.
 struct Piece {
   SeqWork s;
@@ -164,11 +169,11 @@ struct PieceWalk {
         ++b;
         continue;
       }
-      const long long item = (u - base) / x.s.blocks;
+      const long long item = quotient(u - base, x.s.blocks);
       x.seq = b;
       x.blk0 = (int)(u - base - item * x.s.blocks);
       const int nblk = (int)min((long long)(x.s.blocks - x.blk0), end - u);
-      x.head = (int)(item / x.s.tiles);
+      x.head = (int)quotient(item, x.s.tiles);
       x.tile = (int)(item - (long long)x.head * x.s.tiles);
       x.whole = nblk == x.s.blocks;
       x.first = u == begin;
@@ -185,21 +190,26 @@ struct PieceWalk {
   }
 };
 
-// Which of the 64 keys [first, first + 64) token `tok` of the piece's sequence sees.
-__device__ __forceinline__ uint64_t seen_keys(const PagedArgs& p, const Piece& x, int tok, int first) {
+// The first word of a token's tree mask: read when the piece begins, needed at its last keys.
+__device__ __forceinline__ uint64_t tree_word(const PagedArgs& p, const Piece& x, int tok) {
+  return p.tree ? (uint64_t)p.tree[(long long)(x.s.q_start + tok) * p.tree_words] : 0ull;
+}
+
+// Which of the 64 keys [first, first + 64) token `tok` of the piece's sequence sees; word0: its tree_word.
+__device__ __forceinline__ uint64_t seen_keys(const PagedArgs& p, const Piece& x, int tok, int first, uint64_t word0) {
   const int last = (p.tree ? x.s.kv_len : min(x.past + tok + 1, x.s.kv_len)) - first;   // keys before the end
   uint64_t m = last >= 64 ? ~0ull : (last <= 0 ? 0ull : (1ull << last) - 1);
   if (p.tree) {
     const int j0 = first - x.past;   // index of the first key among the new tokens
     if (j0 > -64) {
-      const long long* w = p.tree + (long long)(x.s.q_start + tok) * p.tree_words;
       uint64_t t;
       if (j0 <= 0) {
-        t = (uint64_t)w[0] << -j0;
+        t = word0 << -j0;
         if (j0 < 0) t |= (1ull << -j0) - 1;   // cached keys
       } else {
+        const long long* w = p.tree + (long long)(x.s.q_start + tok) * p.tree_words;
         const int at = j0 >> 6, sh = j0 & 63;
-        t = at < p.tree_words ? (uint64_t)w[at] >> sh : 0ull;
+        t = at == 0 ? word0 >> sh : (at < p.tree_words ? (uint64_t)w[at] >> sh : 0ull);
         if (sh && at + 1 < p.tree_words) t |= (uint64_t)w[at + 1] << (64 - sh);
       }
       m &= t;
@@ -210,7 +220,7 @@ __device__ __forceinline__ uint64_t seen_keys(const PagedArgs& p, const Piece& x
 
 // The CTA whose share unit u lies in.
 __device__ __forceinline__ int cta_of(const Share& s, long long u) {
-  return (int)(((u + 1) * s.ctas - 1) / s.total);
+  return (int)quotient((u + 1) * s.ctas - 1, s.total);
 }
 
 // A tile that goes on in the next CTA: noted for the join.
@@ -240,32 +250,16 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Box of a four-dimensional tensor (columns, heads, tokens, pages) into shared memory.
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
-                                            int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
-
-// Page of a piece's key, clamped to the cache (0 for a key that is not read), and the element offset of the
-// key or its value there.
-__device__ __forceinline__ int cache_page(const PagedArgs& p, const Piece& x, const int32_t* table, int key) {
-  return key < x.key_end ? table[key / p.page_size] : 0;
-}
-__device__ __forceinline__ long long place_in_cache(const PagedArgs& p, const Piece& x, int page, int key,
-                                                    bool values) {
-  if (key >= x.key_end) return 0;
-  page = page < 0 ? 0 : (page >= p.num_pages ? p.num_pages - 1 : page);
-  const int in = key % p.page_size;
-  return values ? page * p.v_page + in * p.v_token + x.head * p.v_head
-                : page * p.k_page + in * p.k_token + x.head * p.k_head;
-}
+// Element offset of a piece's key or value in its cache: 0 for one that is not read.
 __device__ __forceinline__ long long cache_offset(const PagedArgs& p, const Piece& x, const int32_t* table, int key,
                                                   bool values) {
-  return place_in_cache(p, x, cache_page(p, x, table, key), key, values);
+  if (key >= x.key_end) return 0;
+  const int at = key / p.page_size;
+  int page = table[at];
+  page = page < 0 ? 0 : (page >= p.num_pages ? p.num_pages - 1 : page);
+  const int in = key - at * p.page_size;
+  return values ? page * p.v_page + in * p.v_token + x.head * p.v_head
+                : page * p.k_page + in * p.k_token + x.head * p.k_head;
 }
 
 }  // namespace

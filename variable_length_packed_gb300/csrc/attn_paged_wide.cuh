@@ -2,21 +2,24 @@
 // fifth-generation tensor cores: chunks of new tokens and trees of drafted ones, where more
 // than 32 rows share a key/value head.
 //
-// The same split of the batch's keys over the CTAs as the narrow kernel's (attn_paged.cu), one CTA
-// per SM; inside a CTA the work is divided among warps:
-//   warps 0-3, 4-7  softmax of the even and the odd units of a piece, one thread per row: scores out of
-//                   tensor memory, weights back over them, a running maximum and sums; at the
-//                   piece's end the two streams' outputs are added, half of the columns each
-//   warps 8, 9      keys and values, out of the pages into the swizzled layout of the matrix unit:
-//                   tensor copies of whole boxes of a page, or rows in pieces of 16 bytes
-//   warp 10         issues the matrix products: S = Q K^T, O += P V
-// What bounds it: with up to 128 rows for each key a unit's 32 KB take about 1400 cycles to come
-// from memory on an SM, its two products 512 cycles of the tensor pipe, and the softmax of one
-// unit 1000 to 1500.  So two softmax streams, each with two score tiles and an output tile of its
-// own (all of tensor memory): up to four units' scores are computed ahead, and neither product waits
-// for the other stream.  Two CTAs per SM with one stream and one score tile each ran scores,
-// softmax and output of a unit one after another: 92 us where this takes @WIDE@ (trees of 27
-// tokens, 108 rows, over 120000 keys of 8 heads; 74 us at the copy bandwidth).
+// The same split of the batch's keys over the CTAs as the narrow kernel's (attn_paged.cu); inside a CTA
+// the work is divided among warps:
+//   warps 0-3  softmax, one thread per row: queries into tensor memory, scores out of it, weights
+//              back over them, the running maximum and sums, the output at the end
+//   warps 4-5  loads: 32 keys of each unit, 16-byte asynchronous copies out of the pages into
+//              the swizzled layout of the matrix unit (any page size, order and stride)
+//   warp 6     issues the matrix products: S = Q K^T (Q from tensor memory), O += P V
+// What bounds it: with up to 128 rows for each key the unit's 32 KB take about 1400 cycles to
+// come from memory on an SM, its two products 512 cycles of the tensor pipe and its softmax 1000 to
+// 1500.  A CTA runs S, softmax, P V of a unit one after another; two CTAs per SM (half of the
+// tensor memory and shared memory each) overlap one another's.  Queries in tensor memory leave
+// shared memory for three units of keys and values.
+// Measured (16 sequences, 27 drafted tokens of 32 + 8 heads of 128): each further 120000 keys take 73 us,
+// 6.7 TB/s; 120000 keys 94 us, the rest being the start (17 us for 2000 keys: finding the share,
+// first use of code, tables and pages one after another).  Measured and left: one CTA per SM with two
+// softmax streams, two score tiles for each and the queries in shared memory took 107 us with
+// keys and values by tensor copies of whole boxes of a page (16 tokens by 64 columns), 153 us with two
+// warps copying rows; with the keys in the cache it was slower too (78 against 60 us at 54 drafted tokens).
 //
 // Every wait is bounded as in the other attention kernels: one that runs out sets the CTA's
 // status word, and the CTA lets what it started finish and leaves.
@@ -27,26 +30,17 @@ namespace thd {
 namespace {
 
 constexpr int kWideRows = 128;
-constexpr int kWideThreads = 384;
-constexpr int kWideKStages = 5, kWideVStages = 6;   // units of keys, of values on the way
-constexpr int kWideLag = 3;               // rows: units whose copies may still be flying when one is announced
-constexpr uint32_t kWideTmemCols = 512;   // S (and P) of stream t, buffer s: 64 at 128 t + 64 s; O of stream t at 256 + 128 t
+constexpr int kWideThreads = 224;   // seven warps: two CTAs leave a thread 128 registers
+constexpr int kWideLoaders = 2;     // loading warps
+constexpr int kWideStages = 3;
+constexpr uint32_t kWideTmemCols = 256;   // S and P [0, 64), Q [64, 128), O [128, 128 + DP)
 
 template <int DP>
 struct WideSmem {
   static constexpr int kTileBytes = kUnit * DP * 2;   // panels of 64 rows x 128 bytes
-  alignas(1024) uint8_t q[kWideRows * DP * 2];        // panels of 128 rows x 128 bytes
-  alignas(1024) uint8_t k[kWideKStages][kTileBytes];
-  alignas(1024) uint8_t v[kWideVStages][kTileBytes];
-  // each stream's maximum, sum of the rounded weights, sum of the weights; by turns of pieces, since a
-  // stream without units in a piece comes to its statistics while the others still read the last ones
-  float stats[2][2][3][kWideRows];
-  uint64_t places[2][kUnit];      // addresses of a unit's keys, values
-  uint64_t k_full[kWideKStages], k_empty[kWideKStages], v_full[kWideVStages], v_empty[kWideVStages];
-  // by stream and by turns of its units: a wait names a phase by its parity, so it must come at most one
-  // phase late, and the scores of a unit say that the products of the unit two before it are done
-  uint64_t s_full[2][2], p_full[2][2], o_full[2][2];
-  uint64_t q_full, stats_full, o_free, drain, never;
+  alignas(1024) uint8_t k[kWideStages][kTileBytes];
+  alignas(1024) uint8_t v[kWideStages][kTileBytes];
+  uint64_t full[kWideStages], empty[kWideStages], q_full, s_full, p_full, o_full, drain, never;
   uint32_t tmem_base, abort;
   Share share;
 };
@@ -56,133 +50,10 @@ struct WideSmem {
   (__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &p.status[blockIdx.x], THD_STATUS_WAIT_TIMEOUT,      \
                                      p.wait_limit_ns, p.wait_check_mask) ? 1 : 0) != 0)
 
-// Copies the 64 rows of a unit out of the pages, by one warp in pieces of 16 bytes: each lane finds
-// two rows (their pages given), and the addresses go round through shared memory, so that 512 bytes
-// cost a load of an address, an add and the copy.  Rows that no query sees become zeros.
 template <typename DT, int DP>
-__device__ __forceinline__ void copy_rows(const PagedArgs& p, const Piece& x, const int (&page)[2], int first,
-                                          bool values, const DT** places, uint8_t* tile) {
-  constexpr int kChunks = DP / 8, kLaneKeys = 32 / kChunks, kCopies = kUnit / kLaneKeys;
-  const int lane = threadIdx.x & 31;
-  const int copy_key = lane / kChunks, copy_chunk = lane % kChunks;
-  const bool copy_in = copy_chunk * 8 < p.d;
-  const int col = copy_in ? copy_chunk * 8 : 0;
-  const DT* cache = static_cast<const DT*>(values ? p.vc : p.kc);
-  __syncwarp();   // the last addresses have been read
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    places[32 * k + lane] = cache + place_in_cache(p, x, page[k], first + 32 * k + lane, values);
-  __syncwarp();
-  const uint32_t at = smem_u32(tile) + (copy_chunk >> 3) * (kUnit * 128) + copy_key * 128;
-  const int keys = copy_in ? x.key_end - first : 0;   // of the unit, that some row sees
-#pragma unroll
-  for (int c0 = 0; c0 < kCopies; c0 += 8) {   // eight addresses at a time, so that reading them overlaps
-    const DT* from[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) from[c] = places[(c0 + c) * kLaneKeys + copy_key] + col;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const int key = (c0 + c) * kLaneKeys + copy_key;
-      const uint32_t swizzled = ((copy_chunk & 7) ^ (key & 7)) << 4;   // one of 8 / kLaneKeys values
-      cp_async16(at + (c0 + c) * (kLaneKeys * 128) + swizzled, from[c], key < keys);
-    }
-  }
-}
-
-// Streams all of the CTA's units of keys (or values) through a ring of shared memory; one warp.  With any
-// pages and head_dim: copies of 16 bytes, a unit announced kWideLag units later, when its own have landed.
-template <typename DT, int DP, int kRing>
-__device__ void wide_load_rows(const PagedArgs& p, PieceWalk walk, bool values,
-                               uint8_t (*ring)[WideSmem<DP>::kTileBytes], uint64_t* places, uint64_t* full,
-                               uint64_t* empty, volatile uint32_t* abort_flag) {
-  const int lane = threadIdx.x & 31;
-  uint32_t n = 0;   // units issued
-  auto announce = [&](uint32_t i) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&full[i % kRing]);
-  };
-  Piece x;
-  while (walk.next<kWideRows>(p, x)) {
-    const int32_t* table = p.table + (long long)x.seq * p.table_stride;
-    int page[2];   // of the lane's two rows of the unit issued next
-#pragma unroll
-    for (int k = 0; k < 2; ++k) page[k] = cache_page(p, x, table, x.blk0 * kUnit + 32 * k + lane);
-    for (int i = 0; i < x.steps; ++i, ++n) {
-      const int first = (x.blk0 + i) * kUnit;
-      if (n >= kRing && !WIDE_WAIT(&empty[n % kRing], (n / kRing - 1) & 1)) {
-        cp_async_wait<0>();
-        return;
-      }
-      copy_rows<DT, DP>(p, x, page, first, values, reinterpret_cast<const DT**>(places), ring[n % kRing]);
-      cp_async_commit();
-      if (i + 1 < x.steps) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) page[k] = cache_page(p, x, table, first + kUnit + 32 * k + lane);
-      }
-      if (n >= kWideLag) {
-        cp_async_wait<kWideLag>();
-        announce(n - kWideLag);
-      }
-    }
-  }
-  cp_async_wait<0>();
-  for (uint32_t i = n < kWideLag ? 0 : n - kWideLag; i < n; ++i) announce(i);
-}
-
-// The same by tensor copies, where a page is a multiple of 8 tokens and head_dim 64 or 128: boxes of `box`
-// tokens (the largest power of two that divides the page and the unit) by 64 columns, a lane each.
-// A box past the last visible key is left out; the unit of values that such a key ends in goes row by
-// row instead, so that what lies behind it becomes zeros (the scores there are masked, whatever they are).
-template <typename DT, int DP, int kRing>
-__device__ void wide_load_boxes(const PagedArgs& p, const CUtensorMap* map, int box, PieceWalk walk, bool values,
-                                uint8_t (*ring)[WideSmem<DP>::kTileBytes], uint64_t* places, uint64_t* full,
-                                uint64_t* empty, volatile uint32_t* abort_flag) {
-  constexpr int kPanels = DP / 64;
-  const int lane = threadIdx.x & 31;
-  const int panel = lane % kPanels, row = lane / kPanels * box;   // of this lane's box
-  uint32_t n = 0;
-  bool ok = true;
-  Piece x;
-  while (ok && walk.next<kWideRows>(p, x)) {
-    const int32_t* table = p.table + (long long)x.seq * p.table_stride;
-    int page = row < kUnit ? cache_page(p, x, table, x.blk0 * kUnit + row) : 0;
-    for (int i = 0; i < x.steps; ++i, ++n) {
-      const int first = (x.blk0 + i) * kUnit, keys = min(kUnit, x.key_end - first);
-      const uint32_t st = n % kRing;
-      if (n >= kRing && !WIDE_WAIT(&empty[st], (n / kRing - 1) & 1)) {
-        ok = false;
-        break;
-      }
-      if (values && keys < kUnit) {
-        int pages[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) pages[k] = cache_page(p, x, table, first + 32 * k + lane);
-        copy_rows<DT, DP>(p, x, pages, first, true, reinterpret_cast<const DT**>(places), ring[st]);
-        cp_async_commit();
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[st]);
-      } else {
-        const int at = max(0, min(page, p.num_pages - 1)), token = (first + row) % p.page_size;
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], (keys + box - 1) / box * box * 128 * kPanels);
-        __syncwarp();
-        if (row < keys)
-          tma_load_4d(ring[st] + panel * (kUnit * 128) + row * 128, map, &full[st], panel * 64, x.head, token, at);
-      }
-      if (i + 1 < x.steps && row < kUnit) page = cache_page(p, x, table, first + kUnit + row);
-    }
-  }
-  if (!ok)   // the copies in flight land before the CTA leaves
-    for (uint32_t i = n < kRing ? 0 : n - kRing; i < n; ++i) drain_wait(&full[i % kRing], (i / kRing) & 1);
-}
-
-template <typename DT, int DP, bool kBoxes>
-__global__ void __launch_bounds__(kWideThreads, 1)
-    attn_paged_wide_kernel(const PagedArgs p, const __grid_constant__ CUtensorMap key_map,
-                           const __grid_constant__ CUtensorMap value_map, int box) {
+__global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const PagedArgs p) {
   using Tr = Pair16<DT>;
+  constexpr int kChunks = DP / 8;
   constexpr int kPanelBytes = kUnit * 128;
   constexpr uint32_t idesc_qk = umma_idesc_f16(Tr::kBF16, kWideRows, kUnit, false);
   constexpr uint32_t idesc_pv = umma_idesc_f16(Tr::kBF16, kWideRows, DP, true);
@@ -194,18 +65,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
-    for (int i = 0; i < kWideKStages; ++i) mbar_init(&sm.k_full[i], 1), mbar_init(&sm.k_empty[i], 1);
-    for (int i = 0; i < kWideVStages; ++i) mbar_init(&sm.v_full[i], 1), mbar_init(&sm.v_empty[i], 1);
-    for (int t = 0; t < 2; ++t) {
-      for (int s = 0; s < 2; ++s) {
-        mbar_init(&sm.s_full[t][s], 1);
-        mbar_init(&sm.p_full[t][s], 4);   // one lane of each of the stream's warps
-        mbar_init(&sm.o_full[t][s], 1);
-      }
+    for (int i = 0; i < kWideStages; ++i) {
+      mbar_init(&sm.full[i], kWideLoaders);   // one lane of each loading warp
+      mbar_init(&sm.empty[i], 1);   // the products that read the stage
     }
-    mbar_init(&sm.q_full, 8);             // one lane of each softmax warp
-    mbar_init(&sm.stats_full, 8);
-    mbar_init(&sm.o_free, 8);
+    mbar_init(&sm.q_full, 4);
+    mbar_init(&sm.s_full, 1);
+    mbar_init(&sm.p_full, 4);
+    mbar_init(&sm.o_full, 1);
     mbar_init(&sm.drain, 1);
     mbar_init(&sm.never, 1);
     fence_mbar_init();
@@ -213,7 +80,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     p.splits[blockIdx.x].n = 0;
     p.status[blockIdx.x] = 0u;
   }
-  if (warp == 10) {
+  if (warp == 6) {
     tmem_alloc(&sm.tmem_base, kWideTmemCols);
     tmem_relinquish();
   }
@@ -226,150 +93,154 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   PieceWalk walk(share);
   Piece x;
 
-  if (warp == 8) {
-    if constexpr (kBoxes)
-      wide_load_boxes<DT, DP, kWideKStages>(p, &key_map, box, walk, false, sm.k, sm.places[0], sm.k_full, sm.k_empty,
-                                            abort_flag);
-    else
-      wide_load_rows<DT, DP, kWideKStages>(p, walk, false, sm.k, sm.places[0], sm.k_full, sm.k_empty, abort_flag);
-  } else if (warp == 9) {
-    if constexpr (kBoxes)
-      wide_load_boxes<DT, DP, kWideVStages>(p, &value_map, box, walk, true, sm.v, sm.places[1], sm.v_full, sm.v_empty,
-                                            abort_flag);
-    else
-      wide_load_rows<DT, DP, kWideVStages>(p, walk, true, sm.v, sm.places[1], sm.v_full, sm.v_empty, abort_flag);
-  } else if (warp == 10) {
+  if (warp >= 4 && warp < 6) {
+    // ---------------------------------------------------------------- loads
+    constexpr int kWarpKeys = kUnit / kWideLoaders;
+    constexpr int kLaneKeys = 32 / kChunks, kCopies = kWarpKeys / kLaneKeys;
+    const int copy_key = lane / kChunks, copy_chunk = lane % kChunks;
+    const bool copy_in = copy_chunk * 8 < p.d;
+    uint32_t n = 0;   // units issued
+    bool ok = true;
+    // announces unit i, whose copies have landed
+    auto announce = [&](uint32_t i) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.full[i % kWideStages]);
+    };
+    while (ok && walk.next<kWideRows>(p, x)) {
+      const int32_t* table = p.table + (long long)x.seq * p.table_stride;
+      for (int i = 0; i < x.steps; ++i, ++n) {
+        const int first = (x.blk0 + i) * kUnit + (warp - 4) * kWarpKeys;
+        // each lane the place of one key and of its value
+        const long long koff = cache_offset(p, x, table, first + lane, false);
+        const long long voff = cache_offset(p, x, table, first + lane, true);
+        const uint32_t st = n % kWideStages;
+        if (n >= kWideStages && !WIDE_WAIT(&sm.empty[st], (n / kWideStages - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        const uint32_t kt = smem_u32(sm.k[st]), vt = smem_u32(sm.v[st]);
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c) {
+          const int key = c * kLaneKeys + copy_key, row = (warp - 4) * kWarpKeys + key;
+          const bool take = copy_in && first + key < x.key_end;
+          const uint32_t at = (copy_chunk >> 3) * kPanelBytes + row * 128 + (((copy_chunk & 7) ^ (row & 7)) << 4);
+          const long long ko = __shfl_sync(0xffffffffu, koff, key), vo = __shfl_sync(0xffffffffu, voff, key);
+          const int col = take ? copy_chunk * 8 : 0;
+          cp_async16(kt + at, static_cast<const DT*>(p.kc) + ko + col, take);
+          cp_async16(vt + at, static_cast<const DT*>(p.vc) + vo + col, take);
+        }
+        cp_async_commit();
+        if (n > 0) {
+          cp_async_wait<1>();
+          announce(n - 1);
+        }
+      }
+    }
+    cp_async_wait<0>();
+    if (n > 0) announce(n - 1);
+  } else if (warp == 6) {
     // ---------------------------------------------------------------- products
     const bool issue = elect_one_sync();
-    auto ready = [&](uint64_t* bar, uint32_t parity) {   // lane 0's answer for the whole warp
-      return __shfl_sync(0xffffffffu, mbar_test_wait(bar, parity) ? 1 : 0, 0) != 0;
-    };
-    uint32_t ns = 0, np = 0;         // units whose scores, whose outputs have been issued
-    uint32_t cs[2] = {0, 0}, cp[2] = {0, 0};   // the same by stream
-    uint32_t pieces = 0;
-    const uint32_t hi = smem_desc_sw128_hi(1024), qlo = smem_desc_sw128_lo(smem_u32(sm.q), 16);
+    uint32_t n = 0, pieces = 0;   // units, pieces
     bool ok = true;
+    const uint32_t khi = smem_desc_sw128_hi(1024);
     if (p.inject_wait) ok = WIDE_WAIT(&sm.never, 0);   // test setting: a wait that runs out, loads in flight
     while (ok && walk.next<kWideRows>(p, x)) {
       if (x.steps == 0) continue;
       if (!WIDE_WAIT(&sm.q_full, pieces & 1)) break;
-      int is = 0, ip = 0;   // of this piece
-      uint64_t since = globaltimer_ns();
-      for (uint32_t polls = 1; ok && ip < x.steps; ++polls) {
-        bool moved = false;
-        // scores of the next unit: its tile of tensor memory is free once the outputs of the unit four
-        // before it, which read its weights there, have been issued
-        if (is < x.steps && is < ip + 4 && ready(&sm.k_full[ns % kWideKStages], (ns / kWideKStages) & 1)) {
-          const int t = is & 1, s = cs[t] & 1;
-          tc_fence_after();
-          const uint32_t klo = smem_desc_sw128_lo(smem_u32(sm.k[ns % kWideKStages]), 16);
-#pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk)
-            umma_ss_if(issue, tmem + 128 * t + 64 * s,
-                       smem_desc_join(qlo + (((kk >> 2) * (kWideRows * 128) + (kk & 3) * 32) >> 4), hi),
-                       smem_desc_join(klo + (((kk >> 2) * kPanelBytes + (kk & 3) * 32) >> 4), hi), idesc_qk,
-                       kk > 0 ? 1u : 0u);
-          umma_commit_if(issue, &sm.s_full[t][s]);
-          umma_commit_if(issue, &sm.k_empty[ns % kWideKStages]);
-          ++is, ++ns, ++cs[t];
-          moved = true;
-        }
-        // outputs of the oldest unit
-        const int t = ip & 1, s = cp[t] & 1;
-        if (ip < is && ready(&sm.p_full[t][s], (cp[t] >> 1) & 1) &&
-            ready(&sm.v_full[np % kWideVStages], (np / kWideVStages) & 1)) {
-          if (ip == 0 && pieces > 0 && !WIDE_WAIT(&sm.o_free, (pieces - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t vlo = smem_desc_sw128_lo(smem_u32(sm.v[np % kWideVStages]), kPanelBytes);
-#pragma unroll
-          for (int kk = 0; kk < kUnit / 16; ++kk)
-            umma_ts_if(issue, tmem + 256 + 128 * t, tmem + 128 * t + 64 * s + kk * 8,
-                       smem_desc_join(vlo + ((kk * 16 * 128) >> 4), hi), idesc_pv, (ip > 1 || kk > 0) ? 1u : 0u);
-          umma_commit_if(issue, &sm.o_full[t][s]);
-          umma_commit_if(issue, &sm.v_empty[np % kWideVStages]);
-          ++ip, ++np, ++cp[t];
-          moved = true;
-        }
-        if (moved) {
-          polls = 0;
-        } else if ((polls & p.wait_check_mask) == 0) {   // bounded as mbar_wait is
-          if (polls <= p.wait_check_mask + 1) since = globaltimer_ns();
-          const bool late = lane == 0 && globaltimer_ns() - since > p.wait_limit_ns;
-          if (late) {
-            *abort_flag = 1u;
-            atomicOr(&p.status[blockIdx.x], THD_STATUS_WAIT_TIMEOUT);
-          }
-          if (__any_sync(0xffffffffu, late || *abort_flag)) ok = false;
-        }
-      }
       ++pieces;
+      for (int i = 0; i < x.steps; ++i, ++n) {
+        const uint32_t st = n % kWideStages;
+        if (!WIDE_WAIT(&sm.full[st], (n / kWideStages) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t klo = smem_desc_sw128_lo(smem_u32(sm.k[st]), 16);
+        const uint32_t vlo = smem_desc_sw128_lo(smem_u32(sm.v[st]), kPanelBytes);
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)
+          umma_ts_if(issue, tmem, tmem + 64 + kk * 8,
+                     smem_desc_join(klo + (((kk >> 2) * kPanelBytes + (kk & 3) * 32) >> 4), khi), idesc_qk,
+                     kk > 0 ? 1u : 0u);
+        umma_commit_if(issue, &sm.s_full);
+        if (!WIDE_WAIT(&sm.p_full, n & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kUnit / 16; ++kk)
+          umma_ts_if(issue, tmem + 128, tmem + kk * 8, smem_desc_join(vlo + ((kk * 16 * 128) >> 4), khi), idesc_pv,
+                     (i > 0 || kk > 0) ? 1u : 0u);
+        umma_commit_if(issue, &sm.empty[st]);
+        umma_commit_if(issue, &sm.o_full);
+      }
     }
     // what was issued completes before tensor memory is released
     umma_commit_if(issue, &sm.drain);
     drain_wait(&sm.drain, 0);
-  } else if (warp < 8) {
+  } else {
     // ---------------------------------------------------------------- softmax
-    const int t = warp >> 2, r = tid & 127;   // stream; row of the tile, lane of tensor memory
-    const uint32_t t_lane = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + t_lane + 128 * t, tO = tmem + t_lane + 256;
+    const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
+    const uint32_t tS = tmem + t_lane, tQ = tS + 64, tO = tS + 128;
+    const int r = tid;   // row of the tile, lane of tensor memory
     const float sl2 = p.scale_log2;
-    uint32_t n[2] = {0, 0};   // units of each stream so far
-    uint32_t pieces = 0;
+    uint32_t n = 0;      // units
     bool ok = true;
     while (ok && walk.next<kWideRows>(p, x)) {
       const int row = x.row0 + r, tok = row / p.group, hq = x.head * p.group + (row - tok * p.group);
       const bool valid = r < x.rows;
-      const long long at = ((long long)(x.s.q_start + (valid ? tok : 0)) * p.Hq + (valid ? hq : 0)) * p.d;
-      const int units[2] = {(x.steps + 1) / 2, x.steps / 2};
+      const uint64_t word0 = tree_word(p, x, valid ? tok : 0);
+      float m_run = -INFINITY, l_run = 0.f, l_exact = 0.f;
       if (x.steps > 0) {
-        // this stream's half of the row's query; the last piece's products have read theirs
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const DT*>(p.q) + at);
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const DT*>(p.q) + ((long long)(x.s.q_start + (valid ? tok : 0)) * p.Hq + (valid ? hq : 0)) * p.d);
 #pragma unroll
-        for (int e = 0; e < DP / 16; ++e) {
-          const int c = t * (DP / 16) + e;
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (valid && c * 8 < p.d) w = src[c];
-          *reinterpret_cast<uint4*>(sm.q + (c >> 3) * (kWideRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w;
+        for (int c = 0; c < DP / 32; ++c) {
+          uint32_t qv[16];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (valid && (c * 4 + e) * 8 < p.d) w = src[c * 4 + e];
+            qv[4 * e] = w.x, qv[4 * e + 1] = w.y, qv[4 * e + 2] = w.z, qv[4 * e + 3] = w.w;
+          }
+          tmem_st16(tQ + 16 * c, qv);
         }
-        fence_proxy_async_smem();
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.q_full);
       }
-      float m_run = -INFINITY, l_run = 0.f, l_exact = 0.f;
-      for (int i = t; i < x.steps; i += 2) {
-        const uint32_t c = n[t] + (i >> 1);
-        const uint32_t tT = tS + 64 * (c & 1);
-        if (!WIDE_WAIT(&sm.s_full[t][c & 1], (c >> 1) & 1)) {
+      for (int i = 0; i < x.steps; ++i, ++n) {
+        if (!WIDE_WAIT(&sm.s_full, n & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
         uint32_t sr[64];
-        tmem_ld32(tT, sr);
-        tmem_ld32(tT + 32, sr + 32);
+        tmem_ld32(tS, sr);
+        tmem_ld32(tS + 32, sr + 32);
         tmem_ld_wait_regs32(sr);
         tmem_tie_regs32(sr + 32);
         const int first = (x.blk0 + i) * kUnit;
         if (first + kUnit > min(p.tree ? x.past : x.past + 1, x.s.kv_len)) {   // some key may be hidden from some row
-          const uint64_t seen = valid ? seen_keys(p, x, tok, first) : 0ull;
+          const uint64_t seen = valid ? seen_keys(p, x, tok, first, word0) : 0ull;
           const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            if (!(lo >> e & 1)) sr[e] = __float_as_uint(-INFINITY);
-            if (!(hi >> e & 1)) sr[32 + e] = __float_as_uint(-INFINITY);
+          for (int c = 0; c < 32; ++c) {
+            if (!(lo >> c & 1)) sr[c] = __float_as_uint(-INFINITY);
+            if (!(hi >> c & 1)) sr[32 + c] = __float_as_uint(-INFINITY);
           }
         }
-        float mx[4] = {m_run, -INFINITY, -INFINITY, -INFINITY};
+        float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 64; e += 8) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mx[k] = fmax3f(mx[k], __uint_as_float(sr[e + 2 * k]), __uint_as_float(sr[e + 2 * k + 1]));
+        for (int c = 0; c < 64; c += 4) {
+          mx0 = fmax3f(mx0, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+          mx1 = fmax3f(mx1, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
         }
-        const float m_new = fmax3f(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+        const float m_new = fmax3f(m_run, mx0, mx1);
         // the maximum moves only when it grows by more than 8 (log2): weights stay below 2^8 and the
         // output is seldom rescaled
         const bool need = (m_new - m_run) * sl2 > 8.f;   // false while both are -inf
@@ -381,130 +252,92 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           l_exact *= alpha;
         }
         const float mb = (m_run == -INFINITY ? 0.f : m_run) * sl2;
-        float ex[4] = {0.f, 0.f, 0.f, 0.f}, rd[4] = {0.f, 0.f, 0.f, 0.f};
+        float e0 = 0.f, e1 = 0.f, r0 = 0.f, r1 = 0.f;
         uint32_t pk[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float a = ex2_approx(fmaf(__uint_as_float(sr[2 * e]), sl2, -mb));
-          const float b = ex2_approx(fmaf(__uint_as_float(sr[2 * e + 1]), sl2, -mb));
-          pk[e] = Tr::put(a, b);
-          const float2 w = Tr::get(pk[e]);
-          ex[(2 * e) & 3] += a;
-          ex[(2 * e + 1) & 3] += b;
-          rd[(2 * e) & 3] += w.x;
-          rd[(2 * e + 1) & 3] += w.y;
+        for (int c = 0; c < 32; ++c) {
+          const float a = ex2_approx(fmaf(__uint_as_float(sr[2 * c]), sl2, -mb));
+          const float b = ex2_approx(fmaf(__uint_as_float(sr[2 * c + 1]), sl2, -mb));
+          pk[c] = Tr::put(a, b);
+          e0 += a;
+          e1 += b;
+          const float2 r = Tr::get(pk[c]);
+          r0 += r.x;
+          r1 += r.y;
         }
-        l_exact += (ex[0] + ex[1]) + (ex[2] + ex[3]);
-        l_run += (rd[0] + rd[1]) + (rd[2] + rd[3]);
-        tmem_st32(tT, pk);
-        if (i > 1 && __any_sync(0xffffffffu, need)) {
-          if (!WIDE_WAIT(&sm.o_full[t][(c - 1) & 1], ((c - 1) >> 1) & 1)) {
+        l_exact += e0 + e1;
+        l_run += r0 + r1;
+        tmem_st32(tS, pk);
+        if (i > 0 && __any_sync(0xffffffffu, need)) {
+          if (!WIDE_WAIT(&sm.o_full, (n - 1) & 1)) {
             tmem_st_wait();
             ok = false;
             break;
           }
           tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < DP / 32; ++k) {
+          for (int c = 0; c < DP / 32; ++c) {
             uint32_t o[32];
-            tmem_ld32(tO + 128 * t + 32 * k, o);
+            tmem_ld32(tO + 32 * c, o);
             tmem_ld_wait_regs32(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(tO + 128 * t + 32 * k, o);
+            tmem_st32(tO + 32 * c, o);
           }
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[t][c & 1]);
+        if (lane == 0) mbar_arrive(&sm.p_full);
       }
       if (!ok) break;
-      // ---- the tile's output, or this piece's share of it: both streams' outputs, half of the columns ----
-      float ms[2] = {-INFINITY, -INFINITY}, ls[2] = {0.f, 0.f}, le[2] = {0.f, 0.f}, w[2], sum = 0.f, se = 0.f;
+      // ---- the tile's output, or this piece's share of it ----
       if (x.steps > 0) {
-        auto& stats = sm.stats[pieces & 1];
-        stats[t][0][r] = m_run;
-        stats[t][1][r] = l_run;
-        stats[t][2][r] = l_exact;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.stats_full);
-        if (!WIDE_WAIT(&sm.stats_full, pieces & 1)) break;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          ms[k] = stats[k][0][r];
-          ls[k] = stats[k][1][r];
-          le[k] = stats[k][2][r];
-        }
-        // the last product of each stream, and with it those before
-        n[0] += units[0];
-        n[1] += units[1];
-        for (int k = 0; ok && k < 2; ++k)
-          if (units[k] > 0) ok = WIDE_WAIT(&sm.o_full[k][(n[k] - 1) & 1], ((n[k] - 1) >> 1) & 1);
-        if (!ok) break;
+        if (!WIDE_WAIT(&sm.o_full, (n - 1) & 1)) break;
         tc_fence_after();
-        ++pieces;
       }
-      const float mm = fmaxf(ms[0], ms[1]);
-      const float top = mm * sl2;   // -inf: no key seen
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        w[k] = ms[k] == -INFINITY ? 0.f : ex2_approx((ms[k] - mm) * sl2);
-        sum += w[k] * ls[k];
-        se += w[k] * le[k];
-      }
+      const float top = m_run * sl2;   // -inf: no key seen
       const int part = part_of_piece(x);
-      const float inv = x.whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-      const float w0 = w[0] * inv, w1 = w[1] * inv;
-      DT* dst = static_cast<DT*>(p.out) + at;
+      const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+      DT* dst = static_cast<DT*>(p.out) + ((long long)(x.s.q_start + (valid ? tok : 0)) * p.Hq + (valid ? hq : 0)) * p.d;
       float* pdst = p.part_o + (long long)part * kWideRows * DP + r * 4;
 #pragma unroll
-      for (int k = 0; k < DP / 64; ++k) {
-        const int col = t * (DP / 2) + 32 * k;
-        float f[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) f[e] = 0.f;
+      for (int c = 0; c < DP / 32; ++c) {
+        uint32_t o[32];
         if (x.steps > 0) {
-          uint32_t o[32];
-          tmem_ld32(tO + col, o);
+          tmem_ld32(tO + 32 * c, o);
           tmem_ld_wait_regs32(o);
+        } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) f[e] = w0 == 0.f ? 0.f : w0 * __uint_as_float(o[e]);
-          if (units[1] > 0) {
-            tmem_ld32(tO + 128 + col, o);
-            tmem_ld_wait_regs32(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) f[e] += w1 == 0.f ? 0.f : w1 * __uint_as_float(o[e]);
-          }
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
         if (valid) {
           if (x.whole) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              if (col + e < p.d) *reinterpret_cast<uint4*>(dst + col + e) = pack8<DT>(f + e);
+            for (int e = 0; e < 32; e += 8) {
+              float f[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) f[k] = l_run == 0.f ? 0.f : __uint_as_float(o[e + k]) * inv;
+              if (32 * c + e < p.d) *reinterpret_cast<uint4*>(dst + 32 * c + e) = pack8<DT>(f);
+            }
           } else {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(pdst + ((col + e) / 4) * (kWideRows * 4)) =
-                  make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+              *reinterpret_cast<uint4*>(pdst + (8 * c + e / 4) * (kWideRows * 4)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         }
       }
-      if (x.steps > 0) {   // the outputs are read before the next piece's products write over them
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.o_free);
-      }
-      if (valid && t == 0) {
+      tc_fence_before();   // the output is read before the next piece's products write over it
+      if (valid) {
         if (x.whole) {
           if (p.lse)
             p.lse[(long long)hq * p.T + x.s.q_start + tok] =
-                se == 0.f ? -INFINITY : top * 0.69314718055994531f + logf(se);
+                l_exact == 0.f ? -INFINITY : top * 0.69314718055994531f + logf(l_exact);
         } else {
           float* pm = p.part_m + (long long)part * 3 * kWideRows;
           pm[r] = top;
-          pm[kWideRows + r] = sum;
-          pm[2 * kWideRows + r] = se;
+          pm[kWideRows + r] = l_run;
+          pm[2 * kWideRows + r] = l_exact;
         }
       }
       if (tid == 0) note_split(p, x, share);
@@ -512,7 +345,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 10) {
+  if (warp == 6) {
     tc_fence_after();
     tmem_dealloc(tmem, kWideTmemCols);
   }

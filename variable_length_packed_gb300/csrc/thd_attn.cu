@@ -195,23 +195,6 @@ int launch_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& 
 
 }  // namespace
 
-namespace thd {
-// A 4-D view (head_dim values, heads, tokens of a page, pages) of a paged cache, box = 64 values x 1 head x
-// `box` tokens x 1 page, 128-byte swizzle.  strides: bytes from page to page, token to token, head to head.
-bool encode_cache_map(CUtensorMap* map, const void* base, int d, int heads, int page_size, int pages, int box,
-                      const int64_t* strides, bool bf16) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)page_size, (cuuint64_t)pages};
-  cuuint64_t steps[3] = {(cuuint64_t)strides[2], (cuuint64_t)strides[1], (cuuint64_t)strides[0]};
-  cuuint32_t boxes[4] = {64u, 1u, (cuuint32_t)box, 1u};
-  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base),
-            dims, steps, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-}  // namespace thd
-
 extern "C" {
 
 size_t thd_attn_bwd_workspace_size(int total_tokens, int num_heads_q, int head_dim) {

@@ -182,12 +182,12 @@ def thd_qk_norm_rope(q, k, cu_seqlens, rope_cos=None, rope_sin=None, cu_seqlens_
     rows, rot = _tables(rope_cos, rope_sin, dev, d)
     fp32 = _weights(q_weight, k_weight, dev, d, dtype)
     if q_out is None:
-        q_out = q.new_empty((T, hq, d))
+        q_out = torch.empty((T, hq, d), dtype=dtype, device=dev)
     else:
         _whole(q_out, "q_out", dev, dtype, q.shape)
     if k is not None:
         if k_out is None:
-            k_out = q.new_empty((T, hkv, d))
+            k_out = torch.empty((T, hkv, d), dtype=dtype, device=dev)
         else:
             _whole(k_out, "k_out", dev, dtype, k.shape)
     _call("thd_qk_norm_rope", dev, _addr(q), qs, _addr(k), ks, _addr(q_weight), _addr(k_weight), fp32, float(eps),
@@ -226,19 +226,19 @@ def thd_qk_norm_rope_bwd(grad_q, grad_k, q, k, cu_seqlens, rope_cos=None, rope_s
     B = _meta(dev, batch_size, cu_seqlens, cu_seqlens_padded, "position_offsets", position_offsets)
     rows, rot = _tables(rope_cos, rope_sin, dev, d)
     if dq is None:
-        dq = grad_q.new_empty((T, hq, d))
+        dq = torch.empty((T, hq, d), dtype=dtype, device=dev)
     dqs = _rows(dq, "dq", dev, dtype, grad_q.shape)
     dks = 0
     if grad_k is not None:
         if dk is None:
-            dk = grad_q.new_empty((T, hkv, d))
+            dk = torch.empty((T, hkv, d), dtype=dtype, device=dev)
         dks = _rows(dk, "dk", dev, dtype, grad_k.shape)
     grads = []
     for name, w, g in (("dq_weight", q_weight, dq_weight), ("dk_weight", k_weight, dk_weight)):
         if w is None and g is not None:
             raise ValueError(f"{name} needs its weight")
         if w is not None and g is None:
-            g = grad_q.new_empty(d, dtype=torch.float32)
+            g = torch.empty(d, dtype=torch.float32, device=dev)
         _whole(g, name, dev, torch.float32, (d,))
         grads.append(g)
     size = 0
@@ -333,7 +333,7 @@ def thd_kv_append(k, v, k_cache, v_cache, page_table, cache_lens, cu_seqlens, cu
         raise ValueError("a page must hold a token")
     if q is not None:
         if q_out is None:
-            q_out = k.new_empty((T, hq, d))
+            q_out = torch.empty((T, hq, d), dtype=dtype, device=dev)
         else:
             _whole(q_out, "q_out", dev, dtype, q.shape)
     _call("thd_kv_append", dev, _addr(q), qs, _addr(k), ks, v.data_ptr(), vs, _addr(q_weight), _addr(k_weight), fp32,
@@ -376,11 +376,11 @@ def thd_attn_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q, cu_se
             raise ValueError("tree_mask must be [T, words]")
         words = tree_mask.shape[1]
     if out is None:
-        out = q.new_empty((T, hq, d))
+        out = torch.empty((T, hq, d), dtype=dtype, device=dev)
     else:
         _whole(out, "out", dev, dtype, q.shape)
     if lse is None and return_lse:
-        lse = q.new_empty((hq, T), dtype=torch.float32)
+        lse = torch.empty((hq, T), dtype=torch.float32, device=dev)
     else:
         _whole(lse, "lse", dev, torch.float32, (hq, T))
     if workspace is None:
