@@ -283,6 +283,17 @@ def test_append_past_the_table_writes_nothing():
     assert torch.equal(one[1, 0], x) and torch.equal(one[1, 1], 2 * x) and torch.all(one[[0, 2]] == 0)
 
 
+def test_append_past_two_to_the_31_elements():
+    x = torch.randn(3, 1, 128, device="cuda").to(BF16)
+    kc = torch.zeros((1 << 20) + 2, 16, 1, 128, dtype=BF16, device="cuda")
+    vc = torch.zeros_like(kc)
+    last = (1 << 20) + 1
+    vlp.thd_kv_append(x, 2 * x, kc, vc, ints([[last, 7]]), ints([14]), ints([0, 3]))
+    assert torch.equal(kc[last, 14:], x[:2]) and torch.equal(vc[last, 14:], 2 * x[:2])
+    assert torch.equal(kc[7, :1], x[2:]) and torch.equal(vc[7, :1], 2 * x[2:])
+    assert int(kc.count_nonzero()) == int(x.count_nonzero())
+
+
 def test_binding_refusals():
     x = torch.zeros(4, 2, 64, dtype=BF16, device="cuda")
     cu, w = ints([0, 4]), torch.ones(64, dtype=BF16, device="cuda")

@@ -14,10 +14,15 @@
 //  * a unit is kUnit keys of one (sequence, key/value head, row tile); the units of the batch
 //    are laid end to end and every CTA takes an equal share of them, whatever the lengths;
 //  * a CTA whose share ends inside a tile writes an unnormalised partial (at most two per CTA),
-//    and a second kernel, launched to overlap the first one's end, joins them;
-//  * inside a CTA each warp runs alone: it streams its own 16 keys of each unit through its own
-//    ring of shared memory with 16-byte asynchronous copies, keeps a running maximum, sums and
-//    output tile in registers, and meets the other warps only when the tile is done.
+//    and a second kernel, launched to overlap the first one's end, joins them.
+// Tiles of more than 16 rows are attn_paged_wide.cuh's.  Here, with 16 rows (decoding: the heads of
+// one group), the products are 128 of the warp-wide 16 x 8 x 16 ones per 32 KB, about a fifth of their rate when
+// the keys come at memory speed, so each warp runs alone: it streams its own 16 keys of each unit
+// through its own ring of shared memory with 16-byte asynchronous copies, keeps a running maximum, sums
+// and output tile in registers, and meets the other warps only when the tile is done.
+// Measured: 500000 keys of 64 sequences, 32 + 8 heads of 128, one token each, 310 us, 6.6 TB/s of the
+// 6.8 that a copy reaches; 262144 keys of one sequence, 16 heads of 64, 166 us, 6.5 TB/s.  Four times as many
+// CTAs with shorter shares (an SM that is slower takes fewer) gained nothing: 319 and 186 us.
 #include <cmath>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -35,6 +40,7 @@ void wait_settings(uint64_t* limit_ns, uint32_t* check_mask, uint32_t* inject);
 
 namespace {
 
+constexpr int kNarrowRows = 16;      // rows of a tile
 constexpr int kWarps = 4;            // warps of a CTA, 16 keys of the unit each
 constexpr int kWarpKeys = kUnit / kWarps;
 constexpr int kStages = 3;           // units in flight per warp
@@ -72,24 +78,23 @@ __device__ __forceinline__ void mma16816<__half>(float* c, const uint32_t* a, ui
 // Shared memory of a CTA: each warp's ring of key and value tiles (16 rows of DP values,
 // 16-byte chunks XORed with the row so that eight rows of one column of chunks lie in
 // different banks); at a tile's end the warps' sums and outputs take its place.
-template <int DP, int MT>
+template <int DP>
 struct PagedSmem {
   static constexpr int kTileBytes = kWarpKeys * DP * 2;
   static constexpr int kRing = kWarps * kStages * 2 * kTileBytes;
-  static constexpr int kJoin = kWarps * MT * (DP + 3) * 4;
+  static constexpr int kJoin = kWarps * kNarrowRows * (DP + 3) * 4;
   static constexpr int kBytes = kRing > kJoin ? kRing : kJoin;
 };
 
-// MT: rows of a tile (16 or 32).
-template <typename DT, int DP, int MT>
+template <typename DT, int DP>
 __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedArgs p) {
-  constexpr int kMF = MT / 16;          // 16-row fragments
+  constexpr int MT = kNarrowRows;
   constexpr int kKSteps = DP / 16;      // of the score product
   constexpr int kNT = DP / 8;           // 8-column output fragments
   constexpr int kChunks = DP / 8;       // 16-byte chunks of a key
   constexpr int kLaneKeys = 32 / kChunks;               // keys one copy instruction covers
   constexpr int kCopies = kWarpKeys / kLaneKeys;
-  constexpr int kTileBytes = PagedSmem<DP, MT>::kTileBytes;
+  constexpr int kTileBytes = PagedSmem<DP>::kTileBytes;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Share share;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -138,43 +143,37 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
     long long next_off = offset_of(kStages - 1);
 
     // ---- queries: the A fragments of the tile ----
-    uint32_t qf[kMF][kKSteps][4];
-    int token[kMF][2];            // of the row, -1 past the last row
+    uint32_t qf[kKSteps][4];
+    int token[2];            // of the row, -1 past the last row
     const int qr = lane >> 2, qc = (lane & 3) * 2;
 #pragma unroll
-    for (int f = 0; f < kMF; ++f) {
+    for (int hh = 0; hh < 2; ++hh) {
+      const int r = hh * 8 + qr;
+      const int row = x.row0 + r;
+      const int tok = row / p.group;
+      const bool ok = r < x.rows;
+      token[hh] = ok ? tok : -1;
+      const DT* src = static_cast<const DT*>(p.q) +
+                      ((long long)(x.s.q_start + tok) * p.Hq + x.head * p.group + (row - tok * p.group)) * p.d;
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int r = f * 16 + hh * 8 + qr;
-        const int row = x.row0 + r;
-        const int tok = row / p.group;
-        const bool ok = r < x.rows;
-        token[f][hh] = ok ? tok : -1;
-        const DT* src = static_cast<const DT*>(p.q) +
-                        ((long long)(x.s.q_start + tok) * p.Hq + x.head * p.group + (row - tok * p.group)) * p.d;
+      for (int k = 0; k < kKSteps; ++k) {
 #pragma unroll
-        for (int k = 0; k < kKSteps; ++k) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int col = k * 16 + half * 8 + qc;
-            qf[f][k][half * 2 + hh] = ok && col < p.d ? *reinterpret_cast<const uint32_t*>(src + col) : 0u;
-          }
+        for (int half = 0; half < 2; ++half) {
+          const int col = k * 16 + half * 8 + qc;
+          qf[k][half * 2 + hh] = ok && col < p.d ? *reinterpret_cast<const uint32_t*>(src + col) : 0u;
         }
       }
     }
 
-    float o[kMF][kNT][4], m[kMF][2], l[kMF][2], lr[kMF][2];
+    float o[kNT][4], m[2], l[2], lr[2];
 #pragma unroll
-    for (int f = 0; f < kMF; ++f) {
+    for (int n = 0; n < kNT; ++n)
 #pragma unroll
-      for (int n = 0; n < kNT; ++n)
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[f][n][e] = 0.f;
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        m[f][hh] = -INFINITY;
-        l[f][hh] = lr[f][hh] = 0.f;
-      }
+    for (int hh = 0; hh < 2; ++hh) {
+      m[hh] = -INFINITY;
+      l[hh] = lr[hh] = 0.f;
     }
 
     int stage = 0;
@@ -189,80 +188,69 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
       const uint32_t kt = ring + stage * (2 * kTileBytes), vt = kt + kTileBytes;
       const int unit0 = (x.blk0 + i) * kUnit;
       // ---- scores ----
-      float c[kMF][2][4];
+      float c[2][4];
 #pragma unroll
-      for (int f = 0; f < kMF; ++f)
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) c[f][n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) c[n][e] = 0.f;
 #pragma unroll
       for (int k = 0; k < kKSteps; ++k) {
         uint32_t kb[4];   // keys 0-7 (both halves of the 16 columns), keys 8-15
         const int row = ld_row + (ld_mat >> 1) * 8, chunk = 2 * k + (ld_mat & 1);
         ldsm4(kt + row * (DP * 2) + ((chunk ^ ld_row) << 4), kb);
-#pragma unroll
-        for (int f = 0; f < kMF; ++f) {
-          mma16816<DT>(c[f][0], qf[f][k], kb[0], kb[1]);
-          mma16816<DT>(c[f][1], qf[f][k], kb[2], kb[3]);
-        }
+        mma16816<DT>(c[0], qf[k], kb[0], kb[1]);
+        mma16816<DT>(c[1], qf[k], kb[2], kb[3]);
       }
       // ---- visibility ----
       // some key of the unit may be hidden from some row
       const bool cut = unit0 + kUnit > min(p.tree ? x.past : x.past + 1, x.s.kv_len);
 #pragma unroll
-      for (int f = 0; f < kMF; ++f) {
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int e = 0; e < 4; ++e) c[n][e] *= p.scale_log2;
+      if (cut) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) c[f][n][e] *= p.scale_log2;
-        if (cut) {
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const uint64_t all = token[f][hh] >= 0 ? seen_keys(p, x, token[f][hh], unit0, tree_word(p, x, token[f][hh])) : 0ull;
-            const uint32_t seen = (uint32_t)(all >> (warp * kWarpKeys)) >> qc;   // this lane's: bits 0, 1, 8, 9
-            if (!(seen & 1)) c[f][0][2 * hh] = -INFINITY;
-            if (!(seen & 2)) c[f][0][2 * hh + 1] = -INFINITY;
-            if (!(seen & 256)) c[f][1][2 * hh] = -INFINITY;
-            if (!(seen & 512)) c[f][1][2 * hh + 1] = -INFINITY;
-          }
+        for (int hh = 0; hh < 2; ++hh) {
+          const uint64_t all = token[hh] >= 0 ? seen_keys(p, x, token[hh], unit0, tree_word(p, x, token[hh])) : 0ull;
+          const uint32_t seen = (uint32_t)(all >> (warp * kWarpKeys)) >> qc;   // this lane's: bits 0, 1, 8, 9
+          if (!(seen & 1)) c[0][2 * hh] = -INFINITY;
+          if (!(seen & 2)) c[0][2 * hh + 1] = -INFINITY;
+          if (!(seen & 256)) c[1][2 * hh] = -INFINITY;
+          if (!(seen & 512)) c[1][2 * hh + 1] = -INFINITY;
         }
       }
       // ---- running maximum and sums, weights ----
-      uint32_t pf[kMF][4];
+      uint32_t pf[4];
+      float scale[2];
 #pragma unroll
-      for (int f = 0; f < kMF; ++f) {
-        float scale[2];
+      for (int hh = 0; hh < 2; ++hh) {
+        float top = fmaxf(fmaxf(c[0][2 * hh], c[0][2 * hh + 1]), fmaxf(c[1][2 * hh], c[1][2 * hh + 1]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        top = fmaxf(m[hh], top);
+        const float use = top == -INFINITY ? 0.f : top;
+        scale[hh] = ex2_approx(m[hh] - use);
+        m[hh] = top;
+        float sum = 0.f, sum_r = 0.f;
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float x = fmaxf(fmaxf(c[f][0][2 * hh], c[f][0][2 * hh + 1]), fmaxf(c[f][1][2 * hh], c[f][1][2 * hh + 1]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          const float top = fmaxf(m[f][hh], x);
-          const float use = top == -INFINITY ? 0.f : top;
-          scale[hh] = ex2_approx(m[f][hh] - use);
-          m[f][hh] = top;
-          float sum = 0.f, sum_r = 0.f;
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float p0 = ex2_approx(c[f][n][2 * hh] - use), p1 = ex2_approx(c[f][n][2 * hh + 1] - use);
-            sum += p0 + p1;
-            const uint32_t w = Pair16<DT>::put(p0, p1);
-            const float2 r = Pair16<DT>::get(w);
-            sum_r += r.x + r.y;
-            pf[f][n * 2 + hh] = w;
-          }
-          l[f][hh] = l[f][hh] * scale[hh] + sum;
-          lr[f][hh] = lr[f][hh] * scale[hh] + sum_r;
+        for (int n = 0; n < 2; ++n) {
+          const float p0 = ex2_approx(c[n][2 * hh] - use), p1 = ex2_approx(c[n][2 * hh + 1] - use);
+          sum += p0 + p1;
+          const uint32_t w = Pair16<DT>::put(p0, p1);
+          const float2 r = Pair16<DT>::get(w);
+          sum_r += r.x + r.y;
+          pf[n * 2 + hh] = w;
         }
-        if (__any_sync(0xffffffffu, scale[0] != 1.f || scale[1] != 1.f)) {
+        l[hh] = l[hh] * scale[hh] + sum;
+        lr[hh] = lr[hh] * scale[hh] + sum_r;
+      }
+      if (__any_sync(0xffffffffu, scale[0] != 1.f || scale[1] != 1.f)) {
 #pragma unroll
-          for (int n = 0; n < kNT; ++n) {
-            o[f][n][0] *= scale[0];
-            o[f][n][1] *= scale[0];
-            o[f][n][2] *= scale[1];
-            o[f][n][3] *= scale[1];
-          }
+        for (int n = 0; n < kNT; ++n) {
+          o[n][0] *= scale[0];
+          o[n][1] *= scale[0];
+          o[n][2] *= scale[1];
+          o[n][3] *= scale[1];
         }
       }
       // ---- output ----
@@ -271,11 +259,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
         uint32_t vb[4];   // columns n: keys 0-7, 8-15; columns n + 1: the same
         const int row = ld_row + (ld_mat & 1) * 8, chunk = n + (ld_mat >> 1);
         ldsm4_trans(vt + row * (DP * 2) + ((chunk ^ ld_row) << 4), vb);
-#pragma unroll
-        for (int f = 0; f < kMF; ++f) {
-          mma16816<DT>(o[f][n], pf[f], vb[0], vb[1]);
-          mma16816<DT>(o[f][n + 1], pf[f], vb[2], vb[3]);
-        }
+        mma16816<DT>(o[n], pf, vb[0], vb[1]);
+        mma16816<DT>(o[n + 1], pf, vb[2], vb[3]);
       }
       stage = stage == kStages - 1 ? 0 : stage + 1;
       __syncwarp();   // every lane has read the stage that the next step's copies fill
@@ -287,25 +272,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
     float* jo = reinterpret_cast<float*>(smem);                 // [warp][row][DP]
     float* jm = jo + kWarps * MT * DP;                          // [warp][3][row]
 #pragma unroll
-    for (int f = 0; f < kMF; ++f) {
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int r = f * 16 + hh * 8 + qr;
-        float a = l[f][hh], ar = lr[f][hh];
-        a += __shfl_xor_sync(0xffffffffu, a, 1);
-        a += __shfl_xor_sync(0xffffffffu, a, 2);
-        ar += __shfl_xor_sync(0xffffffffu, ar, 1);
-        ar += __shfl_xor_sync(0xffffffffu, ar, 2);
-        if ((lane & 3) == 0) {
-          jm[(warp * 3 + 0) * MT + r] = m[f][hh];
-          jm[(warp * 3 + 1) * MT + r] = ar;
-          jm[(warp * 3 + 2) * MT + r] = a;
-        }
-#pragma unroll
-        for (int n = 0; n < kNT; ++n)
-          *reinterpret_cast<float2*>(jo + (warp * MT + r) * DP + n * 8 + qc) =
-              make_float2(o[f][n][2 * hh], o[f][n][2 * hh + 1]);
+    for (int hh = 0; hh < 2; ++hh) {
+      const int r = hh * 8 + qr;
+      float a = l[hh], ar = lr[hh];
+      a += __shfl_xor_sync(0xffffffffu, a, 1);
+      a += __shfl_xor_sync(0xffffffffu, a, 2);
+      ar += __shfl_xor_sync(0xffffffffu, ar, 1);
+      ar += __shfl_xor_sync(0xffffffffu, ar, 2);
+      if ((lane & 3) == 0) {
+        jm[(warp * 3 + 0) * MT + r] = m[hh];
+        jm[(warp * 3 + 1) * MT + r] = ar;
+        jm[(warp * 3 + 2) * MT + r] = a;
       }
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+        *reinterpret_cast<float2*>(jo + (warp * MT + r) * DP + n * 8 + qc) =
+            make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
     }
     __syncthreads();
     const int part = part_of_piece(x);
@@ -506,8 +488,8 @@ int launch_paged(PagedArgs& p, char* ws, int sms, cudaStream_t st) {
     if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
     kern<<<grid, kWideThreads, smem, st>>>(p);
   } else {
-    auto kern = attn_paged_kernel<DT, DP, MT>;
-    constexpr int smem = PagedSmem<DP, MT>::kBytes;
+    auto kern = attn_paged_kernel<DT, DP>;
+    constexpr int smem = PagedSmem<DP>::kBytes;
     if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
     kern<<<grid, kWarps * 32, smem, st>>>(p);
   }
@@ -526,15 +508,17 @@ int launch_paged(PagedArgs& p, char* ws, int sms, cudaStream_t st) {
              : THD_ERR_CUDA;
 }
 
+// Tiles of 16 rows where no sequence has more, else of 128.  120000 keys of 16 sequences, 32 + 8 heads of 128,
+// bf16, in us: 16 rows 89 narrow; 20 rows 94 wide, against 124 in narrow tiles of 32; 64 rows 98, against 229 in
+// two such tiles.  Heads of 64 in fp16: 32 rows 72 and 70, 36 rows 73 and 117.  Wide tiles of 4 rows (a
+// decoding batch called without the hint) cost 327 where narrow ones cost 317.
 template <typename DT>
 int launch_paged_of(PagedArgs& p, long long row_hint, char* ws, int sms, cudaStream_t st) {
   if (p.d > 64) {
-    if (row_hint <= 16) return launch_paged<DT, 128, 16>(p, ws, sms, st);
-    if (row_hint <= 32) return launch_paged<DT, 128, 32>(p, ws, sms, st);
+    if (row_hint <= kNarrowRows) return launch_paged<DT, 128, kNarrowRows>(p, ws, sms, st);
     return launch_paged<DT, 128, kWideRows>(p, ws, sms, st);
   }
-  if (row_hint <= 16) return launch_paged<DT, 64, 16>(p, ws, sms, st);
-  if (row_hint <= 32) return launch_paged<DT, 64, 32>(p, ws, sms, st);
+  if (row_hint <= kNarrowRows) return launch_paged<DT, 64, kNarrowRows>(p, ws, sms, st);
   return launch_paged<DT, 64, kWideRows>(p, ws, sms, st);
 }
 
