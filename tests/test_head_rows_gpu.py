@@ -73,6 +73,15 @@ CASES = [
     ([7, 7], 1, 17, 4, 96, 96, BF16, False, True, False, False, True),
     ([4, 12], 0, 2, 0, 112, 64, FP16, True, False, False, True, False),
     ([1] * 40 + [0] * 37 + [3] * 5, 2, 4, 2, 32, 0, BF16, True, False, False, False, False),
+    # many heads: items of one row each
+    ([5, 0, 9], 4, 32, 8, 128, 128, BF16, True, False, True, False, False),
+    ([11, 6], 0, 33, 16, 112, 64, FP16, True, True, False, True, True),
+    ([7, 3, 0, 0, 2], 2, 32, 32, 64, 48, BF16, True, False, False, False, True),
+    ([40], 0, 48, 24, 32, 32, FP16, False, True, False, False, False),
+    ([9], 3, 96, 64, 16, 16, BF16, True, False, True, False, False),
+    # few heads: rows of several sequences, and of none, in one item
+    ([1, 2, 1, 0, 3, 1, 1, 30], 3, 1, 1, 128, 128, BF16, True, False, False, False, True),
+    ([2] * 70, 1, 2, 1, 64, 32, FP16, True, True, True, False, False),
 ]
 
 
@@ -211,6 +220,9 @@ APPENDS = [
     ([13, 0, 7], [9, 0, 21], 3, 8, 4, 4, 64, 64, FP16, True, True, True, True, True),
     ([3, 500], [20, 5], 2, 24, 6, 3, 80, 32, BF16, True, False, True, False, False),
     ([1, 2, 3], [4, 5, 6], 0, 7, 0, 2, 96, 0, FP16, False, False, False, False, True),
+    ([6, 40, 0], [3, 1, 12], 2, 16, 32, 8, 128, 128, BF16, True, False, True, False, False),
+    ([6, 40], [9, 8], 0, 8, 16, 16, 64, 32, FP16, True, True, False, True, True),
+    ([5, 1, 90], [1, 30, 2], 3, 4, 1, 1, 128, 128, BF16, True, False, False, True, False),
 ]
 
 

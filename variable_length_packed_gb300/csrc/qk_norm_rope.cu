@@ -54,6 +54,9 @@ struct RowArgs {
   int q_items, k_items;      // blocks of heads per row
   int row_items;             // of all kinds
   unsigned run;              // items of a warp
+  // few heads: rows of an item and items of each kind
+  int q_rows, k_rows, v_rows;
+  unsigned q_total, k_total, v_total;
   // cache
   void* k_cache;
   void* v_cache;
@@ -67,6 +70,10 @@ constexpr int kRowPasses = 4;     // 32 / lanes-per-head heads in each
 constexpr int kRowStages = 2;     // the item worked on and one on the way
 constexpr int kRowBlocksPerSm = 4;
 constexpr int kRowRun = 6;        // items of a warp at most
+// Per cent of the lanes at work below which items take whole rows (few_heads_kernel).  Share of the copy
+// bandwidth, items of one row against whole rows, heads of 128, normed: 4 + 4 heads (25 %) 44 and 52,
+// 8 + 1 (28 %) 49 and 54, 8 + 2 (31 %) 54 and 53, 16 + 2 (56 %) 79 and 57.
+constexpr int kFewShare = 30;
 
 // Two fp32 values in one 64-bit register: multiplied and added by one instruction.
 typedef unsigned long long f2;
@@ -484,6 +491,188 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowBlocksPerSm) head_rows_ker
   copy_wait<0>();
 }
 
+// ---------------------------------------------------------------------------- few heads
+// Where a row's heads would leave most lanes of an item idle (a model split over many GPUs, keys of
+// one or two heads), an item takes as many whole rows as fit, and each lane group finds its row itself.
+
+// The rows and heads of a lane's passes: pair i kPerPass + group of the item's (row, head) pairs.
+template <int kPasses>
+struct LaneRows {
+  int tok[kPasses], head[kPasses];   // row of the item (or -1: nothing), head
+  int seq[kPasses];                  // sequence of the row, -1: none
+  long long pos[kPasses];            // place in it
+
+  template <int LPH>
+  __device__ __forceinline__ void find(const RowArgs& p, int heads, int rows, int block, unsigned t0, bool mine) {
+    constexpr int kPerPass = 32 / LPH;
+    const int group = (threadIdx.x & 31) / LPH;
+    const long long end = min((long long)p.T, (long long)t0 + rows);
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int pair = i * kPerPass + group;
+      tok[i] = rows > 1 ? pair / heads : 0;
+      head[i] = rows > 1 ? pair - tok[i] * heads : block * (kPasses * kPerPass) + pair;
+      if (!mine || tok[i] >= rows || head[i] >= heads || t0 + tok[i] >= end) tok[i] = -1;
+      seq[i] = -1;
+      pos[i] = 0;
+    }
+    for (long long t = t0; t < end;) {   // once for each stretch of rows of one sequence, or of none
+      const RowSpan span = find_span(p.cu, p.padded, p.B, (int)t);
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const long long row = (long long)t0 + tok[i];
+        if (span.seq >= 0 && tok[i] >= 0 && row >= t && row < span.to) {
+          seq[i] = span.seq;
+          pos[i] = row - span.from;
+        }
+      }
+      t = span.to;
+    }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      if (seq[i] >= 0 && p.offsets) pos[i] += p.offsets[seq[i]];
+  }
+};
+
+// A lane's angles, read at once; turned back where sin_sign is -1.
+__device__ __forceinline__ void load_angles(f2* c, f2* s, const RowArgs& p, int slot, long long pos) {
+  const long long row = pos < 0 ? 0 : (pos >= p.rope_rows ? p.rope_rows - 1 : pos);
+  const int half = p.rotary >> 1;
+  const long long at[2] = {row * half + (p.interleaved ? 4 * slot : 8 * slot),
+                           row * half + (p.interleaved ? 4 * (slot + (p.rotary >> 4)) : 8 * slot + 4)};
+  const f2 sign = pair(p.sin_sign, p.sin_sign);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(p.cos + at[i]);
+    const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(p.sin + at[i]);
+    c[2 * i] = a.x, c[2 * i + 1] = a.y;
+    s[2 * i] = mul2(b.x, sign), s[2 * i + 1] = mul2(b.y, sign);
+  }
+}
+
+// Turns a lane's two chunks.
+__device__ __forceinline__ void turn_chunks(f2* x0, f2* x1, const f2* c, const f2* s, int interleaved) {
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 cl = split(c[i >> 1]), sl = split(s[i >> 1]), ch = split(c[2 + (i >> 1)]), sh = split(s[2 + (i >> 1)]);
+      const float c0 = i & 1 ? cl.y : cl.x, s0 = i & 1 ? sl.y : sl.x, c1 = i & 1 ? ch.y : ch.x, s1 = i & 1 ? sh.y : sh.x;
+      x0[i] = fma2(swapped(x0[i]), pair(-s0, s0), mul2(x0[i], pair(c0, c0)));
+      x1[i] = fma2(swapped(x1[i]), pair(-s1, s1), mul2(x1[i], pair(c1, c1)));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f2 y0 = fma2(x1[i], negated(s[i]), mul2(x0[i], c[i]));
+      x1[i] = fma2(x0[i], s[i], mul2(x1[i], c[i]));
+      x0[i] = y0;
+    }
+  }
+}
+
+// a warp takes one item: queries' first, then keys', then values'
+template <typename DT, int LPH, bool kCache>
+__global__ void __launch_bounds__(kRowWarps * 32, 5) few_heads_kernel(const RowArgs p) {
+  const int lane = threadIdx.x & 31;
+  unsigned item = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  int kind = 0, rows = p.q_rows, blocks = p.q_items;
+  const HeadRows* h = &p.q;
+  if (item >= p.q_total) {
+    item -= p.q_total;
+    kind = 1, rows = p.k_rows, blocks = p.k_items, h = &p.k;
+    if (item >= p.k_total) {
+      item -= p.k_total;
+      if (!kCache || item >= p.v_total) return;
+      kind = 2, rows = p.v_rows, blocks = (int)(p.v_total / (unsigned)((p.T + rows - 1) / rows)), h = &p.v;
+    }
+  }
+  const unsigned first = item / (unsigned)blocks;
+  const int block = (int)(item - first * (unsigned)blocks);
+  const unsigned t0 = first * (unsigned)rows;
+  const int slot = lane % LPH;
+  const bool mine = slot < (p.d >> 4);
+  int c0, c1;
+  lane_chunks(slot, p.rotary, c0, c1);
+  LaneRows<kRowPasses> at;
+  at.find<LPH>(p, h->heads, rows, block, t0, mine);
+  uint4 v[kRowPasses][2];
+  DT* dst[kRowPasses];
+#pragma unroll
+  for (int i = 0; i < kRowPasses; ++i) {
+    const long long t = (long long)t0 + at.tok[i];
+    v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+    dst[i] = nullptr;
+    if (at.tok[i] < 0) continue;
+    if (kCache && kind != 0) {   // a row without a page is not written
+      const long long page_at = at.pos[i] / p.page_size;
+      int page = -1;
+      if (at.seq[i] >= 0 && at.pos[i] >= 0 && page_at < p.max_pages)
+        page = p.table[(long long)at.seq[i] * p.table_stride + page_at];
+      if (page < 0 || page >= p.num_pages) continue;
+      const long long in = at.pos[i] - page_at * p.page_size;
+      dst[i] = kind == 1 ? static_cast<DT*>(p.k_cache) + page * p.k_page + in * p.k_token + at.head[i] * p.k_head
+                         : static_cast<DT*>(p.v_cache) + page * p.v_page + in * p.v_token + at.head[i] * p.v_head;
+    } else {
+      dst[i] = static_cast<DT*>(h->dst) + t * h->dst_stride + (long long)at.head[i] * p.d;
+    }
+    if (at.seq[i] >= 0) {
+      const DT* src = static_cast<const DT*>(h->src) + t * h->src_stride + (long long)at.head[i] * p.d;
+      v[i][0] = *reinterpret_cast<const uint4*>(src + 8 * c0);
+      v[i][1] = *reinterpret_cast<const uint4*>(src + 8 * c1);
+    }
+  }
+  const bool norm = kind != 2 && h->weight != nullptr;
+  const bool rot = kind != 2 && slot < (p.rotary >> 4);
+  if (norm || (kind != 2 && p.rotary > 0)) {
+    f2 w0[4], w1[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w0[e] = w1[e] = pair(1.f, 1.f);
+    if (norm && mine) {
+      load_weight<DT>(h->weight, p.weight_fp32, c0, w0);
+      load_weight<DT>(h->weight, p.weight_fp32, c1, w1);
+    }
+#pragma unroll
+    for (int i = 0; i < kRowPasses; ++i) {
+      f2 x0[4], x1[4], c[4], s[4];
+      const bool row = at.tok[i] >= 0 && at.seq[i] >= 0;
+      if (row && rot)
+        load_angles(c, s, p, slot, kCache && p.positions ? (long long)p.positions[(long long)t0 + at.tok[i]] : at.pos[i]);
+      unpack4<DT>(v[i][0], x0);
+      unpack4<DT>(v[i][1], x1);
+      if (norm) {
+        f2 sq = mul2(x0[0], x0[0]), sq1 = mul2(x1[0], x1[0]);
+#pragma unroll
+        for (int e = 1; e < 4; ++e) {
+          sq = fma2(x0[e], x0[e], sq);
+          sq1 = fma2(x1[e], x1[e], sq1);
+        }
+        const float2 sqs = split(add2(sq, sq1));
+        float sum = sqs.x + sqs.y;
+#pragma unroll
+        for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float r = rsqrtf(sum * p.inv_d + p.eps);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x0[e] = mul2(mul2(x0[e], w0[e]), pair(r, r));
+          x1[e] = mul2(mul2(x1[e], w1[e]), pair(r, r));
+        }
+      }
+      if (row && rot) turn_chunks(x0, x1, c, s, p.interleaved);
+      if (row) {
+        v[i][0] = pack4<DT>(x0);
+        v[i][1] = pack4<DT>(x1);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRowPasses; ++i) {
+    if (dst[i]) {
+      *reinterpret_cast<uint4*>(dst[i] + 8 * c0) = v[i][0];
+      *reinterpret_cast<uint4*>(dst[i] + 8 * c1) = v[i][1];
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------- backward
 struct NormBwdArgs {
   RowArgs a;                 // src: x, dst: dx
@@ -497,9 +686,42 @@ struct NormBwdArgs {
 constexpr int kBwdPasses = 2;
 constexpr int kBwdWarps = 4;
 constexpr int kBwdStages = 3;
+// As kFewShare: 4 + 1 heads (31 %) 35 and 58, 8 + 1 (56 %) 58 and 63, 8 + 2 (62 %) 64 and 63, 16 + 2 (75 %) 75 and 65.
+constexpr int kBwdFewShare = 60;
 constexpr int kBwdRun = 6;        // items of a warp, more where that would give over kBwdMaxBlocks blocks
 constexpr int kBwdBlocksPerSm = 3;
 constexpr int kBwdMaxBlocks = 4096;
+
+// The block's share of dw: over the warp's heads, then over the warps.
+template <int LPH>
+__device__ __forceinline__ void leave_weight_share(const f2* dw0, const f2* dw1, float (*sum)[128], int c0, int c1,
+                                                   bool mine, float* dst, int d) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float2 a = split(dw0[e]), c = split(dw1[e]);
+#pragma unroll
+    for (int o = LPH; o < 32; o <<= 1) {
+      a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+      a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+      c.x += __shfl_xor_sync(0xffffffffu, c.x, o);
+      c.y += __shfl_xor_sync(0xffffffffu, c.y, o);
+    }
+    if (lane < LPH && mine) {
+      sum[warp][8 * c0 + 2 * e] = a.x;
+      sum[warp][8 * c0 + 2 * e + 1] = a.y;
+      sum[warp][8 * c1 + 2 * e] = c.x;
+      sum[warp][8 * c1 + 2 * e + 1] = c.y;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < d; i += blockDim.x) {
+    float total = 0.f;
+#pragma unroll
+    for (int k = 0; k < kBwdWarps; ++k) total += sum[k][i];
+    dst[i] = total;
+  }
+}
 
 // A block works on one kind (queries or keys), so that a lane keeps one sum for dw.  Copies ahead as
 // the forward does: gradients in chunks 0 and 1 of a stage, inputs in 2 and 3.
@@ -680,33 +902,109 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdBlocksPerSm) head_rows_bwd
   }
   copy_wait<0>();
   if (!norm) return;
-  // the block's share of dw: over the warp's heads, then over the warps
-  __syncthreads();
-  float(*sum)[128] = reinterpret_cast<float(*)[128]>(smem);
+  __syncthreads();   // the ring is read no more
+  leave_weight_share<LPH>(dw0, dw1, reinterpret_cast<float(*)[128]>(smem), c0, c1, mine,
+                          b.partial + (long long)blockIdx.x * p.d, p.d);
+}
+
+// Few heads, as few_heads_kernel; a block works on one kind and a warp on a run of items.
+template <typename DT, int LPH>
+__global__ void __launch_bounds__(kBwdWarps * 32) few_heads_bwd_kernel(const NormBwdArgs b) {
+  const RowArgs& p = b.a;
+  __shared__ float sum[kBwdWarps][128];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool is_q = (int)blockIdx.x < b.q_blocks;
+  const HeadRows& h = is_q ? p.q : p.k;
+  const DT* grad = static_cast<const DT*>(is_q ? b.gq : b.gk);
+  const int rows = is_q ? p.q_rows : p.k_rows;
+  const unsigned blocks = (unsigned)(is_q ? p.q_items : p.k_items);
+  const int slot = lane % LPH;
+  const bool mine = slot < (p.d >> 4);
+  const bool norm = h.weight != nullptr;
+  const bool rot = slot < (p.rotary >> 4);
+  int c0, c1;
+  lane_chunks(slot, p.rotary, c0, c1);
+  f2 w0[4], w1[4], dw0[4], dw1[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float2 a = split(dw0[e]), c = split(dw1[e]);
+  for (int e = 0; e < 4; ++e) w0[e] = w1[e] = dw0[e] = dw1[e] = 0ull;
+  if (norm && mine) {
+    load_weight<DT>(h.weight, p.weight_fp32, c0, w0);
+    load_weight<DT>(h.weight, p.weight_fp32, c1, w1);
+  }
+  // row_items of the walk: blocks of heads of a group of rows
+  for (ItemWalk now(is_q ? p.q_total : p.k_total, blocks, (is_q ? blockIdx.x : blockIdx.x - b.q_blocks) * kBwdWarps + warp,
+                    b.run);
+       now.more(); now.next()) {
+    const unsigned t0 = now.t * (unsigned)rows;
+    LaneRows<kBwdPasses> at;
+    at.find<LPH>(p, h.heads, rows, (int)now.part, t0, mine);
+    uint4 g[kBwdPasses][2], v[kBwdPasses][2];
 #pragma unroll
-    for (int o = LPH; o < 32; o <<= 1) {
-      a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
-      a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
-      c.x += __shfl_xor_sync(0xffffffffu, c.x, o);
-      c.y += __shfl_xor_sync(0xffffffffu, c.y, o);
+    for (int i = 0; i < kBwdPasses; ++i) {
+      g[i][0] = g[i][1] = v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (at.tok[i] >= 0 && at.seq[i] >= 0) {
+        const long long t = (long long)t0 + at.tok[i], head = (long long)at.head[i] * p.d;
+        const DT* gsrc = grad + t * h.heads * p.d + head;
+        g[i][0] = *reinterpret_cast<const uint4*>(gsrc + 8 * c0);
+        g[i][1] = *reinterpret_cast<const uint4*>(gsrc + 8 * c1);
+        if (norm) {
+          const DT* src = static_cast<const DT*>(h.src) + t * h.src_stride + head;
+          v[i][0] = *reinterpret_cast<const uint4*>(src + 8 * c0);
+          v[i][1] = *reinterpret_cast<const uint4*>(src + 8 * c1);
+        }
+      }
     }
-    if (lane < LPH && mine) {
-      sum[warp][8 * c0 + 2 * e] = a.x;
-      sum[warp][8 * c0 + 2 * e + 1] = a.y;
-      sum[warp][8 * c1 + 2 * e] = c.x;
-      sum[warp][8 * c1 + 2 * e + 1] = c.y;
+#pragma unroll
+    for (int i = 0; i < kBwdPasses; ++i) {
+      const bool row = at.tok[i] >= 0 && at.seq[i] >= 0;
+      f2 h0[4], h1[4];
+      unpack4<DT>(g[i][0], h0);
+      unpack4<DT>(g[i][1], h1);
+      if (row && rot) {
+        f2 c[4], s[4];
+        load_angles(c, s, p, slot, at.pos[i]);   // turned back (sin_sign)
+        turn_chunks(h0, h1, c, s, p.interleaved);
+      }
+      if (norm) {
+        f2 x0[4], x1[4];
+        unpack4<DT>(v[i][0], x0);
+        unpack4<DT>(v[i][1], x1);
+        f2 sq0 = 0ull, sq1 = 0ull, dot0 = 0ull, dot1 = 0ull;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sq0 = fma2(x0[e], x0[e], sq0);
+          sq1 = fma2(x1[e], x1[e], sq1);
+          dot0 = fma2(mul2(h0[e], w0[e]), x0[e], dot0);
+          dot1 = fma2(mul2(h1[e], w1[e]), x1[e], dot1);
+        }
+        const float2 sqs = split(add2(sq0, sq1)), dots = split(add2(dot0, dot1));
+        float ss = sqs.x + sqs.y, along = dots.x + dots.y;
+#pragma unroll
+        for (int o = LPH / 2; o > 0; o >>= 1) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          along += __shfl_xor_sync(0xffffffffu, along, o);
+        }
+        // where there is no row there is nothing, and with eps = 0 its 1 / rms has no value; lanes past the
+        // head's chunks hold zeros
+        const float r = row ? rsqrtf(ss * p.inv_d + p.eps) : 0.f;
+        const float m = -(along * p.inv_d * r) * r * r;   // in an order that stays in range for tiny heads
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const f2 hr0 = mul2(h0[e], pair(r, r)), hr1 = mul2(h1[e], pair(r, r));
+          dw0[e] = fma2(hr0, x0[e], dw0[e]);
+          dw1[e] = fma2(hr1, x1[e], dw1[e]);
+          h0[e] = fma2(hr0, w0[e], mul2(x0[e], pair(m, m)));
+          h1[e] = fma2(hr1, w1[e], mul2(x1[e], pair(m, m)));
+        }
+      }
+      if (at.tok[i] >= 0) {
+        DT* dst = static_cast<DT*>(h.dst) + ((long long)t0 + at.tok[i]) * h.dst_stride + (long long)at.head[i] * p.d;
+        *reinterpret_cast<uint4*>(dst + 8 * c0) = row ? pack4<DT>(h0) : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(dst + 8 * c1) = row ? pack4<DT>(h1) : make_uint4(0u, 0u, 0u, 0u);
+      }
     }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.d; i += blockDim.x) {
-    float total = 0.f;
-#pragma unroll
-    for (int k = 0; k < kBwdWarps; ++k) total += sum[k][i];
-    b.partial[(long long)blockIdx.x * p.d + i] = total;
-  }
+  if (norm) leave_weight_share<LPH>(dw0, dw1, sum, c0, c1, mine, b.partial + (long long)blockIdx.x * p.d, p.d);
 }
 
 // dw = the blocks' shares summed in a fixed order; a block takes 8 columns of one kind.
@@ -794,6 +1092,34 @@ int launch_rows_at(const RowArgs& p, unsigned grid, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
 }
 
+template <typename DT, int LPH, bool kCache>
+int launch_few_at(const RowArgs& p, unsigned grid, cudaStream_t st) {
+  few_heads_kernel<DT, LPH, kCache><<<grid, kRowWarps * 32, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
+}
+
+template <typename DT, bool kCache>
+int launch_few_of(const RowArgs& p, unsigned grid, cudaStream_t st) {
+  switch (lanes_per_head(p.d)) {
+    case 1: return launch_few_at<DT, 1, kCache>(p, grid, st);
+    case 2: return launch_few_at<DT, 2, kCache>(p, grid, st);
+    case 4: return launch_few_at<DT, 4, kCache>(p, grid, st);
+    default: return launch_few_at<DT, 8, kCache>(p, grid, st);
+  }
+}
+
+// Whether items of whole rows pay: kPasses * 32 / lanes-per-head pairs (`per`) fit one.
+bool few_heads(const RowArgs& p, int per, int share) {
+  const int items = blocks_of_heads(p.q.heads, per) + blocks_of_heads(p.k.heads, per) + blocks_of_heads(p.v.heads, per);
+  return 100 * (p.q.heads + p.k.heads + p.v.heads) < share * per * items;
+}
+
+// Rows of an item and items of a kind of `heads` heads.
+void rows_of_items(int heads, int per, int T, int& rows, long long& total) {
+  rows = heads > 0 && per / heads > 1 ? per / heads : 1;
+  total = heads > 0 ? ((long long)T + rows - 1) / rows * blocks_of_heads(heads, per) : 0;
+}
+
 template <typename DT, bool kCache>
 int launch_rows_of(const RowArgs& p, unsigned grid, cudaStream_t st) {
   switch (lanes_per_head(p.d)) {
@@ -811,6 +1137,17 @@ int launch_rows(RowArgs& p, int dtype, cudaStream_t st) {
   p.k_items = blocks_of_heads(p.k.heads, per);
   const long long row_items = (long long)p.q_items + p.k_items + blocks_of_heads(p.v.heads, per);
   if (row_items == 0) return THD_OK;
+  if (few_heads(p, per, kFewShare)) {
+    long long qt, kt, vt;
+    rows_of_items(p.q.heads, per, p.T, p.q_rows, qt);
+    rows_of_items(p.k.heads, per, p.T, p.k_rows, kt);
+    rows_of_items(p.v.heads, per, p.T, p.v_rows, vt);
+    if (qt + kt + vt >= (1ll << 31)) return THD_ERR_UNSUPPORTED;   // item numbers are 32-bit
+    p.q_total = (unsigned)qt, p.k_total = (unsigned)kt, p.v_total = (unsigned)vt;
+    const unsigned grid = (unsigned)((qt + kt + vt + kRowWarps - 1) / kRowWarps);
+    return dtype == THD_BF16 ? launch_few_of<__nv_bfloat16, kCache>(p, grid, st)
+                             : launch_few_of<__half, kCache>(p, grid, st);
+  }
   const long long items = row_items * p.T;
   if (items >= (1ll << 31)) return THD_ERR_UNSUPPORTED;   // item numbers are 32-bit
   p.row_items = (int)row_items;
@@ -825,7 +1162,11 @@ int launch_rows(RowArgs& p, int dtype, cudaStream_t st) {
 }
 
 template <typename DT, int LPH>
-int launch_bwd_at(const NormBwdArgs& b, unsigned grid, cudaStream_t st) {
+int launch_bwd_at(const NormBwdArgs& b, bool few, unsigned grid, cudaStream_t st) {
+  if (few) {
+    few_heads_bwd_kernel<DT, LPH><<<grid, kBwdWarps * 32, 0, st>>>(b);
+    return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
+  }
   static SmemGrant grant;
   constexpr size_t smem = kBwdWarps * kBwdStages * sizeof(RowStage<kBwdPasses, 4, LPH>);
   if (!grant.ask(head_rows_bwd_kernel<DT, LPH>, smem)) return THD_ERR_CUDA;
@@ -834,12 +1175,12 @@ int launch_bwd_at(const NormBwdArgs& b, unsigned grid, cudaStream_t st) {
 }
 
 template <typename DT>
-int launch_bwd_of(const NormBwdArgs& b, unsigned grid, cudaStream_t st) {
+int launch_bwd_of(const NormBwdArgs& b, bool few, unsigned grid, cudaStream_t st) {
   switch (lanes_per_head(b.a.d)) {
-    case 1: return launch_bwd_at<DT, 1>(b, grid, st);
-    case 2: return launch_bwd_at<DT, 2>(b, grid, st);
-    case 4: return launch_bwd_at<DT, 4>(b, grid, st);
-    default: return launch_bwd_at<DT, 8>(b, grid, st);
+    case 1: return launch_bwd_at<DT, 1>(b, few, grid, st);
+    case 2: return launch_bwd_at<DT, 2>(b, few, grid, st);
+    case 4: return launch_bwd_at<DT, 4>(b, few, grid, st);
+    default: return launch_bwd_at<DT, 8>(b, few, grid, st);
   }
 }
 
@@ -924,7 +1265,13 @@ int thd_qk_norm_rope_bwd(const void* grad_q, const void* grad_k, const void* q, 
   p.k = HeadRows{k, dk, k_weight, k_stride, dk_stride, num_heads_kv};
   p.q_items = blocks_of_heads(num_heads_q, per);
   p.k_items = blocks_of_heads(num_heads_kv, per);
-  const long long qi = (long long)p.q_items * total_tokens, ki = (long long)p.k_items * total_tokens;
+  const bool few = few_heads(p, per, kBwdFewShare);
+  long long qi = (long long)p.q_items * total_tokens, ki = (long long)p.k_items * total_tokens;
+  if (few) {
+    rows_of_items(num_heads_q, per, total_tokens, p.q_rows, qi);
+    rows_of_items(num_heads_kv, per, total_tokens, p.k_rows, ki);
+    p.sin_sign = -1.f;
+  }
   if (qi >= (1ll << 31) || ki >= (1ll << 31)) return THD_ERR_UNSUPPORTED;   // item numbers are 32-bit
   // runs as in launch_rows, but of such a length that there are at most kBwdMaxBlocks blocks: each
   // leaves a share of dw to be summed
@@ -935,6 +1282,7 @@ int thd_qk_norm_rope_bwd(const void* grad_q, const void* grad_k, const void* q, 
   if (run < least) run = least;
   const long long per_block = run * kBwdWarps;
   const long long qb = (qi + per_block - 1) / per_block, kb = (ki + per_block - 1) / per_block;
+  p.q_total = (unsigned)qi, p.k_total = (unsigned)ki;
   b.run = (unsigned)run;
   b.a = p;
   b.gq = grad_q;
@@ -943,8 +1291,8 @@ int thd_qk_norm_rope_bwd(const void* grad_q, const void* grad_k, const void* q, 
   b.q_blocks = (int)qb;
   b.k_blocks = (int)kb;
   if (qb + kb > 0) {
-    st = dtype == THD_BF16 ? launch_bwd_of<__nv_bfloat16>(b, (unsigned)(qb + kb), s)
-                           : launch_bwd_of<__half>(b, (unsigned)(qb + kb), s);
+    st = dtype == THD_BF16 ? launch_bwd_of<__nv_bfloat16>(b, few, (unsigned)(qb + kb), s)
+                           : launch_bwd_of<__half>(b, few, (unsigned)(qb + kb), s);
     if (st != THD_OK) return st;
   }
   weight_sum_kernel<<<dim3(head_dim / 8, 2), kSumRows * 8, 0, s>>>(b.partial, b.q_blocks, b.k_blocks, head_dim,
