@@ -449,7 +449,8 @@ size_t thd_attn_paged_workspace_size(int head_dim);
  * lse          device fp32 [Hq, T] or NULL, as in thd_attn_fwd.
  * head_dim     a multiple of 8 in [8, 128].
  * workspace    device, >= thd_attn_paged_workspace_size(head_dim) bytes, 16-byte aligned,
- *              uninitialised; not shared by calls that overlap on the GPU.
+ *              uninitialised; not shared by calls that overlap on the GPU.  The call's
+ *              status word (THD_STATUS_* bits) is at byte 8 when it has ended.
  * Nothing is read from the device on the host, so a captured call may be replayed
  * with other lengths, tables and masks in the same buffers.
  * Errors: THD_ERR_ARG, THD_ERR_UNSUPPORTED, THD_ERR_WORKSPACE, THD_ERR_CUDA.
@@ -464,8 +465,8 @@ int thd_attn_paged(const void* q, const void* k_cache, const void* v_cache, cons
 /*
  * thd_set_wait_limit_ns — the time limit of one pipeline wait inside the
  * attention kernels (forward, windowed forward, no-allocation forward,
- * backward), for calls made after it on any host thread; returns the previous
- * limit.  0 restores the default of 2 s.
+ * backward, and thd_attn_paged where it waits), for calls made after it on any
+ * host thread; returns the previous limit.  0 restores the default of 2 s.
  *
  * No counterpart on the pages: it belongs to the library's failure handling.
  * Every wait of a kernel on its own pipeline (a copy landing, an MMA
@@ -481,8 +482,8 @@ uint64_t thd_set_wait_limit_ns(uint64_t ns);
 /*
  * thd_set_wait_injection — test setting of the failure path: with enable != 0,
  * every CTA of the attention kernels (forward, windowed forward, no-allocation
- * forward, backward) called after it makes one wait on a barrier that nothing
- * completes before the CTA's end.  That wait runs out after the limit of
+ * forward, backward, thd_attn_paged with tiles of 128 rows) called after it
+ * makes one wait on a barrier that nothing completes before the CTA's end.  That wait runs out after the limit of
  * thd_set_wait_limit_ns whatever the timing of the rest of the pipeline, so the
  * call sets THD_STATUS_WAIT_TIMEOUT and its CTAs leave through the failure path
  * (with their copies and MMAs in flight) every time; its output is unspecified.

@@ -572,7 +572,7 @@ __device__ __forceinline__ void turn_chunks(f2* x0, f2* x1, const f2* c, const f
 
 // a warp takes one item: queries' first, then keys', then values'
 template <typename DT, int LPH, bool kCache>
-__global__ void __launch_bounds__(kRowWarps * 32, 5) few_heads_kernel(const RowArgs p) {
+__global__ void __launch_bounds__(kRowWarps * 32, kCache ? 4 : 5) few_heads_kernel(const RowArgs p) {
   const int lane = threadIdx.x & 31;
   unsigned item = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
   int kind = 0, rows = p.q_rows, blocks = p.q_items;
