@@ -146,6 +146,9 @@ def test_masks_that_leave_a_row_empty():
     x["tree"][4] = 1 << 60            # bits past the new tokens show nothing
     check(x, run(x))
     assert torch.all(run(x)[0][3] == 0) and torch.all(run(x)[0][4] == 0)
+    x = make([5, 70], [9, 71], 4, 4, 2, 64, BF16, words=2)   # fewer keys than drafted tokens
+    for hint in (1, 71):
+        check(x, run(x, max_seqlen_q=hint))
 
 
 def test_many_sequences_and_a_wrong_hint():

@@ -17,6 +17,7 @@ from . import THD_BF16, THD_FP16, THD_OK, ThdError, _check_metadata, load_librar
 # the current stream's handle without the Stream object around it (2 us a call)
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_F32 = torch.float32
 _Places = ctypes.c_int64 * 6
 _CODES = {torch.bfloat16: THD_BF16, torch.float16: THD_FP16}
 
@@ -64,8 +65,11 @@ def _whole(t, name, device, dtype, shape=None):
 
 def _rows(t, name, device, dtype, shape=None):
     """Row stride of a [T, heads, head_dim] tensor whose rows are whole but may lie apart."""
-    if type(t) is not torch.Tensor or t.get_device() != device.index:
-        _on(t, name, device)
+    if (type(t) is torch.Tensor and t.get_device() == device.index and t.dtype is dtype and t.is_contiguous()
+            and (t.shape == shape if shape is not None else t.dim() == 3)):   # the usual case in few steps
+        _, h, d = t.shape
+        return h * d
+    _on(t, name, device)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, heads, head_dim]")
     if t.dtype is not dtype:
@@ -117,6 +121,12 @@ def _tables(cos, sin, device, d):
         return 0, 0
     if cos is None or sin is None:
         raise ValueError("rope_cos and rope_sin come together")
+    if type(cos) is torch.Tensor is type(sin):   # the usual case in few steps
+        shape, index = cos.shape, device.index
+        if (cos.dtype is _F32 is sin.dtype and sin.shape == shape and len(shape) == 2 and shape[0] > 0
+                and 2 * shape[1] <= d and cos.get_device() == index == sin.get_device() and cos.is_contiguous()
+                and sin.is_contiguous()):
+            return shape[0], 2 * shape[1]
     _whole(cos, "rope_cos", device, torch.float32)
     _whole(sin, "rope_sin", device, torch.float32, cos.shape)
     if cos.dim() != 2 or 2 * cos.shape[1] > d:
@@ -128,9 +138,14 @@ def _tables(cos, sin, device, d):
 
 def _weights(wq, wk, device, d, dtype):
     """1 if the norm weights are fp32, 0 if they are of the rows' dtype."""
-    fp32 = 0
     if wq is None and wk is None:
-        return fp32
+        return 0
+    if type(wq) is torch.Tensor is type(wk):   # the usual case in few steps
+        kind, index = wq.dtype, device.index
+        if (kind is wk.dtype and (kind is dtype or kind is _F32) and wq.shape == (d,) == wk.shape
+                and wq.get_device() == index == wk.get_device() and wq.is_contiguous() and wk.is_contiguous()):
+            return 1 if kind is _F32 else 0
+    fp32 = 0
     for name, w in (("q_weight", wq), ("k_weight", wk)):
         if w is not None:
             if not isinstance(w, torch.Tensor) or (w.dtype is not dtype and w.dtype is not torch.float32):
@@ -258,6 +273,16 @@ def thd_qk_norm_rope_bwd(grad_q, grad_k, q, k, cu_seqlens, rope_cos=None, rope_s
 
 def _caches(k_cache, v_cache, device, dtype, page_table, batch_size, writes):
     """Strides of the two caches (ctypes int64[6]: page, token, head of each), and the table's."""
+    if (type(k_cache) is torch.Tensor is type(v_cache) and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and k_cache.dtype is dtype is v_cache.dtype and type(page_table) is torch.Tensor
+            and page_table.is_contiguous() and page_table.dtype is torch.int32
+            and k_cache.get_device() == device.index == v_cache.get_device() == page_table.get_device()):
+        # the usual case in few steps
+        shape, table = k_cache.shape, page_table.shape
+        if len(shape) == 4 and shape == v_cache.shape and len(table) == 2 and table[0] >= batch_size:
+            _, size, heads, d = shape
+            page = size * heads * d
+            return shape, _Places(page, heads * d, d, page, heads * d, d), table[1], table[1]
     shape = k_cache.shape if isinstance(k_cache, torch.Tensor) else None
     places = []
     for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
