@@ -234,13 +234,14 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
             if (!(hi >> c & 1)) sr[32 + c] = __float_as_uint(-INFINITY);
           }
         }
-        float mx0 = -INFINITY, mx1 = -INFINITY;
+        float mx[4] = {m_run, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          mx0 = fmax3f(mx0, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-          mx1 = fmax3f(mx1, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
+        for (int c = 0; c < 64; c += 8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx[k] = fmax3f(mx[k], __uint_as_float(sr[c + 2 * k]), __uint_as_float(sr[c + 2 * k + 1]));
         }
-        const float m_new = fmax3f(m_run, mx0, mx1);
+        const float m_new = fmax3f(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
         // the maximum moves only when it grows by more than 8 (log2): weights stay below 2^8 and the
         // output is seldom rescaled
         const bool need = (m_new - m_run) * sl2 > 8.f;   // false while both are -inf
@@ -252,21 +253,22 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
           l_exact *= alpha;
         }
         const float mb = (m_run == -INFINITY ? 0.f : m_run) * sl2;
-        float e0 = 0.f, e1 = 0.f, r0 = 0.f, r1 = 0.f;
+        // sums of the weights and of the weights as rounded, in two chains of pairs each
+        const float2 scale2 = make_float2(sl2, sl2), bias2 = make_float2(-mb, -mb);
+        float2 ex[2], rd[2];
+        ex[0] = ex[1] = rd[0] = rd[1] = make_float2(0.f, 0.f);
         uint32_t pk[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
-          const float a = ex2_approx(fmaf(__uint_as_float(sr[2 * c]), sl2, -mb));
-          const float b = ex2_approx(fmaf(__uint_as_float(sr[2 * c + 1]), sl2, -mb));
-          pk[c] = Tr::put(a, b);
-          e0 += a;
-          e1 += b;
-          const float2 r = Tr::get(pk[c]);
-          r0 += r.x;
-          r1 += r.y;
+          const float2 e =
+              __ffma2_rn(make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), scale2, bias2);
+          const float2 w = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+          pk[c] = Tr::put(w.x, w.y);
+          ex[c & 1] = __fadd2_rn(ex[c & 1], w);
+          Tr::add(pk[c], rd[c & 1].x, rd[c & 1].y);
         }
-        l_exact += e0 + e1;
-        l_run += r0 + r1;
+        l_exact += (ex[0].x + ex[0].y) + (ex[1].x + ex[1].y);
+        l_run += (rd[0].x + rd[0].y) + (rd[1].x + rd[1].y);
         tmem_st32(tS, pk);
         if (i > 0 && __any_sync(0xffffffffu, need)) {
           if (!WIDE_WAIT(&sm.o_full, (n - 1) & 1)) {

@@ -115,6 +115,13 @@ struct Pair16<__nv_bfloat16> {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&v);
   }
+  // a += the pair's first value, b += its second (exact widening, one instruction each)
+  __device__ static __forceinline__ void add(uint32_t x, float& a, float& b) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "add.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(x));
+  }
 };
 template <>
 struct Pair16<__half> {
@@ -125,6 +132,12 @@ struct Pair16<__half> {
   __device__ static __forceinline__ uint32_t put(float a, float b) {
     __half2 v = __floats2half2_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&v);
+  }
+  __device__ static __forceinline__ void add(uint32_t x, float& a, float& b) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "add.rn.f32.f16 %0, l, %0;\n\tadd.rn.f32.f16 %1, h, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(x));
   }
 };
 
