@@ -192,9 +192,11 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
     while (ok && walk.next<kWideRows>(p, x)) {
       const int row = x.row0 + r, tok = row / p.group, hq = x.head * p.group + (row - tok * p.group);
       const bool valid = r < x.rows;
+      // a warp past the tile's rows only keeps step: what its lanes of tensor memory hold reaches no row
+      const bool idle = warp * 32 >= x.rows;
       const uint64_t word0 = tree_word(p, x, valid ? tok : 0);
       float m_run = -INFINITY, l_run = 0.f, l_exact = 0.f;
-      if (x.steps > 0) {
+      if (x.steps > 0 && !idle) {
         const uint4* src = reinterpret_cast<const uint4*>(
             static_cast<const DT*>(p.q) + ((long long)(x.s.q_start + (valid ? tok : 0)) * p.Hq + (valid ? hq : 0)) * p.d);
 #pragma unroll
@@ -211,12 +213,16 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_full);
       }
+      if (x.steps > 0 && lane == 0) mbar_arrive(&sm.q_full);
       for (int i = 0; i < x.steps; ++i, ++n) {
         if (!WIDE_WAIT(&sm.s_full, n & 1)) {
           ok = false;
           break;
+        }
+        if (idle) {
+          if (lane == 0) mbar_arrive(&sm.p_full);
+          continue;
         }
         tc_fence_after();
         uint32_t sr[64];
@@ -293,6 +299,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
         if (lane == 0) mbar_arrive(&sm.p_full);
       }
       if (!ok) break;
+      if (idle) continue;
       // ---- the tile's output, or this piece's share of it ----
       if (x.steps > 0) {
         if (!WIDE_WAIT(&sm.o_full, (n - 1) & 1)) break;
