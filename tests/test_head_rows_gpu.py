@@ -212,6 +212,96 @@ def test_metadata_out_of_order_does_not_fault():
     torch.cuda.synchronize()
 
 
+def test_training_step_through_packed_attention():
+    """Norm and rotation, attention and both backward passes in a row, out of and into fused buffers, against
+    torch autograd of the whole in 64 bits.  Six tensors are rounded to bf16 on the way (heads, weights, output,
+    dS, gradients of the heads, gradients), each by at most 2^-8 of itself; with the steps' relative condition
+    taken as 2: 12 * 2^-8 of the norm."""
+    lens, hq, hkv, d = [40, 1, 23, 0, 70], 4, 2, 64
+    rng, g = np.random.default_rng(5), torch.Generator().manual_seed(5)
+    cu, padded, T = batch(lens, 3, rng)
+    x = torch.randn(T, (hq + 2 * hkv) * d, generator=g).to(BF16).cuda()
+    split = lambda x: [p.unflatten(1, (-1, d)) for p in x.split([hq * d, hkv * d, hkv * d], 1)]
+    q, k, v = split(x)
+    wq, wk = ((1 + 0.2 * torch.randn(d, generator=g)).to(BF16).cuda() for _ in range(2))
+    cos, sin = tables(max(lens), d, 100.0)
+    dout = torch.randn(T, hq, d, generator=g).to(BF16).cuda()
+    c, p, B = ints(cu), ints(padded), len(lens)
+    causal = torch.ones(B, dtype=torch.bool, device="cuda")
+    kw = dict(cu_seqlens_padded=p, batch_size=B, q_weight=wq, k_weight=wk)
+    qr, kr = vlp.thd_qk_norm_rope(q, k, c, cos, sin, **kw)
+    vc = v.contiguous()
+    out, lse = vlp.thd_attn_fwd(qr, kr, vc, c, c, p, p, causal, B, max(lens))
+    gq, gk, gv = vlp.thd_attn_bwd(qr, kr, vc, out, lse, dout, c, c, p, p, causal, B, max(lens))
+    dx = torch.zeros_like(x)
+    parts = split(dx)
+    _, _, dwq, dwk = vlp.thd_qk_norm_rope_bwd(gq, gk, q, k, c, cos, sin, dq=parts[0], dk=parts[1], **kw)
+    parts[2].copy_(gv)
+
+    leaf = x.double().requires_grad_()
+    w = [t.double().requires_grad_() for t in (wq, wk)]
+    heads, total = split(leaf), 0.0
+    for start, n in zip(padded, lens):
+        rows = slice(int(start), int(start) + n)
+        turned = []
+        for t, weight in zip(heads[:2], w):
+            h = t[rows]
+            h = h * torch.rsqrt(h.square().mean(-1, keepdim=True) + 1e-6) * weight
+            a, b = h[..., :d // 2], h[..., d // 2:]
+            cc, ss = cos[:n, None].double(), sin[:n, None].double()
+            turned.append(torch.cat([a * cc - b * ss, b * cc + a * ss], -1))
+        qh = turned[0].transpose(0, 1)
+        kh, vh = (t.repeat_interleave(hq // hkv, 1).transpose(0, 1) for t in (turned[1], heads[2][rows]))
+        s = (qh @ kh.transpose(1, 2) * d ** -0.5).masked_fill(
+            torch.ones(n, n, dtype=torch.bool, device="cuda").triu(1), float("-inf"))
+        total = total + ((s.softmax(-1) @ vh).transpose(0, 1) * dout[rows].double()).sum()
+    total.backward()
+    for name, got, want in (("dx", dx, leaf.grad), ("dwq", dwq, w[0].grad), ("dwk", dwk, w[1].grad)):
+        rel = float((got.double() - want).norm() / want.norm())
+        print(f"{name}: {rel:.2e}")
+        assert rel <= 12 * 2.0 ** -8, (name, rel)
+    gone = torch.ones(T, dtype=torch.bool)
+    for start, n in zip(padded, lens):
+        gone[int(start):int(start) + n] = False
+    assert torch.all(dx[gone.cuda()] == 0)
+
+
+def test_rows_captured_and_replayed_with_other_lengths():
+    """A captured forward, backward and append, replayed after the lengths and inputs changed, on another stream."""
+    T, hq, hkv, d = 24, 8, 2, 128
+    g = torch.Generator().manual_seed(6)
+    x, k = draw((T, [hq, hkv], d), BF16, g)
+    gq, gk = draw((T, [hq, hkv], d), BF16, g)
+    w = (1 + 0.2 * torch.randn(d, generator=g)).to(BF16).cuda()
+    cos, sin = tables(64, d)
+    cu, lens, table = ints([0, 10, 24]), ints([3, 0]), ints([[2, 0, 1], [5, 4, 3]])
+    kc = torch.zeros(6, 16, hkv, d, dtype=BF16, device="cuda")
+    vc = torch.zeros_like(kc)
+    call = lambda: (vlp.thd_qk_norm_rope(x, k, cu, cos, sin, q_weight=w, k_weight=w),
+                    vlp.thd_qk_norm_rope_bwd(gq, gk, x, k, cu, cos, sin, q_weight=w, k_weight=w),
+                    vlp.thd_kv_append(k, k, kc, vc, table, lens, cu, q=x, rope_cos=cos, rope_sin=sin, k_weight=w))
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for sizes, before in (([0, 24, 24], [20, 1]), ([0, 1, 9], [0, 7])):
+        cu.copy_(ints(sizes))
+        lens.copy_(ints(before))
+        x.copy_(draw((T, [hq], d), BF16, g)[0])
+        kc.zero_(), vc.zero_()
+        want = call()
+        caches = kc.clone(), vc.clone()
+        kc.zero_(), vc.zero_()
+        with torch.cuda.stream(torch.cuda.Stream()):
+            torch.cuda.current_stream().wait_stream(torch.cuda.default_stream())
+            graph.replay()
+            torch.cuda.current_stream().synchronize()
+        flat = lambda r: [*r[0], *r[1], r[2]]
+        assert all(torch.equal(a, b) for a, b in zip(flat(got), flat(want)))
+        assert torch.equal(kc, caches[0]) and torch.equal(vc, caches[1])
+
+
 # ------------------------------------------------------------------------------ append
 APPENDS = [
     # before, new, gap, page, hq, hkv, d, rotary, dtype, norm, interleaved, fused, positions, heads first
