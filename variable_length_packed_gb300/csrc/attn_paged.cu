@@ -510,8 +510,8 @@ int launch_paged(PagedArgs& p, char* ws, int sms, cudaStream_t st) {
 
 // Tiles of 16 rows where no sequence has more, else of 128.  120000 keys of 16 sequences, 32 + 8 heads of 128,
 // bf16, in us: 16 rows 89 narrow; 20 rows 94 wide, against 124 in narrow tiles of 32; 64 rows 98, against 229 in
-// two such tiles.  Heads of 64 in fp16: 32 rows 72 and 70, 36 rows 73 and 117.  Wide tiles of 4 rows (a
-// decoding batch called without the hint) cost 327 where narrow ones cost 317.
+// two such tiles.  Heads of 64 in fp16: 32 rows 62 and 70, 36 rows 68 and 117.  Wide tiles of 4 rows (a
+// decoding batch called without the hint) cost 324 where narrow ones cost 317.
 template <typename DT>
 int launch_paged_of(PagedArgs& p, long long row_hint, char* ws, int sms, cudaStream_t st) {
   if (p.d > 64) {

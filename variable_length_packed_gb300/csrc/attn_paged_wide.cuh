@@ -20,6 +20,8 @@
 // softmax streams, two score tiles for each and the queries in shared memory took 107 us with
 // keys and values by tensor copies of whole boxes of a page (16 tokens by 64 columns), 153 us with two
 // warps copying rows; with the keys in the cache it was slower too (78 against 60 us at 54 drafted tokens).
+// Heads of 64 (68 us at 64 rows, where memory asks 37): a second score tile in the room they leave, twice the
+// units on the way, and pages read a unit ahead changed nothing.
 //
 // Every wait is bounded as in the other attention kernels: one that runs out sets the CTA's
 // status word, and the CTA lets what it started finish and leaves.
