@@ -348,7 +348,7 @@ int thd_attn_merge(const void* out_a, const float* lse_a, const void* out_b, con
  * q_out, k_out device, [T, Hq, head_dim] and [T, Hkv, head_dim], contiguous, 16-byte
  *              aligned; may be q and k themselves when those are contiguous.
  *              Rows of no sequence are written as zeros.
- * head_dim     a multiple of 16 in [16, 128].
+ * head_dim     a multiple of 16 in [16, 128]; a row of one side below 2^31 values.
  * Errors: THD_ERR_ARG, THD_ERR_UNSUPPORTED, THD_ERR_CUDA.
  */
 int thd_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* q_weight,

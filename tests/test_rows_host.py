@@ -88,6 +88,15 @@ def test_paged_refusals(lib, over, status):
     assert call(lib.thd_attn_paged, PAGED, PAGED, over) == status
 
 
+@pytest.mark.parametrize("side", ["hq", "hkv"])
+@pytest.mark.parametrize("heads", [2**25, 2**30])
+def test_rows_of_too_many_values_are_refused(lib, side, heads):
+    over = {side: heads, "qs": heads * 64, "ks": heads * 64}   # 2^31 values of a row and more
+    assert call(lib.thd_qk_norm_rope, ROPE, ROPE, {**over, "T": 8}) == -2
+    assert call(lib.thd_qk_norm_rope_bwd, BWD, BWD, {**over, "dqs": heads * 64, "dks": heads * 64}) == -2
+    assert call(lib.thd_kv_append, APPEND, APPEND, {**over, "vs": heads * 64}) == -2
+
+
 def test_workspace_sizes(lib):
     assert vlp.thd_qk_norm_rope_bwd_workspace_size(128) > 0 and vlp.thd_qk_norm_rope_bwd_workspace_size(24) == 0
     assert vlp.thd_attn_paged_workspace_size(8) > 0 and vlp.thd_attn_paged_workspace_size(132) == 0

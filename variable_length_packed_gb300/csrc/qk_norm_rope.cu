@@ -1043,6 +1043,7 @@ int check_common(int B, int T, int hq, int hkv, int d, int dtype, float eps, con
   if (weight_fp32 != 0 && weight_fp32 != 1) return THD_ERR_ARG;
   if (d < 16 || d > 128 || d % 16 != 0) return THD_ERR_UNSUPPORTED;
   if (rotary < 0 || rotary > d || rotary % 16 != 0) return THD_ERR_UNSUPPORTED;
+  if ((long long)hq * d >= (1ll << 31) || (long long)hkv * d >= (1ll << 31)) return THD_ERR_UNSUPPORTED;
   if ((wq || wk) && (!std::isfinite(eps) || eps < 0.f)) return THD_ERR_ARG;
   if (rotary > 0 && (!cos || !sin || rope_rows < 1)) return THD_ERR_ARG;
   if (rotary > 0 && (!on16(cos) || !on16(sin))) return THD_ERR_ARG;
@@ -1108,8 +1109,8 @@ int launch_few_of(const RowArgs& p, unsigned grid, cudaStream_t st) {
 
 // Whether items of whole rows pay: kPasses * 32 / lanes-per-head pairs (`per`) fit one.
 bool few_heads(const RowArgs& p, int per, int share) {
-  const int items = blocks_of_heads(p.q.heads, per) + blocks_of_heads(p.k.heads, per) + blocks_of_heads(p.v.heads, per);
-  return 100 * (p.q.heads + p.k.heads + p.v.heads) < share * per * items;
+  const long long items = blocks_of_heads(p.q.heads, per) + blocks_of_heads(p.k.heads, per) + blocks_of_heads(p.v.heads, per);
+  return 100ll * (p.q.heads + p.k.heads + p.v.heads) < share * per * items;
 }
 
 // Rows of an item and items of a kind of `heads` heads.
