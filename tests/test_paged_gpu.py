@@ -348,6 +348,20 @@ def test_binding_refusals():
             pytest.fail(f"call {i} was not refused")
 
 
+def test_counts_past_32_bits_are_refused():
+    """A cache expanded to more pages than the library counts: refused, not cut to what fits 32 bits."""
+    x = make([5], [2], 4, 4, 2, 64, BF16)
+    kc, vc = (x[c][:1].expand(2 ** 32 + 1, -1, -1, -1) for c in ("kc", "vc"))
+    q, t, n, cu = x["q"], ints(x["table"]), ints([5]), ints([0, 2])
+    with pytest.raises(ValueError, match="32 bits"):
+        vlp.thd_attn_paged(q, kc, vc, t, n, cu)
+    table = torch.empty((1, 2 ** 31), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="32 bits"):
+        vlp.thd_attn_paged(q, x["kc"], x["vc"], table, n, cu)
+    with pytest.raises(ValueError, match="32 bits"):
+        vlp.thd_kv_append(q[:, :2].contiguous(), q[:, :2].contiguous(), x["kc"], x["vc"], table, n, cu)
+
+
 def test_a_wait_that_runs_out_is_reported():
     """Wide tiles wait on barriers: with an injected wait and a short limit the call comes back with the
     status bit set, and the next call is as if nothing had been."""

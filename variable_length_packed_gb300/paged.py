@@ -19,6 +19,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _F32 = torch.float32
 _Places = ctypes.c_int64 * 6
+_COUNT_MAX = 2 ** 31 - 1   # the library's counts are C ints, which ctypes would cut to 32 bits without a word
 _CODES = {torch.bfloat16: THD_BF16, torch.float16: THD_FP16}
 
 
@@ -37,6 +38,10 @@ def _workspace_size(name, head_dim):
 
 def _addr(t):
     return None if t is None else t.data_ptr()
+
+
+def _too_large(name):
+    return ValueError(f"{name}: a size does not fit the library's 32 bits")
 
 
 def _on(t, name, device):
@@ -205,6 +210,8 @@ def thd_qk_norm_rope(q, k, cu_seqlens, rope_cos=None, rope_sin=None, cu_seqlens_
             k_out = torch.empty((T, hkv, d), dtype=dtype, device=dev)
         else:
             _whole(k_out, "k_out", dev, dtype, k.shape)
+    if (T | hq | hkv | rows | B) > _COUNT_MAX:   # the or of sizes in range is in range
+        raise _too_large("thd_qk_norm_rope")
     _call("thd_qk_norm_rope", dev, _addr(q), qs, _addr(k), ks, _addr(q_weight), _addr(k_weight), fp32, float(eps),
           _addr(rope_cos), _addr(rope_sin), rows, rot, int(bool(interleaved)), cu_seqlens.data_ptr(),
           _addr(cu_seqlens_padded), _addr(position_offsets), B, _addr(q_out), _addr(k_out), T, hq, hkv, d, code)
@@ -264,6 +271,8 @@ def thd_qk_norm_rope_bwd(grad_q, grad_k, q, k, cu_seqlens, rope_cos=None, rope_s
         else:
             _whole(workspace, "workspace", dev, torch.uint8)
         size = workspace.numel()
+    if (T | hq | hkv | rows | B) > _COUNT_MAX:
+        raise _too_large("thd_qk_norm_rope_bwd")
     _call("thd_qk_norm_rope_bwd", dev, grad_q.data_ptr(), _addr(grad_k), _addr(q), qs, _addr(k), ks, _addr(q_weight),
           _addr(k_weight), fp32, float(eps), _addr(rope_cos), _addr(rope_sin), rows, rot, int(bool(interleaved)),
           cu_seqlens.data_ptr(), _addr(cu_seqlens_padded), _addr(position_offsets), B, dq.data_ptr(), dqs, _addr(dk), dks,
@@ -361,6 +370,8 @@ def thd_kv_append(k, v, k_cache, v_cache, page_table, cache_lens, cu_seqlens, cu
             q_out = torch.empty((T, hq, d), dtype=dtype, device=dev)
         else:
             _whole(q_out, "q_out", dev, dtype, q.shape)
+    if (T | hq | hkv | rows | B | shape[0] | shape[1] | wide) > _COUNT_MAX:
+        raise _too_large("thd_kv_append")
     _call("thd_kv_append", dev, _addr(q), qs, _addr(k), ks, v.data_ptr(), vs, _addr(q_weight), _addr(k_weight), fp32,
           float(eps), _addr(rope_cos), _addr(rope_sin), rows, rot, int(bool(interleaved)), _addr(positions),
           cu_seqlens.data_ptr(), _addr(cu_seqlens_padded), cache_lens.data_ptr(), B, _addr(q_out), k_cache.data_ptr(),
@@ -412,8 +423,11 @@ def thd_attn_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q, cu_se
         workspace = torch.empty(_workspace_size("thd_attn_paged_workspace_size", d), dtype=torch.uint8, device=dev)
     else:
         _whole(workspace, "workspace", dev, torch.uint8)
+    max_seqlen_q = int(max_seqlen_q)
+    if (T | hq | shape[2] | B | shape[0] | shape[1] | wide | words) > _COUNT_MAX or max_seqlen_q > _COUNT_MAX:
+        raise _too_large("thd_attn_paged")
     _call("thd_attn_paged", dev, _addr(q), k_cache.data_ptr(), v_cache.data_ptr(), strides, shape[0], shape[1],
           page_table.data_ptr(), step, wide, kv_lens.data_ptr(), cu_seqlens_q.data_ptr(), _addr(cu_seqlens_q_padded), B,
-          int(max_seqlen_q), _addr(tree_mask), words, 1.0 / math.sqrt(d) if softmax_scale is None else
+          max_seqlen_q, _addr(tree_mask), words, 1.0 / math.sqrt(d) if softmax_scale is None else
           float(softmax_scale), out.data_ptr(), _addr(lse), T, hq, shape[2], d, code, _addr(workspace), workspace.numel())
     return out, lse
