@@ -44,6 +44,9 @@ constexpr int kNarrowRows = 16;      // rows of a tile
 constexpr int kWarps = 4;            // warps of a CTA, 16 keys of the unit each
 constexpr int kWarpKeys = kUnit / kWarps;
 constexpr int kStages = 3;           // units in flight per warp
+// fp16 weights are held times 2^15 (the largest is 1, and fp16 ends below 2^16): without it one below 2^-14
+// of the maximum rounds by 2^-25 of it, which 20000 keys at 2^-23.5 add up to a third of their sum.
+constexpr float kNarrowLift = 15.f;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinAhead = 4;        // partials read at once
 
@@ -95,6 +98,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
   constexpr int kLaneKeys = 32 / kChunks;               // keys one copy instruction covers
   constexpr int kCopies = kWarpKeys / kLaneKeys;
   constexpr int kTileBytes = PagedSmem<DP>::kTileBytes;
+  constexpr float kLift = Pair16<DT>::kBF16 ? 0.f : kNarrowLift, kUnlift = Pair16<DT>::kBF16 ? 1.f : 0x1p-15f;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Share share;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -231,10 +235,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
         const float use = top == -INFINITY ? 0.f : top;
         scale[hh] = ex2_approx(m[hh] - use);
         m[hh] = top;
+        const float lifted = use - kLift;
         float sum = 0.f, sum_r = 0.f;
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const float p0 = ex2_approx(c[n][2 * hh] - use), p1 = ex2_approx(c[n][2 * hh + 1] - use);
+          const float p0 = ex2_approx(c[n][2 * hh] - lifted), p1 = ex2_approx(c[n][2 * hh + 1] - lifted);
           sum += p0 + p1;
           const uint32_t w = Pair16<DT>::put(p0, p1);
           const float2 r = Pair16<DT>::get(w);
@@ -301,7 +306,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
       for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
-        w[k] = ex2_approx(jm[(k * 3) * MT + r] - use);
+        w[k] = ex2_approx(jm[(k * 3) * MT + r] - use) * kUnlift;
         sr += w[k] * jm[(k * 3 + 1) * MT + r];
         se += w[k] * jm[(k * 3 + 2) * MT + r];
         const float4* src = reinterpret_cast<const float4*>(jo + (k * MT + r) * DP + chunk * 8);

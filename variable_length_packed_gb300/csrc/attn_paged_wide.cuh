@@ -35,6 +35,8 @@ constexpr int kWideRows = 128;
 constexpr int kWideThreads = 224;   // seven warps: two CTAs leave a thread 128 registers
 constexpr int kWideLoaders = 2;     // loading warps
 constexpr int kWideStages = 3;
+constexpr float kWideLag = 8.f;           // log2 by which weights may pass 1 before the maximum moves
+constexpr float kWideLift = 7.f;          // as kNarrowLift (attn_paged.cu): fp16 weights stay below 2^(8 + 7)
 constexpr uint32_t kWideTmemCols = 256;   // S and P [0, 64), Q [64, 128), O [128, 128 + DP)
 
 template <int DP>
@@ -57,6 +59,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
   using Tr = Pair16<DT>;
   constexpr int kChunks = DP / 8;
   constexpr int kPanelBytes = kUnit * 128;
+  constexpr float kLift = Tr::kBF16 ? 0.f : kWideLift, kUnlift = Tr::kBF16 ? 1.f : 0x1p-7f;
   constexpr uint32_t idesc_qk = umma_idesc_f16(Tr::kBF16, kWideRows, kUnit, false);
   constexpr uint32_t idesc_pv = umma_idesc_f16(Tr::kBF16, kWideRows, DP, true);
   extern __shared__ uint8_t smem_raw[];
@@ -250,9 +253,8 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
             mx[k] = fmax3f(mx[k], __uint_as_float(sr[c + 2 * k]), __uint_as_float(sr[c + 2 * k + 1]));
         }
         const float m_new = fmax3f(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-        // the maximum moves only when it grows by more than 8 (log2): weights stay below 2^8 and the
-        // output is seldom rescaled
-        const bool need = (m_new - m_run) * sl2 > 8.f;   // false while both are -inf
+        // the maximum moves only when it grows by more than kWideLag: the output is seldom rescaled
+        const bool need = (m_new - m_run) * sl2 > kWideLag;   // false while both are -inf
         float alpha = 1.f;
         if (need) {
           alpha = ex2_approx((m_run - m_new) * sl2);
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
           l_run *= alpha;
           l_exact *= alpha;
         }
-        const float mb = (m_run == -INFINITY ? 0.f : m_run) * sl2;
+        const float mb = (m_run == -INFINITY ? 0.f : m_run) * sl2 - kLift;
         // sums of the weights and of the weights as rounded, in two chains of pairs each
         const float2 scale2 = make_float2(sl2, sl2), bias2 = make_float2(-mb, -mb);
         float2 ex[2], rd[2];
@@ -334,7 +336,9 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
           } else {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(pdst + (8 * c + e / 4) * (kWideRows * 4)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              *reinterpret_cast<float4*>(pdst + (8 * c + e / 4) * (kWideRows * 4)) =
+                  make_float4(__uint_as_float(o[e]) * kUnlift, __uint_as_float(o[e + 1]) * kUnlift,
+                              __uint_as_float(o[e + 2]) * kUnlift, __uint_as_float(o[e + 3]) * kUnlift);
           }
         }
       }
@@ -343,12 +347,12 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
         if (x.whole) {
           if (p.lse)
             p.lse[(long long)hq * p.T + x.s.q_start + tok] =
-                l_exact == 0.f ? -INFINITY : top * 0.69314718055994531f + logf(l_exact);
+                l_exact == 0.f ? -INFINITY : top * 0.69314718055994531f + logf(l_exact * kUnlift);
         } else {
           float* pm = p.part_m + (long long)part * 3 * kWideRows;
           pm[r] = top;
-          pm[kWideRows + r] = l_run;
-          pm[2 * kWideRows + r] = l_exact;
+          pm[kWideRows + r] = l_run * kUnlift;
+          pm[2 * kWideRows + r] = l_exact * kUnlift;
         }
       }
       if (tid == 0) note_split(p, x, share);
