@@ -23,17 +23,20 @@ _COUNT_MAX = 2 ** 31 - 1   # the library's counts are C ints, which ctypes would
 _CODES = {torch.bfloat16: THD_BF16, torch.float16: THD_FP16}
 
 
+@functools.lru_cache(maxsize=None)
+def _workspace_size(name, head_dim):
+    size = getattr(load_library(), name)
+    return int(size(head_dim)) if abs(head_dim) <= _COUNT_MAX else 0
+
+
 def thd_qk_norm_rope_bwd_workspace_size(head_dim):
-    return int(load_library().thd_qk_norm_rope_bwd_workspace_size(int(head_dim)))
+    """Bytes of device workspace thd_qk_norm_rope_bwd needs; 0 for an unsupported head_dim."""
+    return _workspace_size("thd_qk_norm_rope_bwd_workspace_size", int(head_dim))
 
 
 def thd_attn_paged_workspace_size(head_dim):
-    return int(load_library().thd_attn_paged_workspace_size(int(head_dim)))
-
-
-@functools.lru_cache(maxsize=None)
-def _workspace_size(name, head_dim):
-    return int(getattr(load_library(), name)(head_dim))
+    """Bytes of device workspace thd_attn_paged needs; 0 for an unsupported head_dim."""
+    return _workspace_size("thd_attn_paged_workspace_size", int(head_dim))
 
 
 def _addr(t):
@@ -210,7 +213,7 @@ def thd_qk_norm_rope(q, k, cu_seqlens, rope_cos=None, rope_sin=None, cu_seqlens_
             k_out = torch.empty((T, hkv, d), dtype=dtype, device=dev)
         else:
             _whole(k_out, "k_out", dev, dtype, k.shape)
-    if (T | hq | hkv | rows | B) > _COUNT_MAX:   # the or of sizes in range is in range
+    if (T | hq | hkv | d | rows | B) > _COUNT_MAX:   # the or of sizes in range is in range
         raise _too_large("thd_qk_norm_rope")
     _call("thd_qk_norm_rope", dev, _addr(q), qs, _addr(k), ks, _addr(q_weight), _addr(k_weight), fp32, float(eps),
           _addr(rope_cos), _addr(rope_sin), rows, rot, int(bool(interleaved)), cu_seqlens.data_ptr(),
@@ -271,7 +274,7 @@ def thd_qk_norm_rope_bwd(grad_q, grad_k, q, k, cu_seqlens, rope_cos=None, rope_s
         else:
             _whole(workspace, "workspace", dev, torch.uint8)
         size = workspace.numel()
-    if (T | hq | hkv | rows | B) > _COUNT_MAX:
+    if (T | hq | hkv | d | rows | B) > _COUNT_MAX:
         raise _too_large("thd_qk_norm_rope_bwd")
     _call("thd_qk_norm_rope_bwd", dev, grad_q.data_ptr(), _addr(grad_k), _addr(q), qs, _addr(k), ks, _addr(q_weight),
           _addr(k_weight), fp32, float(eps), _addr(rope_cos), _addr(rope_sin), rows, rot, int(bool(interleaved)),
@@ -370,7 +373,7 @@ def thd_kv_append(k, v, k_cache, v_cache, page_table, cache_lens, cu_seqlens, cu
             q_out = torch.empty((T, hq, d), dtype=dtype, device=dev)
         else:
             _whole(q_out, "q_out", dev, dtype, q.shape)
-    if (T | hq | hkv | rows | B | shape[0] | shape[1] | wide) > _COUNT_MAX:
+    if (T | hq | hkv | d | rows | B | shape[0] | shape[1] | wide) > _COUNT_MAX:
         raise _too_large("thd_kv_append")
     _call("thd_kv_append", dev, _addr(q), qs, _addr(k), ks, v.data_ptr(), vs, _addr(q_weight), _addr(k_weight), fp32,
           float(eps), _addr(rope_cos), _addr(rope_sin), rows, rot, int(bool(interleaved)), _addr(positions),
@@ -424,7 +427,7 @@ def thd_attn_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q, cu_se
     else:
         _whole(workspace, "workspace", dev, torch.uint8)
     max_seqlen_q = int(max_seqlen_q)
-    if (T | hq | shape[2] | B | shape[0] | shape[1] | wide | words) > _COUNT_MAX or max_seqlen_q > _COUNT_MAX:
+    if (T | hq | shape[2] | d | B | shape[0] | shape[1] | wide | words | abs(max_seqlen_q)) > _COUNT_MAX:
         raise _too_large("thd_attn_paged")
     _call("thd_attn_paged", dev, _addr(q), k_cache.data_ptr(), v_cache.data_ptr(), strides, shape[0], shape[1],
           page_table.data_ptr(), step, wide, kv_lens.data_ptr(), cu_seqlens_q.data_ptr(), _addr(cu_seqlens_q_padded), B,
