@@ -468,9 +468,6 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const Pag
   }
 }
 
-bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
-
 // Workspace: the call's status word (byte 8), the CTAs' status words and split tiles, then the
 // partial results (outputs, then maxima and sums).
 constexpr int kMaxRows = 128;   // rows of a tile at most

@@ -241,15 +241,6 @@ __device__ __forceinline__ void note_split(const PagedArgs& p, const Piece& x, c
 // Place of the piece's partial result.
 __device__ __forceinline__ int part_of_piece(const Piece& x) { return blockIdx.x * 2 + (x.first ? 0 : 1); }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Element offset of a piece's key or value in its cache: 0 for one that is not read.
 __device__ __forceinline__ long long cache_offset(const PagedArgs& p, const Piece& x, const int32_t* table, int key,
                                                   bool values) {

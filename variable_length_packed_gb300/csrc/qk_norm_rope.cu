@@ -127,14 +127,7 @@ __device__ __forceinline__ uint4 pack4(const f2* f) {
 }
 
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-               "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+  cp_async16(static_cast<uint32_t>(__cvta_generic_to_shared(dst)), src);
 }
 
 // The turn of a lane's two chunks by its angles, with a factor for each value before it:
@@ -353,7 +346,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowBlocksPerSm) head_rows_ker
       }
       ahead.next();
     }
-    copy_commit();
+    cp_async_commit();
     items[kAhead] = it;
   };
 #pragma unroll
@@ -387,7 +380,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowBlocksPerSm) head_rows_ker
     const bool rot = turns && slot < (p.rotary >> 4);
     const int head0 = block * (kRowPasses * kPerPass);
     DT* out = dst + (head0 + lane / LPH) * dst_head;
-    copy_wait<kAhead>();
+    cp_async_wait<kAhead>();
     __syncwarp();
     if (store && it.seq < 0) {
 #pragma unroll
@@ -486,7 +479,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowBlocksPerSm) head_rows_ker
     for (int i = 0; i < kAhead; ++i) items[i] = items[i + 1];
     stage = stage == kRowStages - 1 ? 0 : stage + 1;
   }
-  copy_wait<0>();
+  cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------------------- few heads
@@ -781,7 +774,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdBlocksPerSm) head_rows_bwd
       }
       ahead.next();
     }
-    copy_commit();
+    cp_async_commit();
     inside[kAhead] = in;
   };
 #pragma unroll
@@ -796,7 +789,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdBlocksPerSm) head_rows_bwd
     fetch_next(stage == 0 ? kBwdStages - 1 : stage - 1);
     const int head0 = (int)part * (kBwdPasses * kPerPass);
     DT* out = static_cast<DT*>(h.dst) + (long long)t * h.dst_stride + (long long)(head0 + lane / LPH) * p.d;
-    copy_wait<kAhead>();
+    cp_async_wait<kAhead>();
     __syncwarp();
     if (!inside[0]) {
 #pragma unroll
@@ -898,7 +891,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdBlocksPerSm) head_rows_bwd
     for (int i = 0; i < kAhead; ++i) inside[i] = inside[i + 1];
     stage = stage == kBwdStages - 1 ? 0 : stage + 1;
   }
-  copy_wait<0>();
+  cp_async_wait<0>();
   if (!norm) return;
   __syncthreads();   // the ring is read no more
   leave_weight_share<LPH>(dw0, dw1, reinterpret_cast<float(*)[128]>(smem), c0, c1, mine,
@@ -1029,9 +1022,6 @@ __global__ void __launch_bounds__(kSumRows * 8) weight_sum_kernel(const float* _
 }
 
 // ---------------------------------------------------------------------------- host
-bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
-
 int lanes_per_head(int d) { return d <= 16 ? 1 : (d <= 32 ? 2 : (d <= 64 ? 4 : 8)); }
 
 // The checks the three entry points share.

@@ -1,5 +1,5 @@
-// seq_rows.cuh — what the row operators share: the sequence a packed row belongs to,
-// and 16-bit element conversion.
+// seq_rows.cuh — what the operators around packed attention share: the sequence a packed row
+// belongs to, 16-bit element conversion, asynchronous copies, launch settings and alignment checks.
 //
 // Packed rows, cu_seqlens and slot starts as everywhere in this library: sequence b holds rows
 // [start_b, start_b + cu[b+1] - cu[b]), start_b = padded[b] or cu[b], starts ascending.
@@ -40,6 +40,22 @@ struct SmemGrant {
     return true;
   }
 };
+
+inline bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+// 16 bytes from global to shared memory, asynchronously; zeros (and nothing read) where `take` is false.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Where row t lies, found by the whole warp (every lane passes the same t and gets the same
 // answer): its sequence and the rows [from, to) of it, or seq -1 and rows after t that are
@@ -141,16 +157,6 @@ struct Pair16<__half> {
   }
 };
 
-template <typename DT>
-__device__ __forceinline__ void unpack8(const uint4& x, float* f) {
-  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = Pair16<DT>::get(u[i]);
-    f[2 * i] = p.x;
-    f[2 * i + 1] = p.y;
-  }
-}
 template <typename DT>
 __device__ __forceinline__ uint4 pack8(const float* f) {
   return make_uint4(Pair16<DT>::put(f[0], f[1]), Pair16<DT>::put(f[2], f[3]), Pair16<DT>::put(f[4], f[5]),
