@@ -430,6 +430,8 @@ size_t thd_attn_paged_workspace_size(int head_dim);
  * token's mask is set.  A token that sees no key gets zeros and lse -inf.
  * Values that a token does not see must still be finite where they lie among
  * the L cached ones; whatever lies behind them in a page is not looked at.
+ * Scores, sums and outputs are held in fp32; the weights are rounded to dtype once for
+ * the product with the values, the output once to dtype.
  *
  * q            device [T, Hq, head_dim], contiguous, 16-byte aligned.
  * k_cache, v_cache, cache_strides, num_pages, page_size, page_table,

@@ -12,7 +12,10 @@
 //  * the query heads that share a key/value head are the rows of one tile (row = token * group
 //    + head of the group), so a key is read once for all of them;
 //  * a unit is kUnit keys of one (sequence, key/value head, row tile); the units of the batch
-//    are laid end to end and every CTA takes an equal share of them, whatever the lengths;
+//    are laid end to end and every CTA takes an equal number of them, whatever the lengths.  Units that
+//    the causal mask hides from a whole tile count too, although they are passed over: a share that has many
+//    of them ends early (of one fresh prompt of 8192 the busiest CTA works on 1.97 times the mean, of 2048
+//    new tokens after 30000 on 1.03; decoding steps and trees have none);
 //  * a CTA whose share ends inside a tile writes an unnormalised partial (at most two per CTA),
 //    and a second kernel, launched to overlap the first one's end, joins them.
 // Tiles of more than 16 rows are attn_paged_wide.cuh's.  Here, with 16 rows (decoding: the heads of
@@ -20,9 +23,11 @@
 // the keys come at memory speed, so each warp runs alone: it streams its own 16 keys of each unit
 // through its own ring of shared memory with 16-byte asynchronous copies, keeps a running maximum, sums
 // and output tile in registers, and meets the other warps only when the tile is done.
-// Measured: 500000 keys of 64 sequences, 32 + 8 heads of 128, one token each, 310 us, 6.6 TB/s of the
-// 6.8 that a copy reaches; 262144 keys of one sequence, 16 heads of 64, 166 us, 6.5 TB/s.  Four times as many
-// CTAs with shorter shares (an SM that is slower takes fewer) gained nothing: 319 and 186 us.
+// Measured, with the join: 500000 keys of 64 sequences, 32 + 8 heads of 128, one token each, 310 us, 6.6 TB/s
+// of the 6.8 that a copy reaches; 262144 keys of one sequence, 16 heads of 64, 172 us, 6.2 TB/s.  Four times as
+// many CTAs with shorter shares (an SM that is slower takes fewer) gained nothing: 319 and 186 us.  Heads of 96, 80
+// and 32 are padded to 128 and 64 in shared memory and in the products, though not read: 300000 keys of 64
+// sequences, 16 + 8 heads, 0.64, 0.56 and 0.35 of the copy's rate.
 #include <cmath>
 #include <cstdint>
 #include <cuda_bf16.h>

@@ -1,5 +1,13 @@
 // attn_paged_common.cuh — what the kernels of attn_paged.cu share: arguments, the split of the
-// batch's keys over the CTAs, the walk over a CTA's pieces, and copies out of the pages.
+// batch's keys over the CTAs, the walk over a CTA's pieces, and places in the pages.
+//
+// Both kernels hold scores, maxima, sums and outputs in fp32 and round the weights once to the type of
+// the values, because the matrix units multiply 16-bit operands of one type (thd_attn_fwd does the same).
+// The output is divided by the sum of the rounded weights, so that their rounding does not shift its scale; the
+// log-sum-exp takes the sum of the exact ones.  Error of the norm against 64 bits in bf16: 2.0e-3 to
+// 2.3e-3, of which rounding the output alone is 1.7e-3; fp16 2.8e-4 and 2.1e-4.  Measured and left: weights in
+// two 16-bit parts, with twice the products for the values, bring the error to the output's own rounding and
+// cost 1 % on 500000 keys of heads of 128, 3 % on 262144 of 64, and 2 to 8 % in tiles of 128 rows.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>

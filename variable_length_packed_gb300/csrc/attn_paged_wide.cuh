@@ -1,6 +1,6 @@
 // attn_paged_wide.cuh — attention over a paged cache for tiles of 128 query rows, on the
 // fifth-generation tensor cores: chunks of new tokens and trees of drafted ones, where more
-// than 32 rows share a key/value head.
+// than 16 rows share a key/value head.
 //
 // The same split of the batch's keys over the CTAs as the narrow kernel's (attn_paged.cu); inside a CTA
 // the work is divided among warps:
@@ -19,7 +19,8 @@
 // first use of code, tables and pages one after another).  Measured and left: one CTA per SM with two
 // softmax streams, two score tiles for each and the queries in shared memory took 107 us with
 // keys and values by tensor copies of whole boxes of a page (16 tokens by 64 columns), 153 us with two
-// warps copying rows; with the keys in the cache it was slower too (78 against 60 us at 54 drafted tokens).
+// warps copying rows; with the keys in the L2 it was slower too (78 against 60 us for 54 drafted tokens over
+// 24000 keys).  Two CTAs leave a thread 128 registers; heads of 128 spill 8 to 16 bytes.
 // Heads of 64 (68 us at 64 rows, where memory asks 37): a second score tile in the room they leave, twice the
 // units on the way, and pages read a unit ahead changed nothing.
 //

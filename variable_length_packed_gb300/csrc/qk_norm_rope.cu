@@ -10,7 +10,8 @@
 // Backward, with g the gradient of y:
 //   h_i = g_i cos_i + g_j sin_i,  h_j = g_j cos_i - g_i sin_i   (the rotation by -p)
 //   dw = sum over rows of h * x * r,   dx = r * (h * w - x * r^2 * mean(h * w * x))
-// All in fp32, rounded once to the tensors' type.
+// All in fp32, rounded once to the tensors' type.  dw is summed in fp32 too: a few terms one after another in
+// a lane, then trees (2e-7 of its norm off over 200000 rows of 32 heads, where rounding it to fp32 alone is 3e-8).
 //
 // Layout: a head is d / 8 chunks of 16 bytes.  One lane holds two of them, the two whose values
 // pair up under the half-split rotation (chunks s and s + rotary / 16; of the part behind, one of
@@ -72,7 +73,8 @@ constexpr int kRowBlocksPerSm = 4;
 constexpr int kRowRun = 6;        // items of a warp at most
 // Per cent of the lanes at work below which items take whole rows (few_heads_kernel).  Share of the copy
 // bandwidth, items of one row against whole rows, heads of 128, normed: 4 + 4 heads (25 %) 44 and 52,
-// 8 + 1 (28 %) 49 and 54, 8 + 2 (31 %) 54 and 53, 16 + 2 (56 %) 79 and 57.
+// 8 + 1 (28 %) 49 and 54, 8 + 2 (31 %) 54 and 53, 16 + 2 (56 %) 79 and 57.  The lanes that heads of 48, 80, 96
+// and 112 leave idle in both forms do not count: heads of 80 reach 35 to 42 % with whole rows, of 96 41 to 49 %.
 constexpr int kFewShare = 30;
 
 // Two fp32 values in one 64-bit register: multiplied and added by one instruction.
@@ -561,7 +563,10 @@ __device__ __forceinline__ void turn_chunks(f2* x0, f2* x1, const f2* c, const f
   }
 }
 
-// a warp takes one item: queries' first, then keys', then values'
+// A warp takes one item: queries' first, then keys', then values'.  Nothing is on the way while a warp looks
+// for its rows, which other warps have to cover: five blocks an SM (96 registers a thread, up to 148 bytes
+// spilled) reach 0.55 of the copy's rate at 1 + 1, 4 + 1 and 8 + 1 heads of 128 and 64, four
+// blocks without spills 0.52.  Into a cache: four, 0.55 to 0.64.
 template <typename DT, int LPH, bool kCache>
 __global__ void __launch_bounds__(kRowWarps * 32, kCache ? 4 : 5) few_heads_kernel(const RowArgs p) {
   const int lane = threadIdx.x & 31;
