@@ -147,6 +147,29 @@ int thd_attn_fwd_window(const void* q, const void* k, const void* v,
                         void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * thd_attn_fwd_sinks — thd_attn_fwd_window with first tokens that stay visible.
+ *
+ * No counterpart on the pages: it extends the sliding window, for models that
+ * were trained with such tokens and for caches that keep them.
+ * Key j of a sequence is visible to its query i iff it is visible under the
+ * sequence's mask type and
+ *     i + shift - window_left <= j <= i + shift + window_right  or  j < sink_tokens.
+ * sink_tokens  >= 0; 0 is exactly thd_attn_fwd_window.  Without a window
+ *              ((-1, -1)) nothing is hidden and it has no effect.
+ * Every other argument, the results and the errors are those of
+ * thd_attn_fwd_window (THD_ERR_ARG also for sink_tokens < 0).
+ */
+int thd_attn_fwd_sinks(const void* q, const void* k, const void* v,
+                       const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
+                       const int32_t* cu_seqlens_q_padded, const int32_t* cu_seqlens_kv_padded,
+                       const uint8_t* seq_is_causal,
+                       int batch_size, int max_seqlen, float softmax_scale,
+                       void* out, float* lse,
+                       int total_tokens, int num_heads_q, int num_heads_kv, int head_dim,
+                       int dtype, int window_left, int window_right, int sink_tokens,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * thd_attn_bwd_workspace_size — bytes of device workspace thd_attn_bwd needs for
  * T = total_tokens rows, Hq query heads and head_dim d:
  * 256 + (Hq*T*4 rounded up to 256) + (T*Hq*d*4 rounded up to 256); 0 for invalid sizes.
@@ -205,6 +228,23 @@ int thd_attn_bwd_window(const void* q, const void* k, const void* v, const void*
                         int total_tokens, int num_heads_q, int num_heads_kv, int head_dim,
                         int dtype, int window_left, int window_right,
                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * thd_attn_bwd_sinks — thd_attn_bwd_window for a forward computed with
+ * thd_attn_fwd_sinks: the same window and sink_tokens (0 is exactly
+ * thd_attn_bwd_window).  Other arguments and errors as there, and THD_ERR_ARG
+ * for sink_tokens < 0.
+ */
+int thd_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* out, const float* lse,
+                       const void* dout,
+                       const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
+                       const int32_t* cu_seqlens_q_padded, const int32_t* cu_seqlens_kv_padded,
+                       const uint8_t* seq_is_causal,
+                       int batch_size, int max_seqlen, float softmax_scale,
+                       void* dq, void* dk, void* dv,
+                       int total_tokens, int num_heads_q, int num_heads_kv, int head_dim,
+                       int dtype, int window_left, int window_right, int sink_tokens,
+                       void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * thd_attn_fwd_noalloc — thd_attn_fwd for callers that cannot allocate device

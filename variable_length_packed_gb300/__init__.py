@@ -53,6 +53,8 @@ def load_library():
     lib.thd_attn_fwd.argtypes = [P, P, P, P, P, P, P, P, I, I, F, P, P, I, I, I, I, I, P, SZ, P]
     lib.thd_attn_fwd_window.restype = I
     lib.thd_attn_fwd_window.argtypes = [P, P, P, P, P, P, P, P, I, I, F, P, P, I, I, I, I, I, I, I, P, SZ, P]
+    lib.thd_attn_fwd_sinks.restype = I
+    lib.thd_attn_fwd_sinks.argtypes = [P, P, P, P, P, P, P, P, I, I, F, P, P, I, I, I, I, I, I, I, I, P, SZ, P]
     lib.thd_attn_fwd_noalloc.restype = I
     lib.thd_attn_fwd_noalloc.argtypes = [P, P, P, P, P, P, P, P, I, I, F, P, P, I, I, I, I, I, P]
     lib.thd_attn_noalloc_status.restype = I
@@ -62,6 +64,9 @@ def load_library():
     lib.thd_attn_bwd_window.restype = I
     lib.thd_attn_bwd_window.argtypes = [P, P, P, P, P, P, P, P, P, P, P, I, I, F, P, P, P, I, I, I, I, I, I, I, P, SZ,
                                         P]
+    lib.thd_attn_bwd_sinks.restype = I
+    lib.thd_attn_bwd_sinks.argtypes = [P, P, P, P, P, P, P, P, P, P, P, I, I, F, P, P, P, I, I, I, I, I, I, I, I, P, SZ,
+                                       P]
     lib.thd_attn_bwd_workspace_size.restype = SZ
     lib.thd_attn_bwd_workspace_size.argtypes = [I, I, I]
     lib.thd_attn_merge.restype = I
@@ -194,9 +199,17 @@ def _window_args(window):
     return left, right
 
 
+def _sink_count(sink_tokens):
+    sinks = int(sink_tokens)
+    if not 0 <= sinks < 2 ** 31:
+        raise ValueError("sink_tokens must be >= 0 and fit 32 bits")
+    return sinks
+
+
 def thd_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=None,
                  cu_seqlens_kv_padded=None, seq_is_causal=None, batch_size=None, max_seqlen=0,
-                 softmax_scale=None, out=None, lse=None, return_lse=True, workspace=None, window=(-1, -1)):
+                 softmax_scale=None, out=None, lse=None, return_lse=True, workspace=None, window=(-1, -1),
+                 sink_tokens=0):
     """Packed THD self-attention forward on the current CUDA stream.
 
     q: [T, Hq, d], k/v: [T, Hkv, d] (bf16 or fp16, CUDA, contiguous).  cu_seqlens_*:
@@ -205,6 +218,7 @@ def thd_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=None,
     per-sequence mask type: MASK_PADDING (0), MASK_PADDING_CAUSAL (1, top-left) or
     MASK_PADDING_CAUSAL_BOTTOM_RIGHT (2).  q and k/v sequences may differ in length.
     window: (left, right) sliding window around the mask type's diagonal, -1 = unbounded.
+    sink_tokens: first keys of a sequence that the window does not hide (the mask type still does).
     max_seqlen: a hint (never trusted for correctness); 1..256 selects the kernel that packs
     runs of short sequences into shared tiles (see thd_attn_fwd in include/thd_attn.h).
     Returns (out [T, Hq, d], lse [Hq, T] float32 or None).
@@ -231,13 +245,14 @@ def thd_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=None,
     if workspace is None:
         workspace = torch.empty(thd_attn_workspace_size(), dtype=torch.uint8, device=q.device)
     left, right = _window_args(window)
+    sinks = _sink_count(sink_tokens)
     with torch.cuda.device(q.device):
-        st = _lib().thd_attn_fwd_window(
+        st = _lib().thd_attn_fwd_sinks(
             _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q), _ptr(cu_seqlens_kv),
             _ptr(cu_seqlens_q_padded), _ptr(cu_seqlens_kv_padded), _ptr(seq_is_causal),
             int(batch_size), int(max_seqlen), float(softmax_scale), _ptr(out), _ptr(lse),
             int(T), int(Hq), int(Hkv), int(d), THD_BF16 if q.dtype == torch.bfloat16 else THD_FP16,
-            left, right, _ptr(workspace), workspace.numel(), _stream_handle(q.device))
+            left, right, sinks, _ptr(workspace), workspace.numel(), _stream_handle(q.device))
     if st != THD_OK:
         raise ThdError(st, "thd_attn_fwd")
     return out, lse
@@ -365,9 +380,9 @@ def thd_padding_mask_cross(cu_seqlens_q, cu_seqlens_kv, batch_size, max_seqlen_q
 
 def thd_attn_bwd(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=None,
                  cu_seqlens_kv_padded=None, seq_is_causal=None, batch_size=None, max_seqlen=0,
-                 softmax_scale=None, dq=None, dk=None, dv=None, workspace=None, window=(-1, -1)):
-    """Gradients (dq, dk, dv) of thd_attn_fwd for the same batch and window; out / lse are
-    the forward's outputs.  head_dim 64 or 128."""
+                 softmax_scale=None, dq=None, dk=None, dv=None, workspace=None, window=(-1, -1), sink_tokens=0):
+    """Gradients (dq, dk, dv) of thd_attn_fwd for the same batch, window and sink_tokens; out / lse
+    are the forward's outputs.  head_dim 64 or 128."""
     T, Hq, Hkv, d = _check_qkv(q, k, v)
     _check_metadata_dtypes(cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, seq_is_causal)
     for name, t in (("q", q), ("k", k), ("v", v), ("out", out), ("lse", lse), ("dout", dout),
@@ -396,12 +411,13 @@ def thd_attn_bwd(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlen
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     left, right = _window_args(window)
+    sinks = _sink_count(sink_tokens)
     with torch.cuda.device(q.device):
-        st = _lib().thd_attn_bwd_window(
+        st = _lib().thd_attn_bwd_sinks(
             _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(cu_seqlens_q), _ptr(cu_seqlens_kv),
             _ptr(cu_seqlens_q_padded), _ptr(cu_seqlens_kv_padded), _ptr(seq_is_causal), int(batch_size),
             int(max_seqlen), float(softmax_scale), _ptr(dq), _ptr(dk), _ptr(dv), int(T), int(Hq), int(Hkv), int(d),
-            THD_BF16 if q.dtype == torch.bfloat16 else THD_FP16, left, right, _ptr(workspace), workspace.numel(),
+            THD_BF16 if q.dtype == torch.bfloat16 else THD_FP16, left, right, sinks, _ptr(workspace), workspace.numel(),
             _stream_handle(q.device))
     if st != THD_OK:
         raise ThdError(st, "thd_attn_bwd")

@@ -250,8 +250,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int key = kv0 + row;                       // this thread's key position (TMEM lane)
     // query tiles holding a query that sees a key of [kv0, kv0 + 128): query i sees key j
     // only if i + shift - lo_off <= j <= i + shift + hi_off
-    const long long first_q = (long long)kv0 - s.shift - s.hi_off;
-    const long long last_q = (long long)kv0 + kTileM - 1 - s.shift + s.lo_off;
+    // (or j < sinks and the mask type allows it)
+    const bool has_sinks = kv0 < p.sinks;
+    const int sink_hi = s.causal ? 0 : kNoBound;
+    const long long first_q = (long long)kv0 - s.shift - (has_sinks ? sink_hi : s.hi_off);
+    const long long last_q = (long long)kv0 + kTileM - 1 - s.shift + (has_sinks ? kNoBound : s.lo_off);
     const int qt_first = first_q <= 0 ? 0 : (int)min(first_q / kTileM, (long long)INT32_MAX);
     const int nqt_all = (s.q_len + kTileM - 1) / kTileM;
     const int nqt = last_q < 0 ? 0 : (int)min((long long)nqt_all, last_q / kTileM + 1);
@@ -343,8 +346,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // q0 + c sees key j iff j - shift - hi_off <= q0 + c <= j - shift + lo_off)
         const bool kvalid = key < s.kv_len;
         const long long kd = (long long)key - s.shift - q0;
-        const int c_lo = (int)min(max(kd - s.hi_off, -1ll), (long long)kTileM);
-        const int c_hi = (int)max(min(kd + s.lo_off, (long long)rows_q - 1), -1ll);
+        const bool sink = key < p.sinks;
+        const int c_lo = (int)min(max(kd - (sink ? sink_hi : s.hi_off), -1ll), (long long)kTileM);
+        const int c_hi = (int)max(min(kd + (sink ? kNoBound : s.lo_off), (long long)rows_q - 1), -1ll);
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int c0 = 2 * half + cc;   // 32-column chunk

@@ -45,6 +45,7 @@ struct AttnParams {
   uint32_t inject_wait;    // test setting: each CTA makes one wait that runs out (inject_wait_timeout)
   int claim;               // work items taken per atomic on the counter (>= 1)
   int win_left, win_right; // sliding window (keys before / after the diagonal), -1 = unbounded
+  int sinks;               // first keys of a sequence that the window does not hide (0 without a window)
   int B, T, Hq, Hkv, d, group;
   float scale;             // softmax scale
   float scale_log2;        // softmax scale * log2(e)
@@ -93,6 +94,14 @@ __device__ __forceinline__ int seq_last_key(const SeqInfo& s, int qpos) {
   return l > s.kv_len - 1 ? s.kv_len - 1 : (l < -1 ? -1 : (int)l);
 }
 
+// Keys [0, sink_end) of the sequence are seen by query position qpos wherever its window lies: the first
+// `sinks` ones that the mask type allows.  Grows with qpos, like the two above.
+__device__ __forceinline__ int sink_end(const SeqInfo& s, int qpos, int sinks) {
+  const long long mask_end = s.causal ? (long long)qpos + s.shift + 1 : (long long)s.kv_len;
+  const long long e = min((long long)min(sinks, s.kv_len), mask_end);
+  return e < 0 ? 0 : (int)e;
+}
+
 // Test setting (p.inject_wait, off by default): one bounded wait on phase 0 of `bar`,
 // a barrier that nothing completes before the CTA's own final drain, so the wait runs
 // out after p.wait_limit_ns whatever the timing, sets the status bit and the CTA's
@@ -139,6 +148,32 @@ __device__ __forceinline__ int kv_tiles_for(const SeqInfo& s, int q0, int rows) 
   return last < 0 ? 0 : last / kBlockN + 1;
 }
 __device__ __forceinline__ int kv_first_tile(const SeqInfo& s, int q0) { return seq_first_key(s, q0) / kBlockN; }
+
+// KV tiles that the 128-row Q tile at position q0 < q_len visits under a window: [0, ns) for the first keys
+// that stay visible, then [j0, n).  Where the two touch they are one range with ns = 0; n = 0 when no
+// row sees a key.
+struct KvTiles {
+  int ns, j0, n;
+};
+__device__ __forceinline__ KvTiles kv_tiles_windowed(const SeqInfo& s, int q0, int sinks) {
+  KvTiles r;
+  r.ns = 0;
+  r.n = kv_tiles_for(s, q0, kTileM);
+  r.j0 = kv_first_tile(s, q0);
+  if (r.n <= r.j0) r.n = r.j0 = 0;
+  if (sinks > 0) {
+    const int first = (sink_end(s, min(q0 + kTileM, s.q_len) - 1, sinks) + kBlockN - 1) / kBlockN;
+    if (r.n == 0) {
+      r.n = first;
+    } else if (first >= r.j0) {
+      r.j0 = 0;
+      r.n = max(r.n, first);
+    } else {
+      r.ns = first;
+    }
+  }
+  return r;
+}
 
 // ----------------------------------------------------------------------------
 // Tile scheduler.  Work item = (sequence, query head, block of BLOCK_M query
@@ -210,9 +245,10 @@ __device__ __forceinline__ bool span_is_short(int4 a) { return a.y > 0 && a.y <=
 // first in the same order, then short sequences (2 full context, 1 causal),
 // then sequences without query rows (0), so short sequences form a suffix.
 template <bool kPairs = false>
-__device__ __forceinline__ uint32_t seq_sort_key(const SeqInfo& s) {
+__device__ __forceinline__ uint32_t seq_sort_key(const SeqInfo& s, int sinks) {
   int nkv = (s.kv_len + kBlockN - 1) / kBlockN;
-  if (s.lo_off < kNoBound) nkv = min(nkv, s.lo_off / kBlockN + 2);   // a window bounds the tiles per row block
+  // a window bounds the tiles per row block
+  if (s.lo_off < kNoBound) nkv = min(nkv, s.lo_off / kBlockN + 2 + min(sinks, s.kv_len) / kBlockN + (sinks > 0 ? 1 : 0));
   if (!kPairs) {
     nkv = nkv > 511 ? 511 : nkv;
     return (uint32_t)(nkv * 2 + (s.causal ? 0 : 1));
@@ -386,7 +422,7 @@ __device__ void sched_load_chunk(SchedSmem& s, const AttnParams& p, int base) {
       s.span[i] = make_int4(si.q_start, si.q_len, si.kv_start, si.kv_len);
       const int raw = p.causal ? (int)p.causal[base + i] : kMaskPadding;
       s.code[i] = (uint8_t)(raw == kMaskPadding ? kMaskPadding : (raw == kMaskCausalBottomRight ? raw : 1));
-      k = seq_sort_key<kPairs>(si);
+      k = seq_sort_key<kPairs>(si, p.sinks);
       s.key[i] = (uint16_t)k;
     }
     // one add per distinct key of the 32 (many sequences share a key: the adds to one

@@ -43,7 +43,9 @@
 //
 // With a sliding window (kWin), a Q tile visits only the KV tiles inside its
 // rows' bands, starting at its own first tile, and rows mask keys on both
-// sides; the kernel without a window is a separate instantiation.
+// sides; with first keys that stay visible (kWinSinks, p.sinks) their KV tiles come
+// in front.  The kernels without a window, and with one but no such keys, are
+// instantiations of their own, which those keys cost nothing.
 //
 // TMEM (512 columns): S0 [0,128), S1 [128,256), O0 and O1 after them; P_i
 // occupies the first 64 columns of S_i (two 16-bit values per column).
@@ -71,6 +73,7 @@ constexpr int kWsThreads = 384;  // 12 warps: three warpgroups
 constexpr uint32_t kRegsCtl = 112, kRegsSoftmax = 192;
 static_assert(128 * kRegsCtl + 256 * kRegsSoftmax <= 384 * 168, "register split within the launch's registers");
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
+constexpr int kWinSinks = 2;     // values of kWin: 0 no window, 1 a window, 2 a window and first keys that stay visible
 
 // One 128-row Q tile of a work unit.
 struct WsTile {
@@ -78,6 +81,7 @@ struct WsTile {
   int h;         // query head
   int q0;        // sequence position of the tile's first query row
   int j0, n;     // KV tiles the tile visits: [j0, n); n = 0 when no row sees a key
+  int ns;        // kWin: and [0, ns) before them, ns < j0 (0 where the two ranges are one)
 };
 
 // Work unit: two Q tiles of a long sequence (two heads of one group over the
@@ -92,7 +96,8 @@ struct WsUnit {
   int paired;
   int packed;    // paired tiles of packed groups (row tables in the unit's slot)
   int jb;        // first KV tile loaded (shared: the smallest j0 of the tiles with work)
-  int n_all;     // K/V tiles loaded for the unit: max(n) - jb shared, n0 + n1 paired
+  int nsb;       // kWin: KV tiles [0, nsb) are loaded before it (ring position i is tile ws_ring_tile(i))
+  int n_all;     // K/V tiles loaded for the unit: nsb + max(n) - jb shared, n0 + n1 paired
   int g[2];      // packed tiles: chunk group of each tile (-1: no rows)
   WsTile t[2];
 };
@@ -109,18 +114,28 @@ constexpr uint32_t kRowAbsentKeys = ((uint32_t)kRowAbsent & 0xFFFFu) | (0xFFFFu 
 // What the MMA warp needs of a unit (the sequences' positions stay with the
 // producer and the softmax warps).
 struct MmaUnit {
-  int valid, paired, jb, n_all;
-  int j0[2], n[2];
+  int valid, paired, jb, nsb, n_all;
+  int j0[2], n[2], ns[2];
 };
+
+// KV tile at ring position i of a unit whose tiles share their K/V tiles.
+__device__ __forceinline__ int ws_ring_tile(int i, int nsb, int jb) { return i < nsb ? i : jb + i - nsb; }
 
 // KV tile range of a Q tile, [j0, n), normalised to (0, 0) when empty.  kWin:
 // the call has a sliding window (without one every visited range starts at 0).
-template <bool kWin>
-__device__ __forceinline__ void ws_tile_range(WsTile& tt) {
+template <int kWin>
+__device__ __forceinline__ void ws_tile_range(WsTile& tt, const AttnParams& p) {
   const SeqInfo& s = tt.seq;
-  tt.n = s.q_len > tt.q0 ? kv_tiles_for(s, tt.q0, kTileM) : 0;
-  tt.j0 = kWin ? kv_first_tile(s, tt.q0) : 0;
-  if (tt.n <= tt.j0) tt.n = tt.j0 = 0;
+  if constexpr (kWin) {
+    KvTiles r{0, 0, 0};
+    if (s.q_len > tt.q0) r = kv_tiles_windowed(s, tt.q0, kWin == kWinSinks ? p.sinks : 0);
+    tt.j0 = r.j0;
+    tt.n = r.n;
+    if (kWin == kWinSinks) tt.ns = r.ns;
+  } else {
+    tt.n = s.q_len > tt.q0 ? kv_tiles_for(s, tt.q0, kTileM) : 0;
+    tt.j0 = 0;
+  }
 }
 
 template <int DP>
@@ -149,13 +164,14 @@ static_assert(sizeof(WsSmem<64>) + 1024 <= 227 * 1024 && sizeof(WsSmem<128>) + 1
 // within a CTA).  Units of a chunk: the long sequences' two-tile blocks in the
 // scheduler's order, then the short tiles ((packed group, head) without a
 // window, (sequence, head) with one), heads innermost, two per unit.
-template <bool kWin, bool kPack>
+template <int kWin, bool kPack>
 __device__ __forceinline__ WsUnit ws_decode(SchedSmem& s, const AttnParams& p, unsigned long long w) {
   WsUnit u;
   u.valid = 0;
   u.paired = 0;
   u.packed = 0;
   u.jb = 0;
+  u.nsb = 0;
   u.n_all = 0;
   u.g[0] = u.g[1] = -1;
   if (!sched_seek<kWsBlockM, false, true, kPack>(s, p, w)) return u;
@@ -179,12 +195,17 @@ __device__ __forceinline__ WsUnit ws_decode(SchedSmem& s, const AttnParams& p, u
       u.t[t].seq = seq;
       u.t[t].h = head_pair ? 2 * hsel + t : hsel;
       u.t[t].q0 = head_pair ? qb * kTileM : qb * kWsBlockM + t * kTileM;
-      ws_tile_range<kWin>(u.t[t]);
+      ws_tile_range<kWin>(u.t[t], p);
     }
     // tile 0's rows come first, so its window starts no later than tile 1's
     u.jb = !kWin ? 0 : (u.t[0].n > 0 ? u.t[0].j0 : u.t[1].j0);
+    if (kWin == kWinSinks) {
+      // both tiles have the same ns where both have a gap behind it; a tile without one starts at tile 0
+      if (u.t[0].n > 0 && u.t[1].n > 0) u.jb = min(u.jb, u.t[1].j0);
+      u.nsb = min(u.jb, max(u.t[0].ns, u.t[1].ns));
+    }
     const int jend = max(u.t[0].n, u.t[1].n);
-    u.n_all = jend > u.jb ? jend - u.jb : 0;
+    u.n_all = jend > u.jb ? u.nsb + jend - u.jb : 0;
   } else {
     u.paired = 1;
     u.packed = (kPack && s.pack_on) ? 1 : 0;
@@ -209,12 +230,13 @@ __device__ __forceinline__ WsUnit ws_decode(SchedSmem& s, const AttnParams& p, u
         tt.seq = cached_seq(s, s.order[s.n_long + (int)(idx / (uint32_t)p.Hq)], p);
         tt.h = (int)(idx % (uint32_t)p.Hq);
         tt.q0 = 0;
-        ws_tile_range<kWin>(tt);   // at most KV tile 0
+        ws_tile_range<kWin>(tt, p);   // at most KV tile 0
       } else {   // odd count: no second tile
         tt.seq = SeqInfo{0, 0, 0, 0, 0, 0, kNoBound, kNoBound};
         tt.h = 0;
         tt.q0 = 0;
         tt.j0 = tt.n = 0;
+        if (kWin == kWinSinks) tt.ns = 0;
       }
     }
     u.n_all = u.t[0].n + u.t[1].n;
@@ -293,7 +315,7 @@ __device__ __forceinline__ void ws_fill_rows(uint32_t* tab, const SchedSmem& s, 
 // ---------------------------------------------------------------------------
 // warp 0: scheduler + TMA producer
 // ---------------------------------------------------------------------------
-template <int DP, bool kWin, bool kPack>
+template <int DP, int kWin, bool kPack>
 __device__ void ws_producer(WsSmem<DP>& sm, const AttnParams& p, const CUtensorMap* tm_q, const CUtensorMap* tm_k,
                             const CUtensorMap* tm_v, volatile uint32_t* abort_flag) {
   constexpr uint32_t kTileBytes = WsSmem<DP>::kTileBytes;
@@ -436,7 +458,8 @@ __device__ void ws_producer(WsSmem<DP>& sm, const AttnParams& p, const CUtensorM
       // sequence (shared), or tile 0's then tile 1's own tile (paired)
       for (int li = 0; ok && li < u.n_all; ++li) {
         const int tsel = (u.paired && !(li == 0 && u.t[0].n > 0)) ? 1 : 0;
-        const int row = u.t[tsel].seq.kv_start + (u.paired ? 0 : (u.jb + li) * kBlockN);
+        const int row =
+            u.t[tsel].seq.kv_start + (u.paired ? 0 : (kWin == kWinSinks ? ws_ring_tile(li, u.nsb, u.jb) : u.jb + li) * kBlockN);
         const int kvh = u.t[tsel].h / p.group;
         const int st = kv_cnt % kWsStages;
         const uint32_t reuse = ((kv_cnt / kWsStages) - 1) & 1;
@@ -479,7 +502,7 @@ __device__ void ws_producer(WsSmem<DP>& sm, const AttnParams& p, const CUtensorM
 // ---------------------------------------------------------------------------
 // warp 1 (one thread): MMA issuer
 // ---------------------------------------------------------------------------
-template <typename DT, int DP, bool kWin>
+template <typename DT, int DP, int kWin>
 __device__ void ws_mma(WsSmem<DP>& sm, const AttnParams& p, uint32_t tmem, volatile uint32_t* abort_flag) {
   using Tr = DTypeTraits<DT>;
   constexpr uint32_t idesc_qk = umma_idesc_f16(Tr::kBF16, kTileM, kBlockN, false);
@@ -503,11 +526,13 @@ __device__ void ws_mma(WsSmem<DP>& sm, const AttnParams& p, uint32_t tmem, volat
     x.valid = w.valid;
     x.paired = w.paired;
     x.jb = kWin ? w.jb : 0;
+    x.nsb = kWin == kWinSinks ? w.nsb : 0;
     x.n_all = w.n_all;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       x.j0[t] = kWin ? w.t[t].j0 : 0;
       x.n[t] = w.t[t].n;
+      x.ns[t] = kWin == kWinSinks ? w.t[t].ns : 0;
     }
     __syncwarp();   // every lane has read the unit before the slot is released
     if (leader) mbar_arrive(&sm.item_empty[slot]);
@@ -538,8 +563,10 @@ __device__ void ws_mma(WsSmem<DP>& sm, const AttnParams& p, uint32_t tmem, volat
     }
     if (!u.paired) {
       // ---- one long-sequence block: both tiles share every K/V tile ----
-      // KV tiles jb .. jb + n - 1 are ring positions kv_cnt ..; tile t visits [j0_t, n_t).
-      const int n = u.n_all, jb = u.jb;
+      // KV tiles ws_ring_tile(0 .. n - 1) are ring positions kv_cnt ..; tile t visits [0, ns_t) and [j0_t, n_t).
+      const int n = u.n_all;
+      auto ring = [&](int i) { return kWin == kWinSinks ? ws_ring_tile(i, u.nsb, u.jb) : u.jb + i; };
+      auto visits = [&](int t, int j) { return j < u.n[t] && (j >= u.j0[t] || (kWin == kWinSinks && j < u.ns[t])); };
       const int qs = q_cnt % kQSlots;
       if (!WS_WAIT_WARP(&sm.q_full[qs], (q_cnt / kQSlots) & 1)) break;
       ++q_cnt;
@@ -550,7 +577,7 @@ __device__ void ws_mma(WsSmem<DP>& sm, const AttnParams& p, uint32_t tmem, volat
         const uint32_t ks = k_lo0 + (kv_cnt % kWsStages) * kStep;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (u.n[t] > 0 && u.j0[t] == jb) {
+          if (visits(t, ring(0))) {
             issue_qk<DP>(leader, tS[t], q_lo0 + t * kStep, ks, idesc_qk);
             umma_commit_if(leader, &sm.s_full[t]);
           }
@@ -560,25 +587,25 @@ __device__ void ws_mma(WsSmem<DP>& sm, const AttnParams& p, uint32_t tmem, volat
       }
       bool ok = true;
       for (int i = 0; i < n && ok; ++i) {
-        const int j = jb + i;
+        const int j = ring(i), jn = ring(i + 1);
         const uint32_t c = kv_cnt + i, cn = c + 1;
         const int st = c % kWsStages, stn = cn % kWsStages;
         if (!WS_WAIT_WARP(&sm.v_full[st], (c / kWsStages) & 1)) { ok = false; break; }
         const uint32_t vs = v_lo0 + st * kStep;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (j >= u.j0[t] && j < u.n[t]) {
+          if (visits(t, j)) {
             const uint32_t par = p_cnt[t] & 1;
             ++p_cnt[t];
             if (!WS_WAIT_WARP(&sm.p_lo[t], par)) { ok = false; break; }
             tc_fence_after();
-            issue_pv<0, 4>(leader, tO[t], tS[t], vs, idesc_pv, j > u.j0[t]);
+            issue_pv<0, 4>(leader, tO[t], tS[t], vs, idesc_pv, j > (kWin == kWinSinks && u.ns[t] > 0 ? 0 : u.j0[t]));
             if (!WS_WAIT_WARP(&sm.p_hi[t], par)) { ok = false; break; }
             tc_fence_after();
             issue_pv<4, 8>(leader, tO[t], tS[t], vs, idesc_pv, true);
             umma_commit_if(leader, &sm.o_full[t]);
           }
-          if (j + 1 >= u.j0[t] && j + 1 < u.n[t]) {   // the tile's next S (or its first)
+          if ((kWin != kWinSinks || i + 1 < n) && visits(t, jn)) {   // the tile's next S (or its first)
             if (!WS_WAIT_WARP(&sm.k_full[stn], (cn / kWsStages) & 1)) { ok = false; break; }
             tc_fence_after();
             issue_qk<DP>(leader, tS[t], q_lo0 + t * kStep, k_lo0 + stn * kStep, idesc_qk);
@@ -723,23 +750,25 @@ __device__ __forceinline__ void ws_exp_chunk(const uint32_t* sr, uint32_t* pk, f
   }
 }
 
+// The lowest n bits set (none for n <= 0, all from n = 32 on).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u); }
+
 // Softmax of one KV tile for one row (the calling thread's TMEM lane): S from
 // TMEM, online max / sums, P (rounded to the input type) back over S in two
 // halves of 64 keys, lazy O rescale.  `partial` (warp-uniform): some row of
 // the warp may not see all 128 keys; columns outside the row's visible keys
 // are masked, and when no row of the warp sees a key in the second half, its
 // exponentials are skipped and zero P is stored there.  j: position of the KV
-// tile among the tiles this Q tile visits (row_first / row_last are counted
-// from the first of them).  Returns false when a wait gave up.
+// tile among the tiles this Q tile visits.  Returns false when a wait gave up.
 // row_first / row_last: the row's first and last visible key (row_last < 0 for
-// rows past the sequence); kWin: a window may bound the keys from below.
-template <typename DT, int DP, bool kWin>
+// rows past the sequence); kWin: a window may bound the keys from below, and
+// keys before row_sink are visible too.  kv0: the tile's first key.
+template <typename DT, int DP, int kWin>
 __device__ __forceinline__ bool ws_softmax_tile(WsSmem<DP>& sm, const AttnParams& p, volatile uint32_t* abort_flag,
-                                                uint32_t tS, uint32_t tO, int tile, int j, uint32_t o_cnt,
-                                                bool partial, int row_first, int row_last, float sl2,
+                                                uint32_t tS, uint32_t tO, int tile, int j, int kv0, uint32_t o_cnt,
+                                                bool partial, int row_first, int row_last, int row_sink, float sl2,
                                                 float& m_run, float2& lr_a, float2& lr_b, float2& le_a, float2& le_b) {
   const int lane = threadIdx.x & 31;
-  const int kv0 = j * kBlockN;
   uint32_t sr[128];
 #pragma unroll
   for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, sr + 32 * c);
@@ -751,9 +780,20 @@ __device__ __forceinline__ bool ws_softmax_tile(WsSmem<DP>& sm, const AttnParams
     const int lim = row_last - kv0;
     if constexpr (kWin) {   // sliding window: keys before the row's window too
       const int lo = row_first - kv0;
+      if constexpr (kWin == kWinSinks) {   // a word of bits for 32 columns: in the window, or before row_sink
+        const int few = row_sink - kv0;
 #pragma unroll
-      for (int c = 0; c < 128; ++c)
-        if (c > lim || c < lo) sr[c] = __float_as_uint(-INFINITY);
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t seen = (low_bits(lim + 1 - 32 * w) & ~low_bits(lo - 32 * w)) | low_bits(few - 32 * w);
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (!(seen >> c & 1)) sr[32 * w + c] = __float_as_uint(-INFINITY);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c > lim || c < lo) sr[c] = __float_as_uint(-INFINITY);
+      }
     } else {
 #pragma unroll
       for (int c = 0; c < 128; ++c)
@@ -788,7 +828,7 @@ __device__ __forceinline__ bool ws_softmax_tile(WsSmem<DP>& sm, const AttnParams
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     if (partial && half == 1 &&
-        __all_sync(0xffffffffu, row_last - kv0 < 2 * 32)) {
+        __all_sync(0xffffffffu, (kWin == kWinSinks ? max(row_last, row_sink - 1) : row_last) - kv0 < 2 * 32)) {
       // no row of the warp sees keys 64..127: their P is zero
       uint32_t pk[16];
 #pragma unroll
@@ -935,7 +975,7 @@ __device__ __forceinline__ bool ws_packed_tile(WsSmem<DP>& sm, const AttnParams&
 // ---------------------------------------------------------------------------
 // warps 4-11: softmax + epilogue, tile = warp / 4 - 1
 // ---------------------------------------------------------------------------
-template <typename DT, int DP, bool kWin, bool kPack>
+template <typename DT, int DP, int kWin, bool kPack>
 __device__ void ws_softmax(WsSmem<DP>& sm, const AttnParams& p, uint32_t tmem, int tile,
                            volatile uint32_t* abort_flag) {
   using Tr = DTypeTraits<DT>;
@@ -976,23 +1016,24 @@ __device__ void ws_softmax(WsSmem<DP>& sm, const AttnParams& p, uint32_t tmem, i
     float2 lr_a = make_float2(0.f, 0.f), lr_b = lr_a;   // rounded-P sums (normalise O)
     float2 le_a = lr_a, le_b = lr_a;                     // exact sums (LSE)
     bool ok = true;
-    // the row's visible keys (none for rows past the sequence), counted from the
-    // first KV tile the Q tile visits; the loop runs over the nv tiles it visits
-    const int base = kWin ? tt.j0 * kBlockN : 0;
-    const int row_last = row < rows ? seq_last_key(s, qpos) - base : -1;
-    const int row_first = kWin ? seq_first_key(s, qpos) - base : 0;
-    const int tile_last = seq_last_key(s, qt0) - base;   // smallest last key of the tile's rows
-    const int nv = ni - (kWin ? tt.j0 : 0);
+    // the row's visible keys (none for rows past the sequence); the loop runs over the nv
+    // tiles the Q tile visits
+    const int row_last = row < rows ? seq_last_key(s, qpos) : -1;
+    const int row_first = kWin ? seq_first_key(s, qpos) : 0;
+    const int row_sink = kWin == kWinSinks && row < rows ? sink_end(s, qpos, p.sinks) : 0;
+    const int tile_last = seq_last_key(s, qt0);   // smallest last key of the tile's rows
+    const int ns = kWin == kWinSinks ? tt.ns : 0, j0 = kWin ? tt.j0 : 0;
+    const int nv = ns + ni - j0;
     for (int j = 0; j < nv; ++j) {
       if (!WS_WAIT_WARP(&sm.s_full[tile], s_cnt & 1)) { ok = false; break; }
       ++s_cnt;
       tc_fence_after();
       // partial tile: a row's visible keys end (sequence end, causal diagonal,
       // window) inside it, or (window) start inside it for a row of this warp
-      const int kv0 = j * kBlockN;
+      const int kv0 = (kWin == kWinSinks ? ws_ring_tile(j, ns, j0) : j0 + j) * kBlockN;
       const bool masked = kv0 + kBlockN - 1 > tile_last || (kWin && __any_sync(0xffffffffu, row_first > kv0));
-      ok = ws_softmax_tile<DT, DP, kWin>(sm, p, abort_flag, tS, tO, tile, j, o_cnt, masked, row_first, row_last, sl2,
-                                         m_run, lr_a, lr_b, le_a, le_b);
+      ok = ws_softmax_tile<DT, DP, kWin>(sm, p, abort_flag, tS, tO, tile, j, kv0, o_cnt, masked, row_first, row_last,
+                                         row_sink, sl2, m_run, lr_a, lr_b, le_a, le_b);
       if (!ok) break;
     }
     if (!ok) break;
@@ -1034,11 +1075,11 @@ __device__ void ws_softmax(WsSmem<DP>& sm, const AttnParams& p, uint32_t tmem, i
   }
 }
 
-template <typename DT, int DP, bool kWin, bool kPack>
+template <typename DT, int DP, int kWin, bool kPack>
 __global__ void __launch_bounds__(kWsThreads, 1)
     attn_fwd_ws_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
-  static_assert(!(kWin && kPack), "short sequences are packed only without a window");
+  static_assert(!(kWin != 0 && kPack), "short sequences are packed only without a window");
   extern __shared__ uint8_t smem_raw[];
   WsSmem<DP>& sm = *reinterpret_cast<WsSmem<DP>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
