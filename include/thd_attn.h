@@ -505,6 +505,78 @@ int thd_attn_paged(const void* q, const void* k_cache, const void* v_cache, cons
                    void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * thd_attn_paged_window — thd_attn_paged with a window, with first tokens that stay
+ * visible, and with the weights that cached keys got.
+ *
+ * New token i of n of a sequence with L keys stands at key L - n + i.  With
+ * window_left >= 0 it sees key j iff j <= L - n + i and
+ *     j >= L - n + i - window_left  or  j < sink_tokens.
+ * Keys that no new token sees are not read, nor the table's entries of pages that
+ * hold only such keys: these pages may be given away.
+ * window_left  >= -1; -1: no window, and sink_tokens (>= 0) has no effect.  With a
+ *              tree mask it must be -1 (THD_ERR_UNSUPPORTED).
+ * key_weights  device fp32, or NULL: the weight of token t of head h of page g is at
+ *              g * strides[0] + t * strides[1] + h * strides[2].  For each key j < L of a
+ *              sequence with new tokens and key/value head h
+ *                  w = (j < L - n ? w : 0) + sum of exp(s_j - lse)
+ *              over the sequence's new tokens that see it and the query heads of h.
+ *              The sums are taken in fp32 and in a fixed order.  Keys whose
+ *              table entry is outside [0, num_pages) have none.  No two keys may
+ *              share a place (a page that several sequences of the batch name gets
+ *              unspecified weights).  Needs lse.
+ * weight_strides  host int64 [3], >= 0; not read when key_weights is NULL.
+ * Other arguments and errors as thd_attn_paged, and THD_ERR_ARG for those above.
+ */
+int thd_attn_paged_window(const void* q, const void* k_cache, const void* v_cache, const int64_t* cache_strides,
+                          int num_pages, int page_size, const int32_t* page_table, int64_t page_table_stride,
+                          int max_pages, const int32_t* kv_lens, const int32_t* cu_seqlens_q,
+                          const int32_t* cu_seqlens_q_padded, int batch_size, int max_seqlen_q,
+                          const int64_t* tree_mask, int tree_words, int window_left, int sink_tokens,
+                          float* key_weights, const int64_t* weight_strides, float softmax_scale, void* out, float* lse,
+                          int total_tokens, int num_heads_q, int num_heads_kv, int head_dim, int dtype,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * thd_kv_evict — keys and values of a paged cache dropped by the attention weight that
+ * they got (thd_attn_paged_window's key_weights), in place or into other pages.
+ *
+ * Sequence b has L = kv_lens[b] keys, of which K = min(L, max(keep_lens[b], 0), max_keep)
+ * stay for each key/value head: the first S = min(sink_tokens, K), the last
+ * R = min(recent_tokens, K - S), and of the others the K - S - R with the greatest
+ * weights; of equal weights the lower slots (NaN counts above everything, -0 as 0).
+ * Each head keeps its own.  They keep their order, and their keys, values and weights go
+ * to slots 0 .. K - 1; slots from K on are left as they were.
+ *
+ * k_cache, v_cache, cache_strides, num_pages, page_size, page_table,
+ * page_table_stride, max_pages  as in thd_kv_append; L is at most max_pages * page_size.
+ *              A key whose entry is outside [0, num_pages) counts with weight 0 and is
+ *              not moved.
+ * key_weights, weight_strides  as in thd_attn_paged_window.
+ * new_page_table, new_page_table_stride, new_max_pages  int32 table, laid out as page_table, of the
+ *              pages that the kept keys go to; K is at most new_max_pages * page_size.  They
+ *              must be none of the pages that page_table names for any key of the
+ *              batch; the old pages are left as they were, so several sequences may
+ *              name them.  NULL, or page_table itself: the old pages, in place; no two
+ *              sequences of the batch may share one then.
+ * kv_lens, keep_lens  device int32 [>= batch_size].
+ * sink_tokens, recent_tokens  >= 0.
+ * kept         device int32 [batch_size, Hkv, max_keep]: written with the old slots of the
+ *              kept keys, ascending, then -1.
+ * max_keep     >= 0.
+ * new_lens     device int32 [batch_size]: written with K.  Not kv_lens nor keep_lens.
+ * head_dim     a multiple of 8 in [8, 128].
+ * Nothing is read from the device on the host, so a captured call may be replayed with
+ * other lengths, tables and weights in the same buffers.
+ * Errors: THD_ERR_ARG, THD_ERR_UNSUPPORTED, THD_ERR_CUDA.
+ */
+int thd_kv_evict(void* k_cache, void* v_cache, const int64_t* cache_strides, float* key_weights,
+                 const int64_t* weight_strides, int num_pages, int page_size, const int32_t* page_table,
+                 int64_t page_table_stride, int max_pages, const int32_t* new_page_table,
+                 int64_t new_page_table_stride, int new_max_pages, const int32_t* kv_lens, const int32_t* keep_lens,
+                 int batch_size, int sink_tokens, int recent_tokens, int32_t* kept, int max_keep, int32_t* new_lens,
+                 int num_heads_kv, int head_dim, int dtype, void* stream);
+
+/*
  * thd_set_wait_limit_ns — the time limit of one pipeline wait inside the
  * attention kernels (forward, windowed forward, no-allocation forward,
  * backward, and thd_attn_paged where it waits), for calls made after it on any

@@ -171,9 +171,13 @@ def evict(caches, weights, page_table, kv_lens, keep_lens, new_page_table, batch
         lens.append(K)
         kept.append([])
         at, to = pages_of(page_table, b, L, page), pages_of(new, b, K, page)
+        real = lambda x: (x >= 0) & (x < weights.shape[0])  # noqa: E731
         for h in range(hkv):
-            slots = evict_keep(np.asarray(weights)[at[0], at[1], h], L, K, sinks, recent)
+            # a slot of no page has no weight, and neither goes nor comes
+            w = np.where(real(at[0]), np.asarray(weights)[np.where(real(at[0]), at[0], 0), at[1], h], 0.0)
+            slots = evict_keep(w, L, K, sinks, recent)
             kept[-1].append(slots)
+            f, go = np.array(slots, int), real(to[0]) & real(at[0][slots])
             for x, y in zip(got, src):
-                x[to[0], to[1], h] = np.asarray(y)[at[0][slots], at[1][slots], h]
+                x[to[0][go], to[1][go], h] = np.asarray(y)[at[0][f[go]], at[1][f[go]], h]
     return got[:-1], got[-1], lens, kept

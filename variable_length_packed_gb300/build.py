@@ -23,7 +23,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 STAMP = LIB + ".sha256"
 
 SOURCES = ["thd_attn.cu", "padding_mask.cu", "attn_noalloc.cu", "attn_merge.cu", "qk_norm_rope.cu",
-           "attn_paged.cu"]
+           "attn_paged.cu", "kv_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

@@ -36,6 +36,7 @@
 
 #include "../../include/thd_attn.h"
 #include "attn_paged_common.cuh"
+#include "attn_paged_weights.cuh"
 #include "attn_paged_wide.cuh"
 
 namespace thd {
@@ -45,7 +46,6 @@ void wait_settings(uint64_t* limit_ns, uint32_t* check_mask, uint32_t* inject);
 
 namespace {
 
-constexpr int kNarrowRows = 16;      // rows of a tile
 constexpr int kWarps = 4;            // warps of a CTA, 16 keys of the unit each
 constexpr int kWarpKeys = kUnit / kWarps;
 constexpr int kStages = 3;           // units in flight per warp
@@ -67,22 +67,6 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t* r) {
                : "r"(addr)
                : "memory");
 }
-template <typename DT>
-__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1);
-template <>
-__device__ __forceinline__ void mma16816<__nv_bfloat16>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-template <>
-__device__ __forceinline__ void mma16816<__half>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 // Shared memory of a CTA: each warp's ring of key and value tiles (16 rows of DP values,
 // 16-byte chunks XORed with the row so that eight rows of one column of chunks lie in
 // different banks); at a tile's end the warps' sums and outputs take its place.
@@ -94,7 +78,7 @@ struct PagedSmem {
   static constexpr int kBytes = kRing > kJoin ? kRing : kJoin;
 };
 
-template <typename DT, int DP>
+template <typename DT, int DP, bool kWin>
 __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedArgs p) {
   constexpr int MT = kNarrowRows;
   constexpr int kKSteps = DP / 16;      // of the score product
@@ -109,7 +93,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  find_share<kWarps * 32>(p, MT, &share);
+  find_share<kWarps * 32>(p, [&](int b) { return seq_work<kWin>(p, b, MT).units; }, &share);
   if (tid == 0) {
     p.splits[blockIdx.x].n = 0;
     p.status[blockIdx.x] = 0u;
@@ -122,22 +106,24 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
 
   PieceWalk walk(share);
   Piece x;
-  while (walk.next<MT>(p, x)) {
+  while (walk.next<MT, kWin>(p, x)) {
     // ---- keys and values: this warp's 16 keys of unit blk0 + i ----
     const int32_t* table = p.table + (long long)x.seq * p.table_stride;
     // lane l < 16 holds the offset of key l, lane 16 + l that of value l
     auto offset_of = [&](int i) {
-      return i < x.steps ? cache_offset(p, x, table, (x.blk0 + i) * kUnit + warp * kWarpKeys + (lane & 15), lane >= 16)
+      return i < x.steps ? cache_offset<kWin>(p, x, table,
+                                              unit_of<kWin>(x, x.blk0 + i) * kUnit + warp * kWarpKeys + (lane & 15),
+                                              lane >= 16)
                          : 0ll;
     };
     auto issue = [&](int i, int stage, long long off) {
       if (i < x.steps) {
-        const int first = (x.blk0 + i) * kUnit + warp * kWarpKeys;
+        const int first = unit_of<kWin>(x, x.blk0 + i) * kUnit + warp * kWarpKeys;
         const uint32_t dst = ring + stage * (2 * kTileBytes);
 #pragma unroll
         for (int c = 0; c < kCopies; ++c) {
           const int key = c * kLaneKeys + copy_key;
-          const bool take = copy_in && first + key < x.key_end;
+          const bool take = copy_in && !key_hidden<kWin>(x, first + key);
           const uint32_t at = key * (DP * 2) + ((copy_chunk ^ (key & 7)) << 4);
           const long long ko = __shfl_sync(0xffffffffu, off, key), vo = __shfl_sync(0xffffffffu, off, 16 + key);
           const int col = take ? copy_chunk * 8 : 0;
@@ -195,7 +181,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
         next_off = offset_of(i + kStages);
       }
       const uint32_t kt = ring + stage * (2 * kTileBytes), vt = kt + kTileBytes;
-      const int unit0 = (x.blk0 + i) * kUnit;
+      const int unit0 = unit_of<kWin>(x, x.blk0 + i) * kUnit;
       // ---- scores ----
       float c[2][4];
 #pragma unroll
@@ -211,8 +197,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
         mma16816<DT>(c[1], qf[k], kb[2], kb[3]);
       }
       // ---- visibility ----
-      // some key of the unit may be hidden from some row
-      const bool cut = unit0 + kUnit > min(p.tree ? x.past : x.past + 1, x.s.kv_len);
+      const bool cut = unit_cut<kWin>(p, x, unit0);
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -220,7 +205,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
       if (cut) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const uint64_t all = token[hh] >= 0 ? seen_keys(p, x, token[hh], unit0, tree_word(p, x, token[hh])) : 0ull;
+          const uint64_t all = token[hh] >= 0 ? seen_keys<kWin>(p, x, token[hh], unit0, tree_word(p, x, token[hh])) : 0ull;
           const uint32_t seen = (uint32_t)(all >> (warp * kWarpKeys)) >> qc;   // this lane's: bits 0, 1, 8, 9
           if (!(seen & 1)) c[0][2 * hh] = -INFINITY;
           if (!(seen & 2)) c[0][2 * hh + 1] = -INFINITY;
@@ -480,7 +465,7 @@ constexpr size_t kStatusAt = 256, kSplitAt = kStatusAt + kMaxCtas * sizeof(uint3
 constexpr size_t kPartAt = kSplitAt + kMaxCtas * sizeof(Split);
 constexpr size_t part_bytes(int dp) { return (size_t)kMaxCtas * 2 * kMaxRows * (dp + 3) * 4; }
 
-template <typename DT, int DP, int MT>
+template <typename DT, int DP, int MT, bool kWin>
 int launch_paged(PagedArgs& p, char* ws, int sms, cudaStream_t st) {
   p.call_status = reinterpret_cast<uint32_t*>(ws + 8);
   p.status = reinterpret_cast<uint32_t*>(ws + kStatusAt);
@@ -490,12 +475,12 @@ int launch_paged(PagedArgs& p, char* ws, int sms, cudaStream_t st) {
   const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
   static SmemGrant grant;
   if constexpr (MT == kWideRows) {
-    auto kern = attn_paged_wide_kernel<DT, DP>;
+    auto kern = attn_paged_wide_kernel<DT, DP, kWin>;
     constexpr int smem = (int)sizeof(WideSmem<DP>) + 1024;
     if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
     kern<<<grid, kWideThreads, smem, st>>>(p);
   } else {
-    auto kern = attn_paged_kernel<DT, DP>;
+    auto kern = attn_paged_kernel<DT, DP, kWin>;
     constexpr int smem = PagedSmem<DP>::kBytes;
     if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
     kern<<<grid, kWarps * 32, smem, st>>>(p);
@@ -510,23 +495,34 @@ int launch_paged(PagedArgs& p, char* ws, int sms, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<DT, DP, MT>, static_cast<const PagedArgs>(p)) == cudaSuccess
-             ? THD_OK
-             : THD_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<DT, DP, MT>, static_cast<const PagedArgs>(p)) != cudaSuccess)
+    return THD_ERR_CUDA;
+  if (p.key_weights) {
+    attn_key_weights_kernel<DT, DP, kWin><<<4 * sms, kWeightWarps * 32, 0, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;
+  }
+  return THD_OK;
 }
 
 // Tiles of 16 rows where no sequence has more, else of 128.  120000 keys of 16 sequences, 32 + 8 heads of 128,
 // bf16, in us: 16 rows 89 narrow; 20 rows 94 wide, against 124 in narrow tiles of 32; 64 rows 98, against 229 in
 // two such tiles.  Heads of 64 in fp16: 32 rows 62 and 70, 36 rows 68 and 117.  Wide tiles of 4 rows (a
 // decoding batch called without the hint) cost 324 where narrow ones cost 317.
+template <typename DT, bool kWin>
+int launch_paged_rows(PagedArgs& p, long long row_hint, char* ws, int sms, cudaStream_t st) {
+  if (p.d > 64) {
+    if (row_hint <= kNarrowRows) return launch_paged<DT, 128, kNarrowRows, kWin>(p, ws, sms, st);
+    return launch_paged<DT, 128, kWideRows, kWin>(p, ws, sms, st);
+  }
+  if (row_hint <= kNarrowRows) return launch_paged<DT, 64, kNarrowRows, kWin>(p, ws, sms, st);
+  return launch_paged<DT, 64, kWideRows, kWin>(p, ws, sms, st);
+}
+
+// A window has kernels of its own: a call without one does what it did.
 template <typename DT>
 int launch_paged_of(PagedArgs& p, long long row_hint, char* ws, int sms, cudaStream_t st) {
-  if (p.d > 64) {
-    if (row_hint <= kNarrowRows) return launch_paged<DT, 128, kNarrowRows>(p, ws, sms, st);
-    return launch_paged<DT, 128, kWideRows>(p, ws, sms, st);
-  }
-  if (row_hint <= kNarrowRows) return launch_paged<DT, 64, kNarrowRows>(p, ws, sms, st);
-  return launch_paged<DT, 64, kWideRows>(p, ws, sms, st);
+  if (p.win_left >= 0) return launch_paged_rows<DT, true>(p, row_hint, ws, sms, st);
+  return launch_paged_rows<DT, false>(p, row_hint, ws, sms, st);
 }
 
 }  // namespace
@@ -539,11 +535,11 @@ size_t thd_attn_paged_workspace_size(int head_dim) {
   return thd::kPartAt + thd::part_bytes(head_dim > 64 ? 128 : 64);
 }
 
-int thd_attn_paged(const void* q, const void* k_cache, const void* v_cache, const int64_t* cache_strides,
+int thd_attn_paged_window(const void* q, const void* k_cache, const void* v_cache, const int64_t* cache_strides,
                    int num_pages, int page_size, const int32_t* page_table, int64_t page_table_stride, int max_pages,
                    const int32_t* kv_lens, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_q_padded,
-                   int batch_size, int max_seqlen_q, const int64_t* tree_mask, int tree_words, float softmax_scale,
-                   void* out, float* lse, int total_tokens, int num_heads_q, int num_heads_kv, int head_dim, int dtype,
+                   int batch_size, int max_seqlen_q, const int64_t* tree_mask, int tree_words, int window_left,
+                   int sink_tokens, float* key_weights, const int64_t* weight_strides, float softmax_scale, void* out, float* lse, int total_tokens, int num_heads_q, int num_heads_kv, int head_dim, int dtype,
                    void* workspace, size_t workspace_bytes, void* stream) {
   using namespace thd;
   if (batch_size < 0 || max_seqlen_q < 0 || total_tokens < 0) return THD_ERR_ARG;
@@ -558,9 +554,17 @@ int thd_attn_paged(const void* q, const void* k_cache, const void* v_cache, cons
     return THD_ERR_UNSUPPORTED;
   if ((long long)num_heads_q * head_dim >= (1ll << 31)) return THD_ERR_UNSUPPORTED;
   if (tree_mask && (tree_words < 1 || tree_words > (1 << 20))) return THD_ERR_ARG;
+  if (window_left < -1 || sink_tokens < 0) return THD_ERR_ARG;
+  // where drafted tokens stand to one another only their mask says, so a window has no meaning for them
+  if (window_left >= 0 && tree_mask) return THD_ERR_UNSUPPORTED;
   if (!cache_strides || page_table_stride < max_pages) return THD_ERR_ARG;
   for (int i = 0; i < 6; ++i)
     if (cache_strides[i] < 0 || cache_strides[i] % 8 != 0) return THD_ERR_ARG;
+  if (key_weights) {
+    if (!weight_strides || !lse || !on4(key_weights)) return THD_ERR_ARG;
+    for (int i = 0; i < 3; ++i)
+      if (weight_strides[i] < 0) return THD_ERR_ARG;
+  }
   if (total_tokens == 0) return THD_OK;
   if (!q || !out || !on16(q) || !on16(out) || !on4(lse)) return THD_ERR_ARG;
   if (!on4(page_table) || !on4(kv_lens) || !on4(cu_seqlens_q) || !on4(cu_seqlens_q_padded) ||
@@ -603,6 +607,15 @@ int thd_attn_paged(const void* q, const void* k_cache, const void* v_cache, cons
   p.Hkv = num_heads_kv;
   p.group = group;
   p.d = head_dim;
+  // a window of as many keys as the table has room for hides none
+  p.win_left = window_left < (long long)max_pages * page_size ? window_left : -1;
+  p.sinks = p.win_left >= 0 ? sink_tokens : 0;
+  if (key_weights && batch_size > 0 && max_pages > 0) {
+    p.key_weights = key_weights;
+    p.w_page = weight_strides[0];
+    p.w_token = weight_strides[1];
+    p.w_head = weight_strides[2];
+  }
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   wait_settings(&p.wait_limit_ns, &p.wait_check_mask, &p.inject_wait);
   long long longest = max_seqlen_q > 0 && max_seqlen_q < total_tokens ? max_seqlen_q : total_tokens;
@@ -611,6 +624,18 @@ int thd_attn_paged(const void* q, const void* k_cache, const void* v_cache, cons
                                               static_cast<cudaStream_t>(stream))
              : launch_paged_of<__half>(p, longest * group, static_cast<char*>(workspace), sms,
                                        static_cast<cudaStream_t>(stream));
+}
+
+int thd_attn_paged(const void* q, const void* k_cache, const void* v_cache, const int64_t* cache_strides,
+                   int num_pages, int page_size, const int32_t* page_table, int64_t page_table_stride, int max_pages,
+                   const int32_t* kv_lens, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_q_padded,
+                   int batch_size, int max_seqlen_q, const int64_t* tree_mask, int tree_words, float softmax_scale,
+                   void* out, float* lse, int total_tokens, int num_heads_q, int num_heads_kv, int head_dim, int dtype,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  return thd_attn_paged_window(q, k_cache, v_cache, cache_strides, num_pages, page_size, page_table, page_table_stride,
+                               max_pages, kv_lens, cu_seqlens_q, cu_seqlens_q_padded, batch_size, max_seqlen_q,
+                               tree_mask, tree_words, -1, 0, nullptr, nullptr, softmax_scale, out, lse, total_tokens,
+                               num_heads_q, num_heads_kv, head_dim, dtype, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

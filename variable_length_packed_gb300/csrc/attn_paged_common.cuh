@@ -20,8 +20,25 @@ namespace thd {
 namespace {
 
 constexpr int kUnit = 64;            // keys of a unit
+constexpr int kNarrowRows = 16;      // rows of a narrow tile
 constexpr int kMaxCtas = 320;        // CTAs of a launch at most (two on each of up to 160 SMs)
 
+template <typename DT>
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 // A tile that goes on from one CTA to the next: its rows, and the CTAs that share it.
 struct alignas(16) Split {
   int n;        // CTAs (0: no such tile)
@@ -49,19 +66,34 @@ struct PagedArgs {
   uint64_t wait_limit_ns;
   uint32_t wait_check_mask, inject_wait;
   Split* splits;       // [ctas]
+  float* key_weights;  // weights that the keys got, or null
+  long long w_page, w_token, w_head;                                          // elements
   long long table_stride, k_page, k_token, k_head, v_page, v_token, v_head;   // elements
   int num_pages, page_size, max_pages;
   int tree_words;
+  int win_left, sinks; // kWin: keys before its own slot that a token sees, and first keys that it sees besides
   int B, T, Hq, Hkv, group, d;
   float scale_log2;
 };
 
 // One sequence of the batch, clamped to the buffers.
 struct SeqWork {
-  int q_start, q_len, kv_len, tiles, blocks;
+  int q_start, q_len, kv_len, tiles;
+  int blocks;           // units of a tile: all of the sequence's, or (kWin) as many as a tile's rows see at most
   long long units;
 };
 
+// Units that hold first keys which every token sees (kWin).
+__device__ __forceinline__ int sink_units(const PagedArgs& p, int kv_len) {
+  return (min(p.sinks, kv_len) + kUnit - 1) / kUnit;
+}
+
+// First key of the window of new token `tok`.
+__device__ __forceinline__ int window_first(const PagedArgs& p, int past, int tok) {
+  return (int)max(0ll, (long long)past + tok - p.win_left);
+}
+
+template <bool kWin>
 __device__ __forceinline__ SeqWork seq_work(const PagedArgs& p, int b, int rows_per_tile) {
   SeqWork s;
   const int c0 = p.cu[b], c1 = p.cu[b + 1];
@@ -77,6 +109,11 @@ __device__ __forceinline__ SeqWork seq_work(const PagedArgs& p, int b, int rows_
   const long long rows = ql * p.group;
   s.tiles = (int)((rows + rows_per_tile - 1) / rows_per_tile);
   s.blocks = (s.kv_len + kUnit - 1) / kUnit;
+  if constexpr (kWin) {
+    // a tile's tokens lie (rows - 1) / group apart at most, so its windows cover `span` keys one after another
+    const long long span = (long long)p.win_left + (rows_per_tile - 1 + p.group - 1) / p.group + 1;
+    s.blocks = (int)min((long long)s.blocks, sink_units(p, s.kv_len) + (span + kUnit - 2) / kUnit + 1);
+  }
   s.units = (long long)s.tiles * s.blocks * p.Hkv;
   return s;
 }
@@ -92,14 +129,15 @@ struct Share {
 
 __device__ __forceinline__ long long share_begin(long long total, int ctas, int c) { return total * c / ctas; }
 
-template <int kThreads>
-__device__ void find_share(const PagedArgs& p, int rows_per_tile, Share* out) {
+// units(b): those of sequence b.
+template <int kThreads, typename Units>
+__device__ void find_share(const PagedArgs& p, Units units, Share* out) {
   __shared__ long long warp_sum[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_work(p, b, rows_per_tile).units;
+  for (int b = b0; b < b1; ++b) mine += units(b);
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -130,7 +168,7 @@ __device__ void find_share(const PagedArgs& p, int rows_per_tile, Share* out) {
       long long base = excl;
       int b = b0;
       for (; b < b1; ++b) {
-        const long long u = seq_work(p, b, rows_per_tile).units;
+        const long long u = units(b);
         if (begin < base + u) break;
         base += u;
       }
@@ -156,6 +194,9 @@ struct Piece {
   int past;             // keys before the new tokens (negative: fewer keys than tokens)
   int key_end;          // keys from here on no row of the tile sees
   int blk0, steps;      // units that some row sees (steps may be 0)
+  // kWin: unit i is unit_of(i); the first row's window begins at win_lo and the last one's at win_hi; every row
+  // sees the keys before `few` that it could see without a window
+  int lead, skip, win_lo, win_hi, few;
   bool whole;           // all of the tile's units are in this piece
   bool first;           // the CTA's first piece
   long long tile_end;   // first unit after the tile's
@@ -168,10 +209,10 @@ struct PieceWalk {
   __device__ __forceinline__ explicit PieceWalk(const Share& share)
       : u(share.begin), end(share.end), base(share.seq_base), begin(share.begin), b(share.seq) {}
 
-  template <int MT>
+  template <int MT, bool kWin>
   __device__ __forceinline__ bool next(const PagedArgs& p, Piece& x) {
     while (u < end) {
-      x.s = seq_work(p, b, MT);
+      x.s = seq_work<kWin>(p, b, MT);
       if (u - base >= x.s.units) {
         base += x.s.units;
         ++b;
@@ -189,7 +230,19 @@ struct PieceWalk {
       x.rows = (int)min((long long)MT, (long long)x.s.q_len * p.group - x.row0);
       x.past = x.s.kv_len - x.s.q_len;
       x.key_end = p.tree ? x.s.kv_len : min(x.s.kv_len, max(0, x.past + (x.row0 + x.rows - 1) / p.group + 1));
-      x.steps = min(nblk, max(0, (x.key_end + kUnit - 1) / kUnit - x.blk0));
+      int last = (x.key_end + kUnit - 1) / kUnit;
+      if constexpr (kWin) {
+        const int tok0 = x.row0 / p.group, tok1 = (x.row0 + x.rows - 1) / p.group;
+        x.win_lo = window_first(p, x.past, tok0);
+        x.win_hi = window_first(p, x.past, tok1);
+        x.few = min(p.sinks, x.key_end);
+        // the units of the first keys, then from the window's first one on (one run where the two touch)
+        const int first = sink_units(p, x.s.kv_len), from = x.win_lo / kUnit;
+        x.lead = from > first ? first : 0;
+        x.skip = from > first ? from - first : 0;
+        last -= x.skip;   // a gap has the window's keys behind it
+      }
+      x.steps = min(nblk, max(0, last - x.blk0));
       x.tile_end = base + (item + 1) * x.s.blocks;
       u += nblk;
       return true;
@@ -198,15 +251,39 @@ struct PieceWalk {
   }
 };
 
+// Which unit of the sequence a tile's unit i is.
+template <bool kWin>
+__device__ __forceinline__ int unit_of(const Piece& x, int i) {
+  return !kWin || i < x.lead ? i : i + x.skip;
+}
+
+// No row of the tile sees the key: it is not read.
+template <bool kWin>
+__device__ __forceinline__ bool key_hidden(const Piece& x, int key) {
+  return key >= x.key_end || (kWin && key < x.win_lo && key >= x.few);
+}
+
+// Some key of the unit that begins with key `first` may be hidden from some row.
+template <bool kWin>
+__device__ __forceinline__ bool unit_cut(const PagedArgs& p, const Piece& x, int first) {
+  return first + kUnit > min(p.tree ? x.past : x.past + 1, x.s.kv_len) ||
+         (kWin && first < x.win_hi && first + kUnit > x.few);
+}
+
 // The first word of a token's tree mask: read when the piece begins, needed at its last keys.
 __device__ __forceinline__ uint64_t tree_word(const PagedArgs& p, const Piece& x, int tok) {
   return p.tree ? (uint64_t)p.tree[(long long)(x.s.q_start + tok) * p.tree_words] : 0ull;
 }
 
+// The lowest n of 64 bits set.
+__device__ __forceinline__ uint64_t low_bits64(int n) { return n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1); }
+
 // Which of the 64 keys [first, first + 64) token `tok` of the piece's sequence sees; word0: its tree_word.
+template <bool kWin>
 __device__ __forceinline__ uint64_t seen_keys(const PagedArgs& p, const Piece& x, int tok, int first, uint64_t word0) {
   const int last = (p.tree ? x.s.kv_len : min(x.past + tok + 1, x.s.kv_len)) - first;   // keys before the end
-  uint64_t m = last >= 64 ? ~0ull : (last <= 0 ? 0ull : (1ull << last) - 1);
+  uint64_t m = low_bits64(last);
+  if constexpr (kWin) m &= ~low_bits64(window_first(p, x.past, tok) - first) | low_bits64(p.sinks - first);
   if (p.tree) {
     const int j0 = first - x.past;   // index of the first key among the new tokens
     if (j0 > -64) {
@@ -250,9 +327,10 @@ __device__ __forceinline__ void note_split(const PagedArgs& p, const Piece& x, c
 __device__ __forceinline__ int part_of_piece(const Piece& x) { return blockIdx.x * 2 + (x.first ? 0 : 1); }
 
 // Element offset of a piece's key or value in its cache: 0 for one that is not read.
+template <bool kWin>
 __device__ __forceinline__ long long cache_offset(const PagedArgs& p, const Piece& x, const int32_t* table, int key,
                                                   bool values) {
-  if (key >= x.key_end) return 0;
+  if (key_hidden<kWin>(x, key)) return 0;
   const int at = key / p.page_size;
   int page = table[at];
   page = page < 0 ? 0 : (page >= p.num_pages ? p.num_pages - 1 : page);

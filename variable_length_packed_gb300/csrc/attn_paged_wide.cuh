@@ -55,7 +55,7 @@ struct WideSmem {
   (__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &p.status[blockIdx.x], THD_STATUS_WAIT_TIMEOUT,      \
                                      p.wait_limit_ns, p.wait_check_mask) ? 1 : 0) != 0)
 
-template <typename DT, int DP>
+template <typename DT, int DP, bool kWin>
 __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const PagedArgs p) {
   using Tr = Pair16<DT>;
   constexpr int kChunks = DP / 8;
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
     tmem_alloc(&sm.tmem_base, kWideTmemCols);
     tmem_relinquish();
   }
-  find_share<kWideThreads>(p, kWideRows, &sm.share);
+  find_share<kWideThreads>(p, [&](int b) { return seq_work<kWin>(p, b, kWideRows).units; }, &sm.share);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -113,13 +113,13 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.full[i % kWideStages]);
     };
-    while (ok && walk.next<kWideRows>(p, x)) {
+    while (ok && walk.next<kWideRows, kWin>(p, x)) {
       const int32_t* table = p.table + (long long)x.seq * p.table_stride;
       for (int i = 0; i < x.steps; ++i, ++n) {
-        const int first = (x.blk0 + i) * kUnit + (warp - 4) * kWarpKeys;
+        const int first = unit_of<kWin>(x, x.blk0 + i) * kUnit + (warp - 4) * kWarpKeys;
         // each lane the place of one key and of its value
-        const long long koff = cache_offset(p, x, table, first + lane, false);
-        const long long voff = cache_offset(p, x, table, first + lane, true);
+        const long long koff = cache_offset<kWin>(p, x, table, first + lane, false);
+        const long long voff = cache_offset<kWin>(p, x, table, first + lane, true);
         const uint32_t st = n % kWideStages;
         if (n >= kWideStages && !WIDE_WAIT(&sm.empty[st], (n / kWideStages - 1) & 1)) {
           ok = false;
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
 #pragma unroll
         for (int c = 0; c < kCopies; ++c) {
           const int key = c * kLaneKeys + copy_key, row = (warp - 4) * kWarpKeys + key;
-          const bool take = copy_in && first + key < x.key_end;
+          const bool take = copy_in && !key_hidden<kWin>(x, first + key);
           const uint32_t at = (copy_chunk >> 3) * kPanelBytes + row * 128 + (((copy_chunk & 7) ^ (row & 7)) << 4);
           const long long ko = __shfl_sync(0xffffffffu, koff, key), vo = __shfl_sync(0xffffffffu, voff, key);
           const int col = take ? copy_chunk * 8 : 0;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
     bool ok = true;
     const uint32_t khi = smem_desc_sw128_hi(1024);
     if (p.inject_wait) ok = WIDE_WAIT(&sm.never, 0);   // test setting: a wait that runs out, loads in flight
-    while (ok && walk.next<kWideRows>(p, x)) {
+    while (ok && walk.next<kWideRows, kWin>(p, x)) {
       if (x.steps == 0) continue;
       if (!WIDE_WAIT(&sm.q_full, pieces & 1)) break;
       ++pieces;
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
     const float sl2 = p.scale_log2;
     uint32_t n = 0;      // units
     bool ok = true;
-    while (ok && walk.next<kWideRows>(p, x)) {
+    while (ok && walk.next<kWideRows, kWin>(p, x)) {
       const int row = x.row0 + r, tok = row / p.group, hq = x.head * p.group + (row - tok * p.group);
       const bool valid = r < x.rows;
       // a warp past the tile's rows only keeps step: what its lanes of tensor memory hold reaches no row
@@ -236,9 +236,9 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
         tmem_ld32(tS + 32, sr + 32);
         tmem_ld_wait_regs32(sr);
         tmem_tie_regs32(sr + 32);
-        const int first = (x.blk0 + i) * kUnit;
-        if (first + kUnit > min(p.tree ? x.past : x.past + 1, x.s.kv_len)) {   // some key may be hidden from some row
-          const uint64_t seen = valid ? seen_keys(p, x, tok, first, word0) : 0ull;
+        const int first = unit_of<kWin>(x, x.blk0 + i) * kUnit;
+        if (unit_cut<kWin>(p, x, first)) {
+          const uint64_t seen = valid ? seen_keys<kWin>(p, x, tok, first, word0) : 0ull;
           const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
 #pragma unroll
           for (int c = 0; c < 32; ++c) {

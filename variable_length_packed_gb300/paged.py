@@ -12,13 +12,14 @@ import math
 
 import torch
 
-from . import THD_BF16, THD_FP16, THD_OK, ThdError, _check_metadata, load_library
+from . import THD_BF16, THD_FP16, THD_OK, ThdError, _check_metadata, _sink_count, _window_args, load_library
 
 # the current stream's handle without the Stream object around it (2 us a call)
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _F32 = torch.float32
 _Places = ctypes.c_int64 * 6
+_WeightPlaces = ctypes.c_int64 * 3
 _COUNT_MAX = 2 ** 31 - 1   # the library's counts are C ints, which ctypes would cut to 32 bits without a word
 _CODES = {torch.bfloat16: THD_BF16, torch.float16: THD_FP16}
 
@@ -330,6 +331,22 @@ def _caches(k_cache, v_cache, device, dtype, page_table, batch_size, writes):
     return shape, _Places(*places), wide, step
 
 
+def _key_weights(t, device, shape):
+    """Strides of the keys' weights (ctypes int64[3]: page, token, head), which are written."""
+    _on(t, "key_weights", device)
+    if t.dtype is not _F32:
+        raise TypeError("key_weights must be float32")
+    if tuple(t.shape) != tuple(shape[:3]):
+        raise ValueError("key_weights must be [pages, page_size, Hkv], as the caches")
+    steps = [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)]
+    need = 1
+    for step, n in sorted((s, n) for s, n in zip(steps, t.shape) if n > 1):
+        if step < need:
+            raise ValueError("key_weights: places overlap")
+        need = step * (n - 1) + need
+    return _WeightPlaces(*steps)
+
+
 def thd_kv_append(k, v, k_cache, v_cache, page_table, cache_lens, cu_seqlens, cu_seqlens_padded=None,
                   batch_size=None, q=None, rope_cos=None, rope_sin=None, positions=None, q_weight=None, k_weight=None,
                   eps=1e-6, interleaved=False, q_out=None):
@@ -384,15 +401,20 @@ def thd_kv_append(k, v, k_cache, v_cache, page_table, cache_lens, cu_seqlens, cu
 
 def thd_attn_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q, cu_seqlens_q_padded=None, batch_size=None,
                    max_seqlen_q=0, tree_mask=None, softmax_scale=None, out=None, lse=None, return_lse=True,
-                   workspace=None):
+                   workspace=None, window=(-1, -1), sink_tokens=0, key_weights=None):
     """Attention of packed new tokens over a paged cache: decoding steps, chunks, drafted trees.
 
     q: [T, Hq, d] (bf16 or fp16, contiguous).  k_cache / v_cache / page_table: as in thd_kv_append,
     the new tokens' own keys already in them.  kv_lens: int32 [B], keys of each sequence with the
     new ones.  New token i of n sees key j iff j <= kv_len - n + i; with tree_mask (int64
     [T, words]) iff j < kv_len - n or bit j - (kv_len - n) of its mask is set.  max_seqlen_q: a
-    hint, the most new tokens of a sequence (0: unknown).  Returns (out [T, Hq, d], lse [Hq, T]
-    float32 or None); rows of no sequence and rows that see no key are 0 with lse -inf.
+    hint, the most new tokens of a sequence (0: unknown).  window: (left, right) as in thd_attn_fwd: a
+    token sees `left` keys before its own (-1: all; the right side ends at its own in any case), and the
+    first sink_tokens of the sequence; not with a tree_mask.  Keys that no token sees are not read.
+    key_weights: float32 [pages, page_size, Hkv] in any order in memory, updated: each cached key's is
+    raised by the attention weights that the new tokens and the heads of its group gave it, each new
+    token's key's is set to them.  Returns (out [T, Hq, d], lse [Hq, T] float32 or None); rows of no
+    sequence and rows that see no key are 0 with lse -inf.
     """
     code = _dtype_code(q, "q")
     dev, dtype = q.device, q.dtype
@@ -418,7 +440,14 @@ def thd_attn_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q, cu_se
         out = torch.empty((T, hq, d), dtype=dtype, device=dev)
     else:
         _whole(out, "out", dev, dtype, q.shape)
-    if lse is None and return_lse:
+    left, sinks = -1, 0
+    if window != (-1, -1):
+        left, sinks = _window_args(window)[0], _sink_count(sink_tokens)
+    elif sink_tokens != 0:
+        _sink_count(sink_tokens)
+    places = None if key_weights is None else _key_weights(key_weights, dev, shape)
+    wanted = return_lse or lse is not None
+    if lse is None and (return_lse or key_weights is not None):
         lse = torch.empty((hq, T), dtype=torch.float32, device=dev)
     else:
         _whole(lse, "lse", dev, torch.float32, (hq, T))
@@ -427,10 +456,67 @@ def thd_attn_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q, cu_se
     else:
         _whole(workspace, "workspace", dev, torch.uint8)
     max_seqlen_q = int(max_seqlen_q)
-    if (T | hq | shape[2] | d | B | shape[0] | shape[1] | wide | words | abs(max_seqlen_q)) > _COUNT_MAX:
+    if (T | hq | shape[2] | d | B | shape[0] | shape[1] | wide | words | abs(max_seqlen_q) | max(left, 0)) > _COUNT_MAX:
         raise _too_large("thd_attn_paged")
-    _call("thd_attn_paged", dev, _addr(q), k_cache.data_ptr(), v_cache.data_ptr(), strides, shape[0], shape[1],
+    _call("thd_attn_paged_window", dev, _addr(q), k_cache.data_ptr(), v_cache.data_ptr(), strides, shape[0], shape[1],
           page_table.data_ptr(), step, wide, kv_lens.data_ptr(), cu_seqlens_q.data_ptr(), _addr(cu_seqlens_q_padded), B,
-          max_seqlen_q, _addr(tree_mask), words, 1.0 / math.sqrt(d) if softmax_scale is None else
-          float(softmax_scale), out.data_ptr(), _addr(lse), T, hq, shape[2], d, code, _addr(workspace), workspace.numel())
-    return out, lse
+          max_seqlen_q, _addr(tree_mask), words, left, sinks, _addr(key_weights), places,
+          1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale), out.data_ptr(), _addr(lse), T, hq, shape[2], d, code, _addr(workspace), workspace.numel())
+    return out, lse if wanted else None
+
+
+def thd_kv_evict(k_cache, v_cache, key_weights, page_table, kv_lens, keep_lens, batch_size=None, new_page_table=None,
+                 sink_tokens=0, recent_tokens=0, new_lens=None, kept=None):
+    """Keys and values of a paged cache dropped by the attention weight they got.  Returns the new lengths.
+
+    k_cache / v_cache / page_table: as in thd_kv_append; key_weights: as in thd_attn_paged.  kv_lens /
+    keep_lens: int32 [B], keys of each sequence, and how many of them stay (all, where that is more).  Each
+    key/value head keeps the first sink_tokens, the last recent_tokens, and of the others those with
+    the most weight, of equal ones the lower slots.  They move, with their weights and in their order, to
+    slots 0.. of the pages that new_page_table names (int32 [B, pages], none of the old ones), or of
+    their own pages without it; the other slots are left as they were.  kept: int32 [B, Hkv, width], filled with
+    the old slots of the kept keys and -1 behind them; no more than width keys stay.
+    new_lens: int32 [B] (not kv_lens nor keep_lens).
+    """
+    code = _dtype_code(k_cache, "k_cache")
+    dev, dtype = k_cache.device, k_cache.dtype
+    _on(k_cache, "k_cache", dev)
+    for name, t in (("kv_lens", kv_lens), ("keep_lens", keep_lens)):
+        if t is None:
+            raise TypeError(f"{name} must be an int32 tensor")
+        _whole(t, name, dev, torch.int32)
+    B = kv_lens.numel() if batch_size is None else int(batch_size)
+    if B < 0:
+        raise ValueError("batch_size must be >= 0")
+    for name, t in (("kv_lens", kv_lens), ("keep_lens", keep_lens)):
+        if t.numel() < B:
+            raise ValueError(f"{name} holds {t.numel()} entries, batch_size {B} needs as many")
+    shape, strides, wide, step = _caches(k_cache, v_cache, dev, dtype, page_table, B, True)
+    if shape[1] < 1:
+        raise ValueError("a page must hold a token")
+    new_wide, new_step = wide, step
+    if new_page_table is not None:
+        _, _, new_wide, new_step = _caches(k_cache, v_cache, dev, dtype, new_page_table, B, True)
+    places = _key_weights(key_weights, dev, shape)
+    if kept is None:
+        kept = torch.empty((B, shape[2], min(wide, new_wide) * shape[1]), dtype=torch.int32, device=dev)
+    else:
+        _whole(kept, "kept", dev, torch.int32)
+        if kept.dim() != 3 or kept.shape[0] < B or kept.shape[1] != shape[2]:
+            raise ValueError("kept must be [>= batch_size, Hkv, width]")
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+    else:
+        _whole(new_lens, "new_lens", dev, torch.int32)
+        if new_lens.numel() < B:
+            raise ValueError(f"new_lens holds {new_lens.numel()} entries, batch_size {B} needs as many")
+    sinks, recent = int(sink_tokens), int(recent_tokens)
+    if sinks < 0 or recent < 0:
+        raise ValueError("sink_tokens and recent_tokens must be >= 0")
+    if (B | shape[0] | shape[1] | shape[2] | shape[3] | wide | new_wide | kept.shape[2] | sinks | recent) > _COUNT_MAX:
+        raise _too_large("thd_kv_evict")
+    _call("thd_kv_evict", dev, k_cache.data_ptr(), v_cache.data_ptr(), strides, key_weights.data_ptr(), places, shape[0],
+          shape[1], page_table.data_ptr(), step, wide, _addr(new_page_table), new_step, new_wide, kv_lens.data_ptr(),
+          keep_lens.data_ptr(), B, sinks, recent, kept.data_ptr(), kept.shape[2], new_lens.data_ptr(), shape[2],
+          shape[3], code)
+    return new_lens
