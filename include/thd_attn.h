@@ -230,10 +230,21 @@ int thd_attn_bwd_window(const void* q, const void* k, const void* v, const void*
                         void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * thd_attn_bwd_sinks_workspace_size — bytes of device workspace thd_attn_bwd_sinks needs:
+ * thd_attn_bwd_workspace_size's, and, with window_left >= 0 and 1 <= sink_tokens <= 512, sums of
+ * 8 * head_dim bytes for each such key and head of every sequence and of every 2048 rows.  0 for
+ * invalid sizes.
+ */
+size_t thd_attn_bwd_sinks_workspace_size(int total_tokens, int num_heads_q, int num_heads_kv, int head_dim,
+                                         int batch_size, int window_left, int sink_tokens);
+
+/*
  * thd_attn_bwd_sinks — thd_attn_bwd_window for a forward computed with
  * thd_attn_fwd_sinks: the same window and sink_tokens (0 is exactly
- * thd_attn_bwd_window).  Other arguments and errors as there, and THD_ERR_ARG
- * for sink_tokens < 0.
+ * thd_attn_bwd_window).  dK and dV are summed in a fixed order, so the same call
+ * gives the same bits of them.  Other arguments and errors as there, THD_ERR_ARG
+ * for sink_tokens < 0, and workspace of at least
+ * thd_attn_bwd_sinks_workspace_size's bytes.
  */
 int thd_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* out, const float* lse,
                        const void* dout,

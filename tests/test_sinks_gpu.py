@@ -148,3 +148,43 @@ def test_backward_matches_oracle(d, dtype, hq, hkv):
                                     w.cu_seqlens_padded, w.cu_seqlens_padded, CODES, w.batch_size, w.softmax_scale,
                                     window, sinks)
         check_bwd(grads, ref, (w.q, w.k, w.v), dout, w.softmax_scale, dtype, f"d {d} window {window} sinks {sinks}")
+
+
+@pytest.mark.parametrize("d,dtype,hq,hkv,window,sinks", [(64, BF16, 2, 1, (100, 0), 4), (128, FP16, 3, 3, (500, 0), 130),
+                                                       (128, BF16, 2, 2, (0, 0), 1), (64, FP16, 4, 1, (1023, 0), 16),
+                                                       (64, BF16, 1, 1, (10, 10), 600)])
+def test_keys_seen_by_the_queries_of_several_chunks(d, dtype, hq, hkv, window, sinks):
+    """Sequences of several times 2048 rows: the sums of their first keys come from several items."""
+    lens = [5000, 60, 2300, 4096]
+    codes = np.array([1, 1, 2, 0], np.uint8)
+    w = workloads.from_lengths("far", lens, codes != 0, gaps_before=[3, 1, 900, 0], trailing=5, heads_q=hq, heads_kv=hkv,
+                               head_dim=d, dtype=dtype, seed=1, with_padded=True)
+    dev = to_device(w)
+    c = torch.from_numpy(codes).cuda()
+    args = (dev["cu"], dev["cu"], dev["padded"], dev["padded"], c, w.batch_size, w.max_seqlen, w.softmax_scale)
+    out, lse = vlp.thd_attn_fwd(dev["q"], dev["k"], dev["v"], *args, window=window, sink_tokens=sinks)
+    dout = workloads.grad_output(w, 7)
+    grads = [vlp.thd_attn_bwd(dev["q"], dev["k"], dev["v"], out, lse, dout.cuda(), *args, window=window, sink_tokens=sinks)
+             for _ in range(2)]
+    torch.cuda.synchronize()
+    ref = bounded.attention_bwd(w.q, w.k, w.v, f64(out), f64(lse), dout, w.cu_seqlens, w.cu_seqlens, w.cu_seqlens_padded,
+                                w.cu_seqlens_padded, codes, w.batch_size, w.softmax_scale, window, sinks)
+    check_bwd(grads[0], ref, (w.q, w.k, w.v), dout, w.softmax_scale, dtype, f"d {d} window {window} sinks {sinks}")
+    assert torch.equal(grads[0][1], grads[1][1]) and torch.equal(grads[0][2], grads[1][2])   # one order of the sums
+
+
+def test_workspace_sizes():
+    plain = vlp.load_library().thd_attn_bwd_workspace_size(5000, 4, 64)
+    size = lambda *a: vlp.load_library().thd_attn_bwd_sinks_workspace_size(*a)  # noqa: E731
+    assert size(5000, 4, 2, 64, 3, 100, 0) == plain == size(5000, 4, 2, 64, 3, -1, 4) == size(5000, 4, 2, 64, 3, 100, 513)
+    assert size(5000, 4, 2, 64, 3, 100, 4) == plain + 3 * 2 * 2 * 4 * 64 * 4 + (3 + 2 + 1) * 2 * 2 * 4 * 64 * 4
+    assert size(-1, 4, 2, 64, 3, 100, 4) == 0
+    w = batch(64, BF16, 1)
+    dev = to_device(w)
+    out, lse = forward(w, dev, (64, 0), 4)
+    short = vlp.load_library().thd_attn_bwd_workspace_size(w.total_tokens, 4, 64)
+    with pytest.raises(vlp.ThdError) as err:
+        vlp.thd_attn_bwd(dev["q"], dev["k"], dev["v"], out, lse, out, dev["cu"], dev["cu"], dev["padded"], dev["padded"],
+                         torch.from_numpy(CODES).cuda(), w.batch_size, w.max_seqlen, w.softmax_scale, window=(64, 0),
+                         sink_tokens=4, workspace=torch.empty(short, dtype=torch.uint8, device="cuda"))
+    assert err.value.status == vlp.THD_ERR_WORKSPACE

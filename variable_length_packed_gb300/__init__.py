@@ -67,6 +67,8 @@ def load_library():
     lib.thd_attn_bwd_sinks.restype = I
     lib.thd_attn_bwd_sinks.argtypes = [P, P, P, P, P, P, P, P, P, P, P, I, I, F, P, P, P, I, I, I, I, I, I, I, I, P, SZ,
                                        P]
+    lib.thd_attn_bwd_sinks_workspace_size.restype = SZ
+    lib.thd_attn_bwd_sinks_workspace_size.argtypes = [I, I, I, I, I, I, I]
     lib.thd_attn_bwd_workspace_size.restype = SZ
     lib.thd_attn_bwd_workspace_size.argtypes = [I, I, I]
     lib.thd_attn_merge.restype = I
@@ -412,11 +414,11 @@ def thd_attn_bwd(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlen
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
-    need = int(_lib().thd_attn_bwd_workspace_size(int(T), int(Hq), int(d)))
-    if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     left, right = _window_args(window)
     sinks = _sink_count(sink_tokens)
+    need = int(_lib().thd_attn_bwd_sinks_workspace_size(int(T), int(Hq), int(Hkv), int(d), int(batch_size), left, sinks))
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     with torch.cuda.device(q.device):
         st = _lib().thd_attn_bwd_sinks(
             _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(cu_seqlens_q), _ptr(cu_seqlens_kv),

@@ -46,6 +46,7 @@ struct AttnParams {
   int claim;               // work items taken per atomic on the counter (>= 1)
   int win_left, win_right; // sliding window (keys before / after the diagonal), -1 = unbounded
   int sinks;               // first keys of a sequence that the window does not hide (0 without a window)
+  int far_tiles;           // backward: query tiles of a far item (far_chunks), 0: there are none
   int B, T, Hq, Hkv, d, group;
   float scale;             // softmax scale
   float scale_log2;        // softmax scale * log2(e)
@@ -259,14 +260,36 @@ __device__ __forceinline__ uint32_t seq_sort_key(const SeqInfo& s, int sinks) {
   return (uint32_t)(3 + nkv * 2 + (s.causal ? 0 : 1));
 }
 
+// Backward under a window with first keys that stay visible: a tile of such keys is seen by every query behind
+// it, where other tiles are seen by a window's queries.  Its item takes the query tiles of its
+// window (near_query_tiles of them from the first on), and the ones after them are items of their own, far_tiles
+// query tiles each, cut at multiples of far_tiles: the chunks far_first .. far_first + far_chunks - 1 of
+// the sequence, for each of its sink_tiles (the chunks of later tiles may be empty).
+__device__ __forceinline__ int near_query_tiles(const SeqInfo& s, int kv0) {
+  const int all = (s.q_len + kTileM - 1) / kTileM;
+  const long long last = (long long)kv0 + kTileM - 1 - s.shift + s.lo_off;
+  return last < 0 ? 0 : (int)min((long long)all, last / kTileM + 1);
+}
+__device__ __forceinline__ int sink_tiles(const SeqInfo& s, int sinks) { return (min(sinks, s.kv_len) + kTileM - 1) / kTileM; }
+__device__ __forceinline__ int far_first(const SeqInfo& s, const AttnParams& p) {
+  return near_query_tiles(s, 0) / p.far_tiles;
+}
+__device__ __forceinline__ int far_chunks(const SeqInfo& s, const AttnParams& p) {
+  if (p.far_tiles == 0 || s.kv_len <= 0 || s.q_len <= 0) return 0;
+  const int all = (s.q_len + kTileM - 1) / kTileM;
+  return near_query_tiles(s, 0) < all ? (all + p.far_tiles - 1) / p.far_tiles - far_first(s, p) : 0;
+}
+
 // Items of one sequence: blocks of BLOCK rows of the query sequence times the
-// query heads (forward), or of the key/value sequence times the key/value heads
-// (backward, kKvSide).
+// query heads (forward), or of the key/value sequence times the key/value heads,
+// and its far items (backward, kKvSide).
 template <int BLOCK, bool kKvSide>
 __device__ __forceinline__ uint32_t seq_items(const SeqInfo& s, const AttnParams& p) {
   const int len = kKvSide ? s.kv_len : s.q_len;
   const int heads = kKvSide ? p.Hkv : p.Hq;
-  return len > 0 ? (uint32_t)((len + BLOCK - 1) / BLOCK) * (uint32_t)heads : 0u;
+  uint32_t n = len > 0 ? (uint32_t)((len + BLOCK - 1) / BLOCK) : 0u;
+  if (kKvSide) n += (uint32_t)(far_chunks(s, p) * sink_tiles(s, p.sinks));
+  return n * (uint32_t)heads;
 }
 
 __device__ __forceinline__ uint32_t warp_incl_scan(uint32_t x) {
@@ -500,6 +523,7 @@ __device__ void sched_load_chunk(SchedSmem& s, const AttnParams& p, int base) {
 struct WorkItem {
   int valid;
   int b, h, qblock;
+  int far;   // backward: the chunk of a far item (of the key/value block qblock), else -1
   SeqInfo seq;
 };
 
@@ -609,9 +633,21 @@ __device__ WorkItem sched_decode(SchedSmem& s, const AttnParams& p, unsigned lon
   it.seq = cached_seq(s, s.order[lo], p);
   const uint32_t r = local - s.cum[lo];
   const int len = kKvSide ? it.seq.kv_len : it.seq.q_len;
-  const uint32_t nblk = (uint32_t)((len + BLOCK_M - 1) / BLOCK_M);
+  uint32_t nblk = (uint32_t)((len + BLOCK_M - 1) / BLOCK_M);
+  it.far = -1;
+  if (kKvSide) {   // a head's far items, then its blocks
+    const uint32_t chunks = (uint32_t)far_chunks(it.seq, p), nfar = chunks * (uint32_t)sink_tiles(it.seq, p.sinks);
+    nblk += nfar;
+    const uint32_t in = r % nblk;
+    it.qblock = (int)(in - nfar);
+    if (in < nfar) {
+      it.qblock = (int)(in / chunks);
+      it.far = far_first(it.seq, p) + (int)(in % chunks);
+    }
+  } else {
+    it.qblock = (int)(nblk - 1u - (r % nblk));
+  }
   it.h = (int)(r / nblk);
-  it.qblock = kKvSide ? (int)(r % nblk) : (int)(nblk - 1u - (r % nblk));
   it.valid = 1;
   return it;
 }

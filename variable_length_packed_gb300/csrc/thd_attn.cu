@@ -132,6 +132,28 @@ bool encode_f32_map(CUtensorMap* map, const void* base, int rows, long long cols
   return r == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+namespace thd {
+// 3-D view [T, heads, d], box = 64 columns of `heads_box` heads of `tokens_box` tokens, 128-byte swizzle: the rows of
+// one group of query heads, token by token, for the kernels of other translation units.
+bool encode_group_map(CUtensorMap* map, const void* base, int T, int heads, int d, int heads_box, int tokens_box,
+                      bool bf16) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2ull, (cuuint64_t)heads * (cuuint64_t)d * 2ull};
+  cuuint32_t box[3] = {64u, (cuuint32_t)heads_box, (cuuint32_t)tokens_box};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace thd
+
+namespace {
+
 template <typename DT, int DP, bool kTMA>
 int launch_serial(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const thd::AttnParams& p,
                   int grid, cudaStream_t stream) {
@@ -178,13 +200,30 @@ size_t bwd_workspace_bytes(int T, int Hq, int d) {
   return kWorkspaceBytes + align256((size_t)Hq * T * 4) + align256((size_t)T * Hq * d * 4);
 }
 
+// The shared sums of the backward pass under a window with first keys that stay visible: their sizes, and
+// how many bytes they take behind the workspace of the pass without.
+struct FarSums {
+  int rows = 0, key_tiles = 0;
+  size_t near_bytes = 0, far_bytes = 0;
+};
+FarSums far_sums_of(int T, int Hkv, int B, int d, int window_left, int sinks) {
+  FarSums f;
+  if (window_left < 0 || sinks <= 0 || sinks > thd::kFarMaxSinks || B <= 0 || T <= 0) return f;
+  f.rows = sinks < thd::kTileM ? sinks : thd::kTileM;
+  f.key_tiles = (sinks + thd::kTileM - 1) / thd::kTileM;
+  const size_t part = (size_t)Hkv * f.key_tiles * 2 * f.rows * d * 4;
+  f.near_bytes = align256((size_t)B * part);
+  f.far_bytes = align256(((size_t)B + (size_t)T / (thd::kFarTiles * thd::kTileM) + 1) * part);
+  return f;
+}
+
 template <typename DT, int DP>
 int launch_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
                const CUtensorMap& mdq, const thd::BwdParams& bp, int sms, cudaStream_t stream) {
   const int small_grid = sms * 8;
   thd::attn_bwd_pre_kernel<DT><<<small_grid, 256, 0, stream>>>(bp);
   if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;
-  auto kern = thd::attn_bwd_kernel<DT, DP>;
+  auto kern = bp.a.sinks > 0 ? thd::attn_bwd_kernel<DT, DP, true> : thd::attn_bwd_kernel<DT, DP, false>;
   const size_t smem = one_cta_per_sm(sizeof(thd::BwdSmem<DP>) + 1024);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return THD_ERR_CUDA;
@@ -203,6 +242,14 @@ size_t thd_attn_bwd_workspace_size(int total_tokens, int num_heads_q, int head_d
   return bwd_workspace_bytes(total_tokens, num_heads_q, head_dim);
 }
 
+size_t thd_attn_bwd_sinks_workspace_size(int total_tokens, int num_heads_q, int num_heads_kv, int head_dim,
+                                         int batch_size, int window_left, int sink_tokens) {
+  if (total_tokens < 0 || num_heads_q < 1 || num_heads_kv < 1 || head_dim < 1 || batch_size < 0 || sink_tokens < 0)
+    return 0;
+  const FarSums f = far_sums_of(total_tokens, num_heads_kv, batch_size, head_dim, window_left, sink_tokens);
+  return bwd_workspace_bytes(total_tokens, num_heads_q, head_dim) + f.near_bytes + f.far_bytes;
+}
+
 int thd_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* out, const float* lse,
                         const void* dout, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
                         const int32_t* cu_seqlens_q_padded, const int32_t* cu_seqlens_kv_padded,
@@ -218,7 +265,7 @@ int thd_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* 
   if (head_dim != 64 && head_dim != 128) return THD_ERR_UNSUPPORTED;
   if (num_heads_q % num_heads_kv != 0) return THD_ERR_UNSUPPORTED;
   const long long max_items = ((long long)total_tokens / 128 + (long long)batch_size + 1) * num_heads_kv;
-  if (max_items >= (1ll << 31)) return THD_ERR_UNSUPPORTED;
+  if (max_items * (sink_tokens > 0 ? 6 : 1) >= (1ll << 31)) return THD_ERR_UNSUPPORTED;
   if ((long long)num_heads_q * head_dim * 2 >= (1ll << 31)) return THD_ERR_UNSUPPORTED;
   if (total_tokens == 0) return THD_OK;
   if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv) return THD_ERR_ARG;
@@ -232,7 +279,8 @@ int thd_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* 
       (cu_seqlens_kv_padded && !aligned(cu_seqlens_kv_padded, 4)))
     return THD_ERR_ARG;
   if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < bwd_workspace_bytes(total_tokens, num_heads_q, head_dim))
+      workspace_bytes < thd_attn_bwd_sinks_workspace_size(total_tokens, num_heads_q, num_heads_kv, head_dim, batch_size,
+                                                          window_left, sink_tokens))
     return THD_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int sms = num_sms_of_current_device();
@@ -273,6 +321,12 @@ int thd_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* 
   char* wsb = static_cast<char*>(workspace);
   bp.D = reinterpret_cast<float*>(wsb + kWorkspaceBytes);
   bp.dacc = reinterpret_cast<float*>(wsb + kWorkspaceBytes + align256((size_t)num_heads_q * total_tokens * 4));
+  const FarSums far = far_sums_of(total_tokens, num_heads_kv, batch_size, head_dim, window_left, sink_tokens);
+  p.far_tiles = far.rows > 0 ? thd::kFarTiles : 0;
+  bp.far_rows = far.rows;
+  bp.far_key_tiles = far.key_tiles;
+  bp.near_sums = reinterpret_cast<float*>(wsb + bwd_workspace_bytes(total_tokens, num_heads_q, head_dim));
+  bp.far_sums = reinterpret_cast<float*>(wsb + bwd_workspace_bytes(total_tokens, num_heads_q, head_dim) + far.near_bytes);
 
   if (cudaMemsetAsync(workspace, 0, 16, st) != cudaSuccess) return THD_ERR_CUDA;
   const bool bf16 = dtype == THD_BF16;
