@@ -158,6 +158,25 @@ def test_weights_match_oracle(keys, new, page, hq, hkv, d, dtype, gap, words, fi
         assert torch.equal(again, w)
 
 
+@pytest.mark.parametrize("keys,new,page,hq,hkv,d,dtype,words,left,sinks", [
+    ([2000, 300], [40, 90], 16, 10, 2, 128, BF16, 0, -1, 0),             # tiles of 125 rows
+    ([700, 1300], [200, 1], 16, 48, 3, 64, FP16, 0, -1, 0),              # of 8 tokens
+    ([500], [30], 16, 100, 1, 40, BF16, 0, -1, 0),                       # of one token
+    ([400], [3], 16, 200, 1, 32, BF16, 0, -1, 0),                        # more heads in a group than rows in a tile
+    ([900, 257, 256], [60, 60, 256], 8, 4, 2, 8, BF16, 0, -1, 0),        # the narrowest heads
+    ([900, 129, 128], [60, 60, 128], 8, 4, 2, 16, FP16, 0, 77, 3),
+    ([3000, 1] * 40, [33, 1] * 40, 16, 8, 4, 128, BF16, 0, -1, 0),       # several items for each CTA
+    ([5000] * 6, [300] * 6, 16, 8, 2, 64, BF16, 0, 1000, 300),
+    ([400, 900], [100, 130], 16, 8, 2, 96, FP16, 3, -1, 0),              # trees over several words and tiles
+])
+def test_weights_from_many_rows(keys, new, page, hq, hkv, d, dtype, words, left, sinks):
+    x = make(keys, new, page, hq, hkv, d, dtype, words=words, seed=3, gap=2)
+    table = hide(x, left, sinks) if left >= 0 else x["table"]
+    w = weights_of(x)
+    had = w.clone()
+    check(x, run(x, table, left, sinks, w), left, sinks, had, w)
+
+
 def test_sinks_without_a_window_and_weights_without_the_lse():
     x = make([300, 40], [2, 5], 16, 8, 2, 64, BF16)
     a, b = run(x, x["table"], -1, 0), run(x, x["table"], -1, 9)

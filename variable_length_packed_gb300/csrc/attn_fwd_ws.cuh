@@ -750,9 +750,6 @@ __device__ __forceinline__ void ws_exp_chunk(const uint32_t* sr, uint32_t* pk, f
   }
 }
 
-// The lowest n bits set (none for n <= 0, all from n = 32 on).
-__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u); }
-
 // Softmax of one KV tile for one row (the calling thread's TMEM lane): S from
 // TMEM, online max / sums, P (rounded to the input type) back over S in two
 // halves of 64 keys, lazy O rescale.  `partial` (warp-uniform): some row of

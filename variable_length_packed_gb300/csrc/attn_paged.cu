@@ -37,6 +37,7 @@
 #include "../../include/thd_attn.h"
 #include "attn_paged_common.cuh"
 #include "attn_paged_weights.cuh"
+#include "attn_paged_weights_wide.cuh"
 #include "attn_paged_wide.cuh"
 
 namespace thd {
@@ -465,6 +466,27 @@ constexpr size_t kStatusAt = 256, kSplitAt = kStatusAt + kMaxCtas * sizeof(uint3
 constexpr size_t kPartAt = kSplitAt + kMaxCtas * sizeof(Split);
 constexpr size_t part_bytes(int dp) { return (size_t)kMaxCtas * 2 * kMaxRows * (dp + 3) * 4; }
 
+// The keys' weights: tiles of 128 rows on the tensor cores where the attention took them, unless a group has more
+// heads than such a tile rows.
+template <typename DT, int DP, bool kWide, bool kWin>
+int launch_key_weights(const PagedArgs& p, int sms, cudaStream_t st) {
+  if constexpr (kWide) {
+    if (p.group <= kWwRows) {
+      const int tokens = kWwRows / p.group;
+      CUtensorMap map;
+      if (!encode_group_map(&map, p.q, p.T, p.Hq, p.d, p.group, tokens, Pair16<DT>::kBF16)) return THD_ERR_CUDA;
+      auto kern = attn_key_weights_wide_kernel<DT, DP, kWin>;
+      constexpr int smem = (int)sizeof(WwSmem<DP>) + 1024;
+      static SmemGrant grant;
+      if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
+      kern<<<sms, kWwThreads, smem, st>>>(map, p, tokens);
+      return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
+    }
+  }
+  attn_key_weights_kernel<DT, DP, kWin><<<4 * sms, kWeightWarps * 32, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
+}
+
 template <typename DT, int DP, int MT, bool kWin>
 int launch_paged(PagedArgs& p, char* ws, int sms, cudaStream_t st) {
   p.call_status = reinterpret_cast<uint32_t*>(ws + 8);
@@ -497,11 +519,7 @@ int launch_paged(PagedArgs& p, char* ws, int sms, cudaStream_t st) {
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<DT, DP, MT>, static_cast<const PagedArgs>(p)) != cudaSuccess)
     return THD_ERR_CUDA;
-  if (p.key_weights) {
-    attn_key_weights_kernel<DT, DP, kWin><<<4 * sms, kWeightWarps * 32, 0, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;
-  }
-  return THD_OK;
+  return p.key_weights ? launch_key_weights<DT, DP, MT == kWideRows, kWin>(p, sms, st) : THD_OK;
 }
 
 // Tiles of 16 rows where no sequence has more, else of 128.  120000 keys of 16 sequences, 32 + 8 heads of 128,

@@ -114,7 +114,14 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
       : "memory");
 }
-// The same copy issued by the lanes whose `issue` is set (one lane of a converged
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+// The same 2-D copy issued by the lanes whose `issue` is set (one lane of a converged
 // warp; every lane evaluates the operands).
 __device__ __forceinline__ void tma_load_2d_if(bool issue, void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
                                                int c1) {
@@ -396,6 +403,9 @@ __device__ __forceinline__ float fmax3f(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+
+// The lowest n bits set (none for n <= 0, all from n = 32 on).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u); }
 
 // 2^x with the hardware approximation (PTX ex2.approx, the MUFU unit);
 // returns 0 for x == -inf.
