@@ -516,6 +516,18 @@ int thd_attn_paged(const void* q, const void* k_cache, const void* v_cache, cons
                    void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * thd_attn_paged_weights_workspace_size — bytes of workspace with which thd_attn_paged_window
+ * reads the keys once although it adds up their weights: thd_attn_paged_workspace_size's and
+ * 4 bytes for each query head, new token and cached key of its sequence.  It serves batches whose sequences
+ * have at most 16 rows (new tokens times the query heads of a key/value head) each and
+ * share no pages; others, and calls with less workspace, take the products with the
+ * keys twice.  0 for invalid sizes.
+ */
+size_t thd_attn_paged_weights_workspace_size(int head_dim, int num_heads_q, int batch_size, int max_seqlen_q,
+                                             int num_pages, int page_size, int max_pages, int window_left,
+                                             int sink_tokens);
+
+/*
  * thd_attn_paged_window — thd_attn_paged with a window, with first tokens that stay
  * visible, and with the weights that cached keys got.
  *
@@ -536,6 +548,8 @@ int thd_attn_paged(const void* q, const void* k_cache, const void* v_cache, cons
  *              share a place (a page that several sequences of the batch name gets
  *              unspecified weights).  Needs lse.
  * weight_strides  host int64 [3], >= 0; not read when key_weights is NULL.
+ * workspace    as thd_attn_paged; with key_weights more of it saves reading the keys
+ *              twice (thd_attn_paged_weights_workspace_size).
  * Other arguments and errors as thd_attn_paged, and THD_ERR_ARG for those above.
  */
 int thd_attn_paged_window(const void* q, const void* k_cache, const void* v_cache, const int64_t* cache_strides,

@@ -41,14 +41,14 @@ def hide(x, left, sinks):
 
 
 def run(x, table, left, sinks, weights=None, **over):
-    work = torch.zeros(vlp.thd_attn_paged_workspace_size(x["q"].shape[2]), dtype=torch.uint8, device="cuda")
+    work = torch.zeros(vlp.thd_attn_paged_workspace_size(x["q"].shape[2]) + (1 << 22), dtype=torch.uint8, device="cuda")
     kw = dict(cu_seqlens_q_padded=None if x["padded"] is None else ints(x["padded"]), batch_size=x["B"], workspace=work,
               tree_mask=None if x["tree"] is None else torch.tensor(x["tree"]).cuda(), window=(left, -1),
               sink_tokens=sinks, key_weights=weights)
     kw.update(over)
     got = vlp.thd_attn_paged(x["q"], x["kc"], x["vc"], ints(table), ints(x["keys"]), ints(x["cu"]), **kw)
     torch.cuda.synchronize()
-    assert int(work[8:12].view(torch.int32).item()) == 0
+    assert int(work[8:12].view(torch.int32).item()) == 0   # of a workspace that the call was given
     return got
 
 
@@ -175,6 +175,26 @@ def test_weights_from_many_rows(keys, new, page, hq, hkv, d, dtype, words, left,
     w = weights_of(x)
     had = w.clone()
     check(x, run(x, table, left, sinks, w), left, sinks, had, w)
+
+
+def test_weights_with_and_without_room_for_the_scores():
+    for left, sinks in ((-1, 0), (100, 5)):
+        x = make([777, 64, 65, 3, 0, 1000], [1, 2, 1, 3, 1, 4], 16, 16, 4, 128, BF16, gap=3)
+        sizes = (128, 16, 6, 4, len(x["kc"]), 16, x["table"].shape[1], (left, -1), sinks)
+        base, full = vlp.thd_attn_paged_workspace_size(128), vlp.thd_attn_paged_weights_workspace_size(*sizes)
+        assert full > base and vlp.thd_attn_paged_weights_workspace_size(129, *sizes[1:]) == 0
+        for size in (base, base + 4096, full):
+            w = weights_of(x)
+            had = w.clone()
+            work = torch.empty(size, dtype=torch.uint8, device="cuda")
+            check(x, vlp.thd_attn_paged(x["q"], x["kc"], x["vc"], ints(x["table"]), ints(x["keys"]), ints(x["cu"]),
+                                        ints(x["padded"]), max_seqlen_q=4, workspace=work, window=(left, -1),
+                                        sink_tokens=sinks, key_weights=w), left, sinks, had, w)
+        # a hint that is too small: a sequence of several narrow tiles
+        y = make([300, 500], [9, 2], 16, 16, 4, 128, BF16)
+        w = weights_of(y)
+        had = w.clone()
+        check(y, run(y, y["table"], left, sinks, w, max_seqlen_q=2, workspace=None), left, sinks, had, w)
 
 
 def test_sinks_without_a_window_and_weights_without_the_lse():

@@ -17,7 +17,8 @@ import torch
 __all__ = ["thd_attn_fwd", "thd_attn_bwd", "thd_attn_fwd_noalloc", "thd_attn_noalloc_status", "thd_attn_merge", "thd_padding_mask",
            "thd_padding_mask_cross", "MASK_PADDING", "MASK_PADDING_CAUSAL", "MASK_PADDING_CAUSAL_BOTTOM_RIGHT", "thd_attn_workspace_size", "thd_set_wait_limit_ns", "thd_set_wait_injection", "thd_status_string",
            "ThdError", "library_path", "load_library", "STATUS_WAIT_TIMEOUT", "thd_qk_norm_rope", "thd_qk_norm_rope_bwd",
-           "thd_qk_norm_rope_bwd_workspace_size", "thd_kv_append", "thd_attn_paged", "thd_attn_paged_workspace_size", "thd_kv_evict"]
+           "thd_qk_norm_rope_bwd_workspace_size", "thd_kv_append", "thd_attn_paged", "thd_attn_paged_workspace_size",
+           "thd_attn_paged_weights_workspace_size", "thd_kv_evict"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -99,6 +100,8 @@ def load_library():
     lib.thd_attn_paged_window.restype = I
     lib.thd_attn_paged_window.argtypes = [P, P, P, P, I, I, P, L, I, P, P, P, I, I, P, I, I, I, P, P, F, P, P, I, I, I, I,
                                           I, P, SZ, P]
+    lib.thd_attn_paged_weights_workspace_size.restype = SZ
+    lib.thd_attn_paged_weights_workspace_size.argtypes = [I, I, I, I, I, I, I, I, I]
     lib.thd_kv_evict.restype = I
     lib.thd_kv_evict.argtypes = [P, P, P, P, P, I, I, P, L, I, P, L, I, P, P, I, I, I, P, I, P, I, I, I, P]
     lib.thd_attn_paged_workspace_size.restype = SZ
@@ -431,5 +434,6 @@ def thd_attn_bwd(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlen
     return dq, dk, dv
 
 
-from .paged import (thd_attn_paged, thd_attn_paged_workspace_size, thd_kv_append, thd_kv_evict,  # noqa: E402
-                    thd_qk_norm_rope, thd_qk_norm_rope_bwd, thd_qk_norm_rope_bwd_workspace_size)
+from .paged import (thd_attn_paged, thd_attn_paged_weights_workspace_size,  # noqa: E402
+                    thd_attn_paged_workspace_size, thd_kv_append, thd_kv_evict, thd_qk_norm_rope, thd_qk_norm_rope_bwd,
+                    thd_qk_norm_rope_bwd_workspace_size)

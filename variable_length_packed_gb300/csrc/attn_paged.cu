@@ -79,7 +79,8 @@ struct PagedSmem {
   static constexpr int kBytes = kRing > kJoin ? kRing : kJoin;
 };
 
-template <typename DT, int DP, bool kWin>
+// kScores: the scores are kept for the keys' weights, in place of reading the keys once more.
+template <typename DT, int DP, bool kWin, bool kScores>
 __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedArgs p) {
   constexpr int MT = kNarrowRows;
   constexpr int kKSteps = DP / 16;      // of the score product
@@ -107,7 +108,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
 
   PieceWalk walk(share);
   Piece x;
-  while (walk.next<MT, kWin>(p, x)) {
+  bool keep_scores = false;
+  if constexpr (kScores) {
+    const ScorePlaces at = score_places<kWarps * 32, kWin>(p, share.seq);
+    keep_scores = at.fit;
+    walk.scores = at.base;
+  }
+  while (walk.next<MT, kWin, kScores>(p, x)) {
     // ---- keys and values: this warp's 16 keys of unit blk0 + i ----
     const int32_t* table = p.table + (long long)x.seq * p.table_stride;
     // lane l < 16 holds the offset of key l, lane 16 + l that of value l
@@ -212,6 +219,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
           if (!(seen & 2)) c[0][2 * hh + 1] = -INFINITY;
           if (!(seen & 256)) c[1][2 * hh] = -INFINITY;
           if (!(seen & 512)) c[1][2 * hh + 1] = -INFINITY;
+        }
+      }
+      if constexpr (kScores) {
+        if (keep_scores) {
+          float* dst = p.scores + walk.scores +
+                       (((long long)x.head * x.s.blocks + x.blk0 + i) * x.rows + qr) * kUnit + warp * kWarpKeys + qc;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh)
+            if (token[hh] >= 0) {
+              float2* to = reinterpret_cast<float2*>(dst + hh * 8 * kUnit);
+              to[0] = make_float2(c[0][2 * hh], c[0][2 * hh + 1]);
+              to[4] = make_float2(c[1][2 * hh], c[1][2 * hh + 1]);
+            }
         }
       }
       // ---- running maximum and sums, weights ----
@@ -483,8 +503,16 @@ int launch_key_weights(const PagedArgs& p, int sms, cudaStream_t st) {
       return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
     }
   }
-  attn_key_weights_kernel<DT, DP, kWin><<<4 * sms, kWeightWarps * 32, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(4 * sms);
+  cfg.blockDim = dim3(kWeightWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_key_weights_kernel<DT, DP, kWin>, p) == cudaSuccess ? THD_OK : THD_ERR_CUDA;
 }
 
 template <typename DT, int DP, int MT, bool kWin>
@@ -494,6 +522,7 @@ int launch_paged(PagedArgs& p, char* ws, int sms, cudaStream_t st) {
   p.splits = reinterpret_cast<Split*>(ws + kSplitAt);
   p.part_o = reinterpret_cast<float*>(ws + kPartAt);
   p.part_m = p.part_o + (size_t)kMaxCtas * 2 * MT * DP;
+  if (MT != kNarrowRows || !p.key_weights || p.score_room <= 0) p.scores = nullptr;
   const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
   static SmemGrant grant;
   if constexpr (MT == kWideRows) {
@@ -502,9 +531,10 @@ int launch_paged(PagedArgs& p, char* ws, int sms, cudaStream_t st) {
     if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
     kern<<<grid, kWideThreads, smem, st>>>(p);
   } else {
-    auto kern = attn_paged_kernel<DT, DP, kWin>;
+    auto kern = p.scores ? attn_paged_kernel<DT, DP, kWin, true> : attn_paged_kernel<DT, DP, kWin, false>;
     constexpr int smem = PagedSmem<DP>::kBytes;
-    if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
+    static SmemGrant grant_scores;
+    if (!(p.scores ? grant_scores : grant).ask(kern, smem)) return THD_ERR_CUDA;
     kern<<<grid, kWarps * 32, smem, st>>>(p);
   }
   if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;
@@ -551,6 +581,27 @@ extern "C" {
 size_t thd_attn_paged_workspace_size(int head_dim) {
   if (head_dim < 8 || head_dim > 128 || head_dim % 8 != 0) return 0;
   return thd::kPartAt + thd::part_bytes(head_dim > 64 ? 128 : 64);
+}
+
+size_t thd_attn_paged_weights_workspace_size(int head_dim, int num_heads_q, int batch_size, int max_seqlen_q,
+                                             int num_pages, int page_size, int max_pages, int window_left,
+                                             int sink_tokens) {
+  const size_t base = thd_attn_paged_workspace_size(head_dim);
+  if (base == 0 || num_heads_q < 1 || batch_size < 0 || max_seqlen_q < 1 || num_pages < 0 || page_size < 1 ||
+      max_pages < 0 || window_left < -1 || sink_tokens < 0)
+    return 0;
+  // keys in whole units: of a sequence at most, and, of sequences that share no pages, of all of them
+  const double unit = thd::kUnit;
+  double keys = (double)max_pages * page_size;
+  if (window_left >= 0) {
+    const double seen = (double)window_left + max_seqlen_q + sink_tokens + 3 * unit;
+    keys = seen < keys ? seen : keys;
+  }
+  double all = (double)batch_size * (keys + unit);
+  const double held = (double)num_pages * page_size + (double)batch_size * unit;
+  if (held < all) all = held;
+  const double bytes = all * num_heads_q * max_seqlen_q * 4.0;
+  return bytes < 1e15 ? (base + 15) / 16 * 16 + (size_t)bytes : 0;
 }
 
 int thd_attn_paged_window(const void* q, const void* k_cache, const void* v_cache, const int64_t* cache_strides,
@@ -633,6 +684,9 @@ int thd_attn_paged_window(const void* q, const void* k_cache, const void* v_cach
     p.w_page = weight_strides[0];
     p.w_token = weight_strides[1];
     p.w_head = weight_strides[2];
+    const size_t base = (thd_attn_paged_workspace_size(head_dim) + 15) / 16 * 16;
+    p.scores = reinterpret_cast<float*>(static_cast<char*>(workspace) + base);
+    p.score_room = workspace_bytes > base ? (long long)((workspace_bytes - base) / 4) : 0;
   }
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   wait_settings(&p.wait_limit_ns, &p.wait_check_mask, &p.inject_wait);

@@ -67,6 +67,8 @@ struct PagedArgs {
   uint32_t wait_check_mask, inject_wait;
   Split* splits;       // [ctas]
   float* key_weights;  // weights that the keys got, or null
+  float* scores;       // narrow tiles with key_weights: the scores (score_places), room for score_room of them
+  long long score_room;
   long long w_page, w_token, w_head;                                          // elements
   long long table_stride, k_page, k_token, k_head, v_page, v_token, v_head;   // elements
   int num_pages, page_size, max_pages;
@@ -202,19 +204,84 @@ struct Piece {
   long long tile_end;   // first unit after the tile's
 };
 
+// What of its sequence a tile (its s, row0 and rows set) sees: past, key_end and the window's fields.  Returns how many
+// of the tile's units hold a key that some row sees.
+template <bool kWin>
+__device__ __forceinline__ int piece_bounds(const PagedArgs& p, Piece& x) {
+  x.past = x.s.kv_len - x.s.q_len;
+  x.key_end = p.tree ? x.s.kv_len : min(x.s.kv_len, max(0, x.past + (x.row0 + x.rows - 1) / p.group + 1));
+  int last = (x.key_end + kUnit - 1) / kUnit;
+  if constexpr (kWin) {
+    const int tok0 = x.row0 / p.group, tok1 = (x.row0 + x.rows - 1) / p.group;
+    x.win_lo = window_first(p, x.past, tok0);
+    x.win_hi = window_first(p, x.past, tok1);
+    x.few = min(p.sinks, x.key_end);
+    // the units of the first keys, then from the window's first one on (one run where the two touch)
+    const int first = sink_units(p, x.s.kv_len), from = x.win_lo / kUnit;
+    x.lead = from > first ? first : 0;
+    x.skip = from > first ? from - first : 0;
+    last -= x.skip;   // a gap has the window's keys behind it
+  }
+  return last;
+}
+
+// Scores kept for the keys' weights, where they fit the call's room and every sequence is one narrow tile: of
+// sequence b the units of its tile for each key/value head, 64 scores of each of its rows a unit, sequences one
+// behind another.
+__device__ __forceinline__ long long seq_scores(const PagedArgs& p, const SeqWork& s) {
+  return (long long)p.Hkv * s.blocks * kUnit * s.q_len * p.group;
+}
+struct ScorePlaces {
+  bool fit;         // the scores are kept
+  long long base;   // first score of sequence `seq`
+};
+template <int kThreads, bool kWin>
+__device__ ScorePlaces score_places(const PagedArgs& p, int seq) {
+  __shared__ long long sums[2][kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long before = 0, all = 0;
+  bool one = p.scores != nullptr;
+  for (int b = threadIdx.x; b < p.B; b += kThreads) {
+    const SeqWork s = seq_work<kWin>(p, b, kNarrowRows);
+    const long long n = seq_scores(p, s);
+    all += n;
+    if (b < seq) before += n;
+    one = one && s.tiles <= 1;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  if (lane == 0) {
+    sums[0][warp] = before;
+    sums[1][warp] = all;
+  }
+  one = __syncthreads_and(one ? 1 : 0) != 0;
+  before = all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    before += sums[0][w];
+    all += sums[1][w];
+  }
+  return {one && all <= p.score_room, before};
+}
+
 struct PieceWalk {
   long long u, end, base, begin;
+  long long scores;   // first kept score of sequence b (kScores)
   int b;
 
   __device__ __forceinline__ explicit PieceWalk(const Share& share)
-      : u(share.begin), end(share.end), base(share.seq_base), begin(share.begin), b(share.seq) {}
+      : u(share.begin), end(share.end), base(share.seq_base), begin(share.begin), scores(0), b(share.seq) {}
 
-  template <int MT, bool kWin>
+  template <int MT, bool kWin, bool kScores = false>
   __device__ __forceinline__ bool next(const PagedArgs& p, Piece& x) {
     while (u < end) {
       x.s = seq_work<kWin>(p, b, MT);
       if (u - base >= x.s.units) {
         base += x.s.units;
+        if (kScores) scores += seq_scores(p, x.s);
         ++b;
         continue;
       }
@@ -228,20 +295,7 @@ struct PieceWalk {
       x.first = u == begin;
       x.row0 = x.tile * MT;
       x.rows = (int)min((long long)MT, (long long)x.s.q_len * p.group - x.row0);
-      x.past = x.s.kv_len - x.s.q_len;
-      x.key_end = p.tree ? x.s.kv_len : min(x.s.kv_len, max(0, x.past + (x.row0 + x.rows - 1) / p.group + 1));
-      int last = (x.key_end + kUnit - 1) / kUnit;
-      if constexpr (kWin) {
-        const int tok0 = x.row0 / p.group, tok1 = (x.row0 + x.rows - 1) / p.group;
-        x.win_lo = window_first(p, x.past, tok0);
-        x.win_hi = window_first(p, x.past, tok1);
-        x.few = min(p.sinks, x.key_end);
-        // the units of the first keys, then from the window's first one on (one run where the two touch)
-        const int first = sink_units(p, x.s.kv_len), from = x.win_lo / kUnit;
-        x.lead = from > first ? first : 0;
-        x.skip = from > first ? from - first : 0;
-        last -= x.skip;   // a gap has the window's keys behind it
-      }
+      const int last = piece_bounds<kWin>(p, x);
       x.steps = min(nblk, max(0, last - x.blk0));
       x.tile_end = base + (item + 1) * x.s.blocks;
       u += nblk;

@@ -2,7 +2,9 @@
 // cache: w_j (+)= sum over the new tokens and the query heads of the group of exp(scale q.k_j - lse).
 //
 // The log-sum-exps are those that the attention before it wrote, so this pass needs the scores once more,
-// not the values.
+// not the values.  Of narrow tiles (decoding steps) the attention keeps them, 4 bytes a row and key where reading the
+// key again is 2 d: here they only become weights.  Where they do not fit the workspace the products are taken
+// again, by this kernel for a few rows, by the one of 128 rows for more.
 #pragma once
 #include "attn_paged_common.cuh"
 
@@ -25,12 +27,72 @@ __device__ __forceinline__ bool token_sees(const PagedArgs& p, const SeqWork& s,
   return key <= own && (!kWin || key >= own - p.win_left || key < p.sinks);
 }
 
+// From kept scores: a warp takes a unit of a head, its lanes two keys each.
+template <bool kWin>
+__device__ void weights_of_scores(const PagedArgs& p) {
+  const int lane = threadIdx.x & 31;
+  const long long warps = (long long)gridDim.x * kWeightWarps;
+  long long step = (long long)blockIdx.x * kWeightWarps + (threadIdx.x >> 5), base = 0, scores = 0;
+  for (int b = 0; b < p.B; ++b) {
+    Piece x;
+    x.s = seq_work<kWin>(p, b, kNarrowRows);
+    const long long n = x.s.q_len > 0 ? (long long)p.Hkv * x.s.blocks : 0ll;
+    if (step < base + n) {
+      x.row0 = 0;
+      x.rows = x.s.q_len * p.group;
+      const int last = piece_bounds<kWin>(p, x);
+      const int32_t* table = p.table + (long long)b * p.table_stride;
+      for (; step < base + n; step += warps) {
+        const int in = (int)(step - base), head = in / x.s.blocks, blk = in - head * x.s.blocks;
+        if (blk >= last) continue;
+        const int key = unit_of<kWin>(x, blk) * kUnit + lane * 2;
+        float* place[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          place[e] = nullptr;
+          const int k = key + e;
+          // a key that no token sees is left alone: its page may be another sequence's by now
+          if (k < x.s.kv_len && (!kWin || k < p.sinks || k >= x.win_lo)) {
+            const int at = k / p.page_size, page = table[at];
+            if (page >= 0 && page < p.num_pages)
+              place[e] = p.key_weights + page * p.w_page + (k - at * p.page_size) * p.w_token + head * p.w_head;
+          }
+        }
+        const float2* src = reinterpret_cast<const float2*>(p.scores + scores + (long long)in * x.rows * kUnit) + lane;
+        float2 sum = make_float2(0.f, 0.f);
+        float had[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (place[e] && key + e < x.past) had[e] = *place[e];   // a new token's key had none
+#pragma unroll 4
+        for (int r = 0; r < x.rows; ++r) {
+          const int tok = r / p.group;
+          const float2 s = src[r * (kUnit / 2)];
+          const float l = p.lse[(long long)(head * p.group + r - tok * p.group) * p.T + x.s.q_start + tok];
+          const float l2 = l == -INFINITY ? 0.f : -1.4426950408889634f * l;   // such a row's scores are -inf
+          sum.x += ex2_approx(s.x + l2);
+          sum.y += ex2_approx(s.y + l2);
+        }
+        if (place[0]) *place[0] = had[0] + sum.x;
+        if (place[1]) *place[1] = had[1] + sum.y;
+      }
+    }
+    base += n;
+    scores += seq_scores(p, x.s);
+  }
+}
+
 template <typename DT, int DP, bool kWin>
 __global__ void __launch_bounds__(kWeightWarps * 32) attn_key_weights_kernel(const PagedArgs p) {
   constexpr int kKSteps = DP / 16;
   __shared__ Share share;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int qr = lane >> 2, qc = (lane & 3) * 2;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (score_places<kWeightWarps * 32, kWin>(p, 0).fit) {
+    weights_of_scores<kWin>(p);
+    return;
+  }
   // a unit of 64 keys of a head costs reading its keys and a step for every 8 rows
   auto cost = [&](const SeqWork& s) { return 2ll + (long long)s.q_len * p.group / 8; };
   auto whole = [&](int b) {

@@ -18,6 +18,7 @@ from . import THD_BF16, THD_FP16, THD_OK, ThdError, _check_metadata, _sink_count
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _F32 = torch.float32
+_SCORES_MAX = 1 << 30   # bytes that thd_attn_paged allocates at most for scores beside its workspace
 _Places = ctypes.c_int64 * 6
 _WeightPlaces = ctypes.c_int64 * 3
 _COUNT_MAX = 2 ** 31 - 1   # the library's counts are C ints, which ctypes would cut to 32 bits without a word
@@ -38,6 +39,17 @@ def thd_qk_norm_rope_bwd_workspace_size(head_dim):
 def thd_attn_paged_workspace_size(head_dim):
     """Bytes of device workspace thd_attn_paged needs; 0 for an unsupported head_dim."""
     return _workspace_size("thd_attn_paged_workspace_size", int(head_dim))
+
+
+def thd_attn_paged_weights_workspace_size(head_dim, num_heads_q, batch_size, max_seqlen_q, num_pages, page_size, max_pages,
+                                          window=(-1, -1), sink_tokens=0):
+    """Bytes of workspace with which thd_attn_paged reads the keys once although it adds up their weights; 0 for
+    invalid sizes."""
+    sizes = [int(x) for x in (head_dim, num_heads_q, batch_size, max_seqlen_q, num_pages, page_size, max_pages)]
+    left, sinks = _window_args(window)[0], _sink_count(sink_tokens)
+    if max(map(abs, sizes)) > _COUNT_MAX or left > _COUNT_MAX:
+        return 0
+    return int(load_library().thd_attn_paged_weights_workspace_size(*sizes, left, sinks))
 
 
 def _addr(t):
@@ -451,11 +463,17 @@ def thd_attn_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q, cu_se
         lse = torch.empty((hq, T), dtype=torch.float32, device=dev)
     else:
         _whole(lse, "lse", dev, torch.float32, (hq, T))
+    max_seqlen_q = int(max_seqlen_q)
     if workspace is None:
-        workspace = torch.empty(_workspace_size("thd_attn_paged_workspace_size", d), dtype=torch.uint8, device=dev)
+        size = _workspace_size("thd_attn_paged_workspace_size", d)
+        if key_weights is not None:
+            longest = max_seqlen_q if 0 < max_seqlen_q < T else T
+            if longest * hq <= 16 * shape[2]:   # narrow tiles: room for the scores, within reason
+                more = thd_attn_paged_weights_workspace_size(d, hq, B, longest, shape[0], shape[1], wide, (left, -1), sinks)
+                size = max(size, min(more, size + _SCORES_MAX))
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     else:
         _whole(workspace, "workspace", dev, torch.uint8)
-    max_seqlen_q = int(max_seqlen_q)
     if (T | hq | shape[2] | d | B | shape[0] | shape[1] | wide | words | abs(max_seqlen_q) | max(left, 0)) > _COUNT_MAX:
         raise _too_large("thd_attn_paged")
     _call("thd_attn_paged_window", dev, _addr(q), k_cache.data_ptr(), v_cache.data_ptr(), strides, shape[0], shape[1],
