@@ -576,7 +576,7 @@ int thd_attn_paged_window(const void* q, const void* k_cache, const void* v_cach
  * page_table_stride, max_pages  as in thd_kv_append; L is at most max_pages * page_size.
  *              A key whose entry is outside [0, num_pages) counts with weight 0 and is
  *              not moved.
- * key_weights, weight_strides  as in thd_attn_paged_window.
+ * key_weights, weight_strides  as in thd_attn_paged_window; strides below 2^31.
  * new_page_table, new_page_table_stride, new_max_pages  int32 table, laid out as page_table, of the
  *              pages that the kept keys go to; K is at most new_max_pages * page_size.  They
  *              must be none of the pages that page_table names for any key of the

@@ -53,6 +53,7 @@ def test_packed_sinks_refusals(lib, base, fn, over, status):  # noqa: F811
     (dict(table=None), -1), (dict(lens=66), -1), (dict(out=64), -1), (dict(out=128), -1), (dict(B=40, out=192), -1),
     (dict(new=16, nwide=-1), -1), (dict(new=16, nwide=4, nts=3), -1), (dict(new=18, nwide=4, nts=4), -1),
     (dict(wide=2 ** 30, ts=2 ** 30), -2), (dict(new=32, nwide=2 ** 30, nts=2 ** 30), -2), (dict(B=2 ** 27, hkv=2), -2),
+    (dict(ws=(ctypes.c_int64 * 3)(2 ** 31, 2, 1)), -2),
     (dict(B=0), 0), (dict(B=0, kc=None, w=None, kept=None, lens=None), 0)])
 def test_evict_refusals(lib, over, status):  # noqa: F811
     assert call(lib.thd_kv_evict, EVICT, EVICT, over) == status

@@ -6,9 +6,9 @@
 // slots 0 .. K - 1, in the same pages or in others.
 //
 // Two launches.  The first finds, for every (sequence, head), the weight of the last key to stay by
-// counting digits of 8 bits from the top (four passes over the weights, which lie in shared memory after the
-// first where they fit), and writes the kept slots in order.  The second moves the keys, values and weights;
-// it is what takes the time: 8 d + 8 bytes for each kept key and head, read and written once.
+// counting digits from the top (three passes over the weights, read once into shared memory where they fit
+// there), and writes the kept slots in order.  The second moves the keys, values and weights; it is bound by
+// reading and writing 4 d + 4 bytes for each kept key and head.
 #include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -24,7 +24,9 @@ namespace cg = cooperative_groups;
 constexpr int kSelectThreads = 512;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 32;                  // kept keys of a warp's step
-constexpr int kCachedMax = 160 * 1024 / 4;     // weights of a head that are held in shared memory
+constexpr int kDigit = 11;                     // bits of a pass, 10 in the last of three
+constexpr int kBins = 1 << kDigit;             // the sign, the exponent and two bits more spread the first counts
+constexpr int kCachedMax = 92 * 1024 / 4;      // weights of a run that are held in shared memory: two CTAs on an SM
 
 struct EvictArgs {
   uint16_t* kc;
@@ -36,8 +38,10 @@ struct EvictArgs {
   const int32_t* keep_lens;
   int32_t* kept;             // [B, Hkv, max_keep]
   int32_t* new_lens;
-  long long table_stride, to_stride, k_page, k_token, k_head, v_page, v_token, v_head, w_page, w_token, w_head;
+  long long table_stride, to_stride, k_page, k_token, k_head, v_page, v_token, v_head;
+  int w_page, w_token, w_head;   // 32-bit: a third of the select kernel's instructions were 64-bit products
   int num_pages, page_size, max_pages, to_pages;
+  int page_shift;            // page_size = 2^page_shift, or -1
   int sinks, recent, max_keep, cached;
   int B, Hkv, d;
 };
@@ -52,7 +56,7 @@ __device__ __forceinline__ int2 evict_lens(const EvictArgs& p, int b) {
 
 // Page and place in it of a slot; page -1 where the table names none.
 __device__ __forceinline__ int2 slot_place(const EvictArgs& p, const int32_t* table, int slot) {
-  const int at = slot / p.page_size, page = table[at];
+  const int at = p.page_shift >= 0 ? slot >> p.page_shift : slot / p.page_size, page = table[at];
   return make_int2(page >= 0 && page < p.num_pages ? page : -1, slot - at * p.page_size);
 }
 
@@ -63,63 +67,104 @@ __device__ __forceinline__ uint32_t ordered(float w) {
   return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kSelectThreads) kv_evict_select_kernel(const EvictArgs p) {
+// A cluster of CTAs takes a list: each a run of its slots, the counts of all of them read out of one another's
+// shared memory.
+__global__ void __launch_bounds__(kSelectThreads, 3) kv_evict_select_kernel(const EvictArgs p) {
   constexpr int kWarps = kSelectThreads / 32;
-  extern __shared__ uint32_t cache[];
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t s_digit, s_left;
+  extern __shared__ __align__(16) uint32_t cache[];
+  __shared__ __align__(16) uint32_t hist[2][kBins];
+  __shared__ uint32_t s_warp[kWarps], s_digit, s_left;
   __shared__ int s_more[2][kWarps], s_same[2][kWarps];
+  __shared__ int2 s_count;   // of this CTA's slots: those above the bound, and equal to it
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int b = blockIdx.x / p.Hkv, head = blockIdx.x - b * p.Hkv;
+  const int list = blockIdx.x / C, b = list / p.Hkv, head = list - b * p.Hkv;
   const int2 len = evict_lens(p, b);
   const int L = len.x, K = len.y;
   const int first = min(p.sinks, K), last = min(p.recent, K - first);
   const int take = K - first - last, end = L - last;   // `take` of the slots [first, end)
+  // this CTA's slots [from, to), whole warps of them
+  const int run = ((L + C - 1) / C + 31) & ~31;
+  const int from = (int)min((long long)L, (long long)rank * run), to = (int)min((long long)L, (long long)from + run);
   const int32_t* table = p.table + (long long)b * p.table_stride;
+  const float* weights = p.w + (long long)head * p.w_head;
   auto weight_of = [&](int slot) {
     const int2 at = slot_place(p, table, slot);
-    return at.x < 0 ? ordered(0.f) : ordered(p.w[at.x * p.w_page + at.y * p.w_token + head * p.w_head]);
+    return at.x < 0 ? ordered(0.f) : ordered(weights[(long long)at.x * p.w_page + (long long)at.y * p.w_token]);
   };
-  auto key_of = [&](int slot) { return slot - first < p.cached ? cache[slot - first] : weight_of(slot); };
 
   // ---- the least weight that stays, digit by digit ----
   uint32_t bound = take > 0 ? 0u : 0xFFFFFFFFu;   // keys above it stay
   int same = 0;                                   // and so many of those equal to it
+  const int lo = max(from, first), hi = max(lo, min(to, end));
+  const int n = hi - lo, held = min(n, p.cached);   // cache[j]: slot lo + j
+  auto key_of = [&](int slot) { return slot - lo < held ? cache[slot - lo] : weight_of(slot); };
   if (take > 0) {
-    for (int i = first + tid; i < end && i - first < p.cached; i += kSelectThreads) cache[i - first] = weight_of(i);
+    constexpr int kAhead = 8;   // weights read at once: each waits for its page's entry first
+    for (int j0 = tid; j0 < held; j0 += kSelectThreads * kAhead) {
+      uint32_t u[kAhead];
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) u[e] = j0 + e * kSelectThreads < held ? weight_of(lo + j0 + e * kSelectThreads) : 0u;
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e)
+        if (j0 + e * kSelectThreads < held) cache[j0 + e * kSelectThreads] = u[e];
+    }
     uint32_t left = take;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0u;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int bits = pass < 2 ? kDigit : 32 - 2 * kDigit, shift = 32 - min(32, (pass + 1) * kDigit);
+      uint32_t* mine = hist[pass & 1];
+      for (int i = tid; i < kBins; i += kSelectThreads) mine[i] = 0u;
       __syncthreads();
-      for (int i0 = first + warp * 32; i0 < end; i0 += kSelectThreads) {
-        const int i = i0 + lane;
-        const uint32_t u = i < end ? key_of(i) : 0u;
-        const bool in = i < end && (shift == 24 || (u >> (shift + 8)) == (bound >> (shift + 8)));
-        const uint32_t digit = in ? (u >> shift) & 255u : 256u;
-        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-        if (in && lane == __ffs(peers) - 1) atomicAdd(&hist[digit], (uint32_t)__popc(peers));
+      auto count = [&](uint32_t u) {
+        if (pass == 0 || (u ^ bound) >> (shift + bits) == 0u) atomicAdd(&mine[(u >> shift) & ((1u << bits) - 1u)], 1u);
+      };
+      for (int j = tid * 4; j < held; j += kSelectThreads * 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(cache + j);   // what lies behind the last is not counted
+        count(u.x);
+        if (j + 1 < held) count(u.y);
+        if (j + 2 < held) count(u.z);
+        if (j + 3 < held) count(u.w);
       }
+      for (int j0 = held + tid; j0 < n; j0 += kSelectThreads * kAhead) {
+        uint32_t u[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) u[e] = j0 + e * kSelectThreads < n ? weight_of(lo + j0 + e * kSelectThreads) : 0u;
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+          if (j0 + e * kSelectThreads < n) count(u[e]);
+      }
+      if (C > 1) cluster.sync(); else __syncthreads();
+      // a thread adds up kBins / kSelectThreads digits; those above them are the threads' after it
+      constexpr int kMine = kBins / kSelectThreads;
+      static_assert(kMine == 4, "a thread's digits are one 16-byte word");
+      uint4 d = make_uint4(0u, 0u, 0u, 0u);
+      for (int c = 0; c < C; ++c) {
+        const uint4* src = reinterpret_cast<const uint4*>(mine) + tid;
+        const uint4 x = C > 1 ? *cluster.map_shared_rank(src, c) : *src;
+        d.x += x.x, d.y += x.y, d.z += x.z, d.w += x.w;
+      }
+      const uint32_t sum = d.x + d.y + d.z + d.w;
+      uint32_t above = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_down_sync(0xffffffffu, above, o);
+        if (lane + o < 32) above += y;
+      }
+      if (lane == 0) s_warp[warp] = above;
       __syncthreads();
-      if (warp == 0) {   // lane l: digits [8 l, 8 l + 8); counted from the top
-        uint32_t mine = 0;
-        for (int e = 0; e < 8; ++e) mine += hist[lane * 8 + e];
-        uint32_t above = mine;
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t y = __shfl_down_sync(0xffffffffu, above, o);
-          if (lane + o < 32) above += y;
-        }
-        above -= mine;   // of the digits of the lanes after this one
-        if (above < left && left <= above + mine) {
-          for (int e = 7; e >= 0; --e) {
-            const uint32_t n = hist[lane * 8 + e];
-            if (left <= above + n) {
-              s_digit = lane * 8 + e;
-              s_left = left - above;
-              break;
-            }
-            above += n;
+      above -= sum;
+      for (int w = warp + 1; w < kWarps; ++w) above += s_warp[w];
+      if (above < left && left <= above + sum) {
+        const uint32_t of[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int e = 3; e >= 0; --e) {
+          if (above < left && left <= above + of[e]) {
+            s_digit = tid * 4 + e;
+            s_left = left - above;
           }
+          above += of[e];
         }
       }
       __syncthreads();
@@ -128,14 +173,10 @@ __global__ void __launch_bounds__(kSelectThreads) kv_evict_select_kernel(const E
     }
     same = (int)left;
   }
-
-  // ---- the kept slots, in order ----
-  int32_t* kept = p.kept + (long long)blockIdx.x * p.max_keep;
-  int more_before = 0, same_before = 0;
-  for (int i0 = 0, turn = 0; i0 < L; i0 += kSelectThreads, turn ^= 1) {
-    const int i = i0 + tid;
-    bool more = false, equal = false;
-    if (i < L) {
+  // whether a slot stays whatever its equals do, and whether it is one of those equal to the bound
+  auto judge = [&](int i, bool& more, bool& equal) {
+    more = equal = false;
+    if (i < to) {
       if (i < first || i >= end) {
         more = true;
       } else if (take > 0) {
@@ -144,29 +185,73 @@ __global__ void __launch_bounds__(kSelectThreads) kv_evict_select_kernel(const E
         equal = u == bound;
       }
     }
-    const uint32_t more_bits = __ballot_sync(0xffffffffu, more), same_bits = __ballot_sync(0xffffffffu, equal);
+  };
+
+  // ---- what the CTAs before this one keep ----
+  int more_before = 0, same_before = 0;
+  if (C > 1) {
+    int2 n = make_int2(0, 0);
+    if (tid == 0) s_count = n;
+    __syncthreads();
+    for (int i = from + tid; i < to; i += kSelectThreads) {
+      bool more, equal;
+      judge(i, more, equal);
+      n.x += more ? 1 : 0;
+      n.y += equal ? 1 : 0;
+    }
+    n.x = __reduce_add_sync(0xffffffffu, n.x);
+    n.y = __reduce_add_sync(0xffffffffu, n.y);
     if (lane == 0) {
-      s_more[turn][warp] = __popc(more_bits);
-      s_same[turn][warp] = __popc(same_bits);
+      atomicAdd(&s_count.x, n.x);
+      atomicAdd(&s_count.y, n.y);
+    }
+    cluster.sync();
+    for (int c = 0; c < rank; ++c) {
+      const int2 other = *cluster.map_shared_rank(&s_count, c);
+      more_before += other.x;
+      same_before += other.y;
+    }
+    cluster.sync();   // no CTA leaves while another may read its counts
+  }
+
+  // ---- the kept slots, in order: a warp 32 slots of each of kWords runs one after another ----
+  constexpr int kWords = 4;
+  int32_t* kept = p.kept + (long long)list * p.max_keep;
+  for (int i0 = from, turn = 0; i0 < to; i0 += kSelectThreads * kWords, turn ^= 1) {
+    uint32_t more_bits[kWords], same_bits[kWords];
+    int m_sum = 0, e_sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      bool more, equal;
+      judge(i0 + (warp * kWords + w) * 32 + lane, more, equal);
+      more_bits[w] = __ballot_sync(0xffffffffu, more);
+      same_bits[w] = __ballot_sync(0xffffffffu, equal);
+      m_sum += __popc(more_bits[w]);
+      e_sum += __popc(same_bits[w]);
+    }
+    if (lane == 0) {
+      s_more[turn][warp] = m_sum;
+      s_same[turn][warp] = e_sum;
     }
     __syncthreads();
-    int m = more_before, e = same_before;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == warp) {
-        m += __popc(more_bits & ((1u << lane) - 1u));
-        e += __popc(same_bits & ((1u << lane) - 1u));
-        if (more || (equal && e < same)) kept[m + min(e, same)] = i;
-      }
-      more_before += s_more[turn][w];
-      same_before += s_same[turn][w];
-      if (w < warp) {
-        m += s_more[turn][w];
-        e += s_same[turn][w];
-      }
+    // what the warps before this one keep, and all of them
+    const int x = lane < kWarps ? s_more[turn][lane] : 0, y = lane < kWarps ? s_same[turn][lane] : 0;
+    int m = more_before + __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
+    int e = same_before + __reduce_add_sync(0xffffffffu, lane < warp ? y : 0);
+    more_before += __reduce_add_sync(0xffffffffu, x);
+    same_before += __reduce_add_sync(0xffffffffu, y);
+    const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      const int me = m + __popc(more_bits[w] & below), ee = e + __popc(same_bits[w] & below);
+      if ((more_bits[w] >> lane & 1) || ((same_bits[w] >> lane & 1) && ee < same))
+        kept[me + min(ee, same)] = i0 + (warp * kWords + w) * 32 + lane;
+      m += __popc(more_bits[w]);
+      e += __popc(same_bits[w]);
     }
   }
-  for (int i = K + tid; i < p.max_keep; i += kSelectThreads) kept[i] = -1;
-  if (head == 0 && tid == 0) p.new_lens[b] = K;
+  for (int i = K + rank * kSelectThreads + tid; i < p.max_keep; i += C * kSelectThreads) kept[i] = -1;
+  if (head == 0 && rank == 0 && tid == 0) p.new_lens[b] = K;
 }
 
 // Moves: a warp takes 32 kept keys.  A lane finds where one of them lies and goes; then the lanes carry
@@ -185,8 +270,8 @@ __device__ __forceinline__ Moves find_moves(const EvictArgs& p, int b, int head,
     const int2 f = slot_place(p, p.table + (long long)b * p.table_stride, slot);
     const int2 t = slot_place(p, p.to_table + (long long)b * p.to_stride, at);
     if (f.x >= 0 && t.x >= 0 && (f.x != t.x || f.y != t.y)) {
-      m.from = f.x * p.w_page + f.y * p.w_token + head * p.w_head;
-      m.to = t.x * p.w_page + t.y * p.w_token + head * p.w_head;
+      m.from = (long long)f.x * p.w_page + (long long)f.y * p.w_token + (long long)head * p.w_head;
+      m.to = (long long)t.x * p.w_page + (long long)t.y * p.w_token + (long long)head * p.w_head;
       m.kf = f.x * p.k_page + f.y * p.k_token + head * p.k_head;
       m.kt = t.x * p.k_page + t.y * p.k_token + head * p.k_head;
       m.vf = f.x * p.v_page + f.y * p.v_token + head * p.v_head;
@@ -245,7 +330,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_evict_within_kernel(const Evi
 }
 
 // Into other pages: steps of 32 kept keys over all lists, laid end to end, a warp each.
-__global__ void __launch_bounds__(kMoveThreads) kv_evict_apart_kernel(const EvictArgs p) {
+__global__ void __launch_bounds__(kMoveThreads, 2) kv_evict_apart_kernel(const EvictArgs p) {
   constexpr int kWarps = kMoveThreads / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
@@ -259,16 +344,29 @@ __global__ void __launch_bounds__(kMoveThreads) kv_evict_apart_kernel(const Evic
       const int in = (int)(step - base), head = in / per, at = (in - head * per) * kMoveRows;
       const Moves m = find_moves(p, b, head, at + lane, K);
       if (m.to >= 0) p.w[m.to] = p.w[m.from];
-      for (int i = 0; i < kMoveRows; i += rows) {
-        const int src = (i + row) & 31;
-        const long long kf = __shfl_sync(0xffffffffu, m.kf, src), vf = __shfl_sync(0xffffffffu, m.vf, src);
-        const long long kt = __shfl_sync(0xffffffffu, m.kt, src), vt = __shfl_sync(0xffffffffu, m.vt, src);
-        const bool go = __shfl_sync(0xffffffffu, m.to, src) >= 0 && i + row < kMoveRows && row < rows;
-        if (go) {
-          const uint4 k = *reinterpret_cast<const uint4*>(p.kc + kf + col);
-          const uint4 v = *reinterpret_cast<const uint4*>(p.vc + vf + col);
-          *reinterpret_cast<uint4*>(p.kc + kt + col) = k;
-          *reinterpret_cast<uint4*>(p.vc + vt + col) = v;
+      constexpr int kPieces = 8;   // of keys and of values that a lane holds: reads on the way before the first write
+#pragma unroll 1
+      for (int i0 = 0; i0 < kMoveRows; i0 += rows * kPieces) {
+        uint4 k[kPieces], v[kPieces];
+#pragma unroll
+        for (int e = 0; e < kPieces; ++e) {
+          const int src = i0 + e * rows + row;
+          const long long kf = __shfl_sync(0xffffffffu, m.kf, src & 31), vf = __shfl_sync(0xffffffffu, m.vf, src & 31);
+          const bool go = __shfl_sync(0xffffffffu, m.to, src & 31) >= 0 && src < kMoveRows && row < rows;
+          if (go) {
+            k[e] = *reinterpret_cast<const uint4*>(p.kc + kf + col);
+            v[e] = *reinterpret_cast<const uint4*>(p.vc + vf + col);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kPieces; ++e) {
+          const int src = i0 + e * rows + row;
+          const long long kt = __shfl_sync(0xffffffffu, m.kt, src & 31), vt = __shfl_sync(0xffffffffu, m.vt, src & 31);
+          const bool go = __shfl_sync(0xffffffffu, m.to, src & 31) >= 0 && src < kMoveRows && row < rows;
+          if (go) {
+            *reinterpret_cast<uint4*>(p.kc + kt + col) = k[e];
+            *reinterpret_cast<uint4*>(p.vc + vt + col) = v[e];
+          }
         }
       }
     }
@@ -298,6 +396,8 @@ extern "C" int thd_kv_evict(void* k_cache, void* v_cache, const int64_t* cache_s
     if (cache_strides[i] < 0 || cache_strides[i] % 8 != 0) return THD_ERR_ARG;
   for (int i = 0; i < 3; ++i)
     if (weight_strides[i] < 0) return THD_ERR_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (weight_strides[i] >= (1ll << 31)) return THD_ERR_UNSUPPORTED;
   if (new_page_table) {
     if (new_max_pages < 0 || new_page_table_stride < new_max_pages) return THD_ERR_ARG;
     if ((long long)new_max_pages * page_size >= (1ll << 31) - 4096) return THD_ERR_UNSUPPORTED;
@@ -334,11 +434,14 @@ extern "C" int thd_kv_evict(void* k_cache, void* v_cache, const int64_t* cache_s
   p.v_page = cache_strides[3];
   p.v_token = cache_strides[4];
   p.v_head = cache_strides[5];
-  p.w_page = weight_strides[0];
-  p.w_token = weight_strides[1];
-  p.w_head = weight_strides[2];
+  p.w_page = (int)weight_strides[0];
+  p.w_token = (int)weight_strides[1];
+  p.w_head = (int)weight_strides[2];
   p.num_pages = num_pages;
   p.page_size = page_size;
+  p.page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (page_size == 1 << s) p.page_shift = s;
   p.max_pages = max_pages;
   p.sinks = sink_tokens;
   p.recent = recent_tokens;
@@ -347,34 +450,45 @@ extern "C" int thd_kv_evict(void* k_cache, void* v_cache, const int64_t* cache_s
   p.Hkv = num_heads_kv;
   p.d = head_dim;
   const long long room = (long long)max_pages * page_size;
-  p.cached = (int)(room < kCachedMax ? room : kCachedMax);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int lists = batch_size * num_heads_kv;
+  int C = 1;   // CTAs of a list: the lists alone may not fill the GPU
+  while (C < 8 && 2ll * C * lists <= sms) C *= 2;
+  // a list is selected by as many as hold its weights in shared memory (27000 of them read again from the L2 where
+  // they did not fit cost 60 us of 94), or, of few lists, with 4096 slots each or more
+  int Cs = 1;
+  while (Cs < 8 && (room / Cs > kCachedMax || (Cs < C && room / Cs > 4096))) Cs *= 2;
+  const long long run = ((room + Cs - 1) / Cs + 31) / 32 * 32;
+  p.cached = (int)(run < kCachedMax ? (run + 3) / 4 * 4 : kCachedMax);
   static SmemGrant grant;
   if (!grant.ask(kv_evict_select_kernel, kCachedMax * 4)) return THD_ERR_CUDA;
-  kv_evict_select_kernel<<<lists, kSelectThreads, (size_t)p.cached * 4, st>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;
-
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[2]{};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = Cs;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.blockDim = dim3(kMoveThreads);
+  cfg.numAttrs = Cs > 1 ? 1 : 0;
   cfg.stream = st;
+  cfg.gridDim = dim3(lists * Cs);
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = (size_t)p.cached * 4;
+  if (cudaLaunchKernelEx(&cfg, kv_evict_select_kernel, static_cast<const EvictArgs>(p)) != cudaSuccess) return THD_ERR_CUDA;
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = 0;
   cudaError_t e;
   if (within) {
-    int C = 1;   // CTAs of a list: the lists alone may not fill the GPU
-    while (C < 8 && 2 * C * lists <= 2 * sms) C *= 2;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = C;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
+    attr[0].val.clusterDim.x = C;
+    cfg.attrs = C > 1 ? attr : attr + 1;
+    cfg.numAttrs = C > 1 ? 2 : 1;
     cfg.gridDim = dim3(lists * C);
     e = cudaLaunchKernelEx(&cfg, kv_evict_within_kernel, static_cast<const EvictArgs>(p));
   } else {
-    cfg.gridDim = dim3(4 * sms);
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(2 * sms);
     e = cudaLaunchKernelEx(&cfg, kv_evict_apart_kernel, static_cast<const EvictArgs>(p));
   }
   return e == cudaSuccess ? THD_OK : THD_ERR_CUDA;

@@ -296,6 +296,23 @@ def thd_qk_norm_rope_bwd(grad_q, grad_k, q, k, cu_seqlens, rope_cos=None, rope_s
     return dq, dk, grads[0], grads[1]
 
 
+def _table(t, name, device, batch_size):
+    """Entries of a sequence in a page table, and the stride of its rows."""
+    if type(t) is not torch.Tensor or t.get_device() != device.index:
+        _on(t, name, device)
+    if t.dtype is not torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if t.dim() != 2 or t.shape[0] < batch_size:
+        raise ValueError(f"{name} must be [>= batch_size, pages]")
+    wide = t.shape[1]
+    if wide > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the entries of a sequence must be contiguous")
+    step = t.stride(0) if t.shape[0] > 1 else wide
+    if step < wide:
+        raise ValueError(f"{name}: rows overlap")
+    return wide, step
+
+
 def _caches(k_cache, v_cache, device, dtype, page_table, batch_size, writes):
     """Strides of the two caches (ctypes int64[6]: page, token, head of each), and the table's."""
     if (type(k_cache) is torch.Tensor is type(v_cache) and k_cache.is_contiguous() and v_cache.is_contiguous()
@@ -328,35 +345,34 @@ def _caches(k_cache, v_cache, device, dtype, page_table, batch_size, writes):
                     raise ValueError(f"{name}: places overlap")
                 need = step * n
         places += (page if pages > 1 else 0, token if size > 1 else 0, head if heads > 1 else 0)
-    if type(page_table) is not torch.Tensor or page_table.get_device() != device.index:
-        _on(page_table, "page_table", device)
-    if page_table.dtype is not torch.int32:
-        raise TypeError("page_table must be int32")
-    if page_table.dim() != 2 or page_table.shape[0] < batch_size:
-        raise ValueError("page_table must be [>= batch_size, pages]")
-    wide = page_table.shape[1]
-    if wide > 1 and page_table.stride(1) != 1:
-        raise ValueError("page_table: the entries of a sequence must be contiguous")
-    step = page_table.stride(0) if page_table.shape[0] > 1 else wide
-    if step < wide:
-        raise ValueError("page_table: rows overlap")
+    wide, step = _table(page_table, "page_table", device, batch_size)
     return shape, _Places(*places), wide, step
 
 
-def _key_weights(t, device, shape):
-    """Strides of the keys' weights (ctypes int64[3]: page, token, head), which are written."""
-    _on(t, "key_weights", device)
-    if t.dtype is not _F32:
-        raise TypeError("key_weights must be float32")
-    if tuple(t.shape) != tuple(shape[:3]):
-        raise ValueError("key_weights must be [pages, page_size, Hkv], as the caches")
-    steps = [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)]
+@functools.lru_cache(maxsize=256)
+def _weight_places(shape, strides):
+    """Strides (ctypes int64[3]: page, token, head) of a tensor of keys' weights; None where its places overlap."""
+    steps = [s if n > 1 else 0 for s, n in zip(strides, shape)]
     need = 1
-    for step, n in sorted((s, n) for s, n in zip(steps, t.shape) if n > 1):
+    for step, n in sorted((s, n) for s, n in zip(steps, shape) if n > 1):
         if step < need:
-            raise ValueError("key_weights: places overlap")
+            return None
         need = step * (n - 1) + need
     return _WeightPlaces(*steps)
+
+
+def _key_weights(t, device, shape):
+    """Strides of the keys' weights, which are written."""
+    if not (type(t) is torch.Tensor and t.dtype is _F32 and t.get_device() == device.index):
+        _on(t, "key_weights", device)
+        if t.dtype is not _F32:
+            raise TypeError("key_weights must be float32")
+    if t.shape != shape[:3]:
+        raise ValueError("key_weights must be [pages, page_size, Hkv], as the caches")
+    places = _weight_places(tuple(t.shape), t.stride())
+    if places is None:
+        raise ValueError("key_weights: places overlap")
+    return places
 
 
 def thd_kv_append(k, v, k_cache, v_cache, page_table, cache_lens, cu_seqlens, cu_seqlens_padded=None,
@@ -514,7 +530,7 @@ def thd_kv_evict(k_cache, v_cache, key_weights, page_table, kv_lens, keep_lens, 
         raise ValueError("a page must hold a token")
     new_wide, new_step = wide, step
     if new_page_table is not None:
-        _, _, new_wide, new_step = _caches(k_cache, v_cache, dev, dtype, new_page_table, B, True)
+        new_wide, new_step = _table(new_page_table, "new_page_table", dev, B)
     places = _key_weights(key_weights, dev, shape)
     if kept is None:
         kept = torch.empty((B, shape[2], min(wide, new_wide) * shape[1]), dtype=torch.int32, device=dev)
