@@ -22,15 +22,11 @@
 //         are added to the fp32 accumulator by bulk tensor reductions (TMA).
 //   post  dQ = scale * accumulator, rounded to the input type; dK / dV of keys whose
 //         sums several items share.
-// Under a window with first keys that stay visible (p.sinks) a tile of those keys is seen by every
-// query behind it: 512 query tiles and more where a window's tile has ten, one after another on one SM.  Its
-// item therefore takes the queries of its window only; the others are items of 16 query tiles
-// (far_chunks), which write their fp32 sums for the post kernel to add up in their order.  65536 rows of
-// one sequence, 16 + 4 heads of 64, fp16, window 1023, 16 such keys: 2.09 ms, against 9.01 in one item each.
 // head_dim 64 or 128 (TMA loads).  Eight warps: warps w and w + 4 read the
 // same TMEM lanes and split the columns of the elementwise step, the dQ
 // staging and the dK / dV epilogue; the next query tile's Q and dO load while
 // the current tile's dQ is added.
+// Under a window with first keys that stay visible (p.sinks) the main pass is attn_bwd_ws.cuh's.
 #pragma once
 #include "attn_common.cuh"
 
@@ -44,17 +40,27 @@ struct BwdParams {
   void* dv;            // [T, Hkv, d]
   float* dacc;         // fp32 [T, Hq, d] dQ accumulator (workspace)
   float* D;            // fp32 [Hq, T] (workspace)
-  // shared sums (workspace; kSinks with far_tiles): dK (unscaled) and dV, [2][rows][d] each, of the
+  // shared sums (workspace; with far_tiles): dK (unscaled) and dV, [2][rows][d] each, of the
   // items themselves, [B][Hkv][tiles], and of the far items, [slots][Hkv][tiles]
   float* near_sums;
   float* far_sums;
   int far_rows, far_key_tiles;   // rows: keys of a tile that stay visible at most; tiles of such keys at most
 };
 
-// Query tiles of a far item.  Its work is that of an ordinary item under a window of 2048.
+// A tile of first keys that stay visible is seen by every query behind it: 512 query tiles and more where a
+// window's tile has ten, one after another on one SM.  Its item therefore takes the queries of its window
+// only; the others are items of 16 query tiles (far_chunks), which write their fp32 sums for the post kernel to
+// add up in their order.  65536 rows of one sequence, 16 + 4 heads of 64, fp16, window 1023, 16 such keys, on
+// the kernel below: 2.09 ms, against 9.01 in one item each.
+// Query tiles of a far item: its work is that of an ordinary item under a window of 2048.
 constexpr int kFarTiles = 16;
 // Tiles of this many first keys are split; more of them are many items without that.
 constexpr int kFarMaxSinks = 512;
+
+// There, fp16 weights are held times 2^14 for the product with dO: of weights near 2^-10, as a window of 1024 has,
+// many lie below 2^-14, where fp16 rounds to multiples of 2^-24, and dV of the case above was 1.5 times as far from
+// 64 bits as without it.
+constexpr float kBwdLift = 14.f, kBwdUnlift = 0x1p-14f;
 
 // Slot of chunk c of sequence b: sequences lie one behind another, so chunks counted from each one's start
 // take floor(start / rows) + b and the numbers after it, at most B + T / rows in all.
@@ -217,10 +223,7 @@ static_assert(sizeof(BwdSmem<64>) + 1024 <= 227 * 1024 && sizeof(BwdSmem<128>) +
 
 constexpr int kBwdThreads = 256;   // 8 warps: warps w and w + 4 share TMEM lanes, split the columns
 
-// kSinks: a window with first keys that stay visible.  There, fp16 weights are held times 2^14 for the product
-// with dO: of weights near 2^-10, as a window of 1024 has, many lie below 2^-14, where fp16 rounds to multiples
-// of 2^-24, and dV of the case above was 1.5 times as far from 64 bits as without it.
-template <typename DT, int DP, bool kSinks>
+template <typename DT, int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -240,8 +243,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   constexpr uint32_t idesc_dq = umma_idesc_f16_ab(Tr::kBF16, kTileM, DP, true, true);
   constexpr uint32_t hi = smem_desc_sw128_hi(1024);
   constexpr int kHalfChunks = DP / 64;   // 32-column chunks of a head_dim-wide row per half
-  constexpr bool kLifted = kSinks && !Tr::kBF16;
-  constexpr float kLift = kLifted ? 14.f : 0.f, kUnlift = kLifted ? 0x1p-14f : 1.f;
 
   if (tid == 0) {
     mbar_init(&sm.bar_kv, 1);
@@ -309,24 +310,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int key = kv0 + row;                       // this thread's key position (TMEM lane)
     // query tiles holding a query that sees a key of [kv0, kv0 + 128): query i sees key j
     // only if i + shift - lo_off <= j <= i + shift + hi_off
-    // (or, kSinks, j < sinks and the mask type allows it)
-    const bool has_sinks = kSinks && kv0 < p.sinks;
-    const int sink_hi = s.causal ? 0 : kNoBound;
-    const long long first_q = (long long)kv0 - s.shift - (has_sinks ? sink_hi : s.hi_off);
-    int qt_first = first_q <= 0 ? 0 : (int)min(first_q / kTileM, (long long)INT32_MAX);
-    const int nqt_all = (s.q_len + kTileM - 1) / kTileM, near = near_query_tiles(s, kv0);
-    int nqt = near;
-    bool shared = false;   // the sums of the keys that stay visible are added up by the post kernel
-    if (has_sinks) {
-      const bool far = p.far_tiles > 0 && near < nqt_all;
-      shared = far;
-      if (kSinks && it.far >= 0) {
-        qt_first = max(near, it.far * p.far_tiles);
-        nqt = min(nqt_all, (it.far + 1) * p.far_tiles);
-      } else if (!far) {
-        nqt = nqt_all;
-      }
-    }
+    const long long first_q = (long long)kv0 - s.shift - s.hi_off;
+    const long long last_q = (long long)kv0 + kTileM - 1 - s.shift + s.lo_off;
+    const int qt_first = first_q <= 0 ? 0 : (int)min(first_q / kTileM, (long long)INT32_MAX);
+    const int nqt_all = (s.q_len + kTileM - 1) / kTileM;
+    const int nqt = last_q < 0 ? 0 : (int)min((long long)nqt_all, last_q / kTileM + 1);
     const bool any = s.q_len > 0 && qt_first < nqt;
     if (any && tid == 0) {
       kv_par = (int)ph_kv;
@@ -362,8 +350,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int q0 = qt * kTileM;
         const int rows_q = min(kTileM, s.q_len - q0);
         if (tid < kTileM) {
-          sm.lse2[tid] = nl2 - kLift;
-          sm.dd[tid] = ndd * kUnlift;
+          sm.lse2[tid] = nl2;
+          sm.dd[tid] = ndd;
         }
         __syncthreads();
         // ---- S^T = K Q^T, dP^T = V dO^T ----
@@ -415,9 +403,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // q0 + c sees key j iff j - shift - hi_off <= q0 + c <= j - shift + lo_off)
         const bool kvalid = key < s.kv_len;
         const long long kd = (long long)key - s.shift - q0;
-        const bool sink = kSinks && key < p.sinks;
-        const int c_lo = (int)min(max(kd - (sink ? sink_hi : s.hi_off), -1ll), (long long)kTileM);
-        const int c_hi = (int)max(min(kd + (sink ? kNoBound : s.lo_off), (long long)rows_q - 1), -1ll);
+        const int c_lo = (int)min(max(kd - s.hi_off, -1ll), (long long)kTileM);
+        const int c_hi = (int)max(min(kd + s.lo_off, (long long)rows_q - 1), -1ll);
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int c0 = 2 * half + cc;   // 32-column chunk
@@ -436,8 +423,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               for (int u = 0; u < 2; ++u) {
                 const int c = 32 * c0 + 2 * e + u;
                 pv[u] = ex2_approx(fmaf(__uint_as_float(sr[2 * e + u]), sl2, -sm.lse2[c]));
-                dsv[u] = pv[u] * (kLifted ? fmaf(__uint_as_float(dr[2 * e + u]), kUnlift, -sm.dd[c])
-                                          : __uint_as_float(dr[2 * e + u]) - sm.dd[c]);
+                dsv[u] = pv[u] * (__uint_as_float(dr[2 * e + u]) - sm.dd[c]);
               }
               pp[e] = Tr::pack2(pv[0], pv[1]);
               pd[e] = Tr::pack2(dsv[0], dsv[1]);
@@ -452,8 +438,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const bool vis = kvalid && c >= c_lo && c <= c_hi;
                 const float x = ex2_approx(fmaf(__uint_as_float(sr[2 * e + u]), sl2, -sm.lse2[c]));
                 pv[u] = vis ? x : 0.f;
-                dsv[u] = pv[u] * (kLifted ? fmaf(__uint_as_float(dr[2 * e + u]), kUnlift, -sm.dd[c])
-                                          : __uint_as_float(dr[2 * e + u]) - sm.dd[c]);
+                dsv[u] = pv[u] * (__uint_as_float(dr[2 * e + u]) - sm.dd[c]);
               }
               pp[e] = Tr::pack2(pv[0], pv[1]);
               pd[e] = Tr::pack2(dsv[0], dsv[1]);
@@ -539,40 +524,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
 
     // ---- dK, dV rows of this key tile (one column half per thread) ----
-    if (kSinks && it.far >= 0 && !any) {
-      // a chunk of queries that are all near the tile: nothing to add
-    } else if (keys_valid > 0) {
-      // rows whose sums are shared go to their place as they are (kSinks); a far item has no others
-      const bool to_sums = shared && key < min(p.sinks, s.kv_len);
-      const bool row_ok = row < keys_valid && !to_sums && !(kSinks && it.far >= 0);
-      if (kSinks && shared) {
-        const long long place = it.far >= 0 ? far_slot(s, it.b, it.far) : (long long)it.b;
-        float* sums = (it.far >= 0 ? bp.far_sums : bp.near_sums) +
-                      ((place * p.Hkv + g) * bp.far_key_tiles + it.qblock) * (2ll * bp.far_rows * p.d) + (long long)row * p.d;
-#pragma unroll
-        for (int cc = 0; cc < kHalfChunks; ++cc) {
-          const int c = half * kHalfChunks + cc;
-          uint32_t a[32], b[32];
-          if (any && !first) {
-            tmem_ld32(tDK + t_lane + 32 * c, a);
-            tmem_ld32(tDV + t_lane + 32 * c, b);
-            tmem_ld_wait_regs32(a);
-            tmem_tie_regs32(b);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) a[e] = b[e] = 0u;
-          }
-          if (to_sums) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              *reinterpret_cast<uint4*>(sums + 32 * c + e) = make_uint4(a[e], a[e + 1], a[e + 2], a[e + 3]);
-              *reinterpret_cast<float4*>(sums + (long long)bp.far_rows * p.d + 32 * c + e) =
-                  make_float4(__uint_as_float(b[e]) * kUnlift, __uint_as_float(b[e + 1]) * kUnlift,
-                              __uint_as_float(b[e + 2]) * kUnlift, __uint_as_float(b[e + 3]) * kUnlift);
-            }
-          }
-        }
-      }
+    if (keys_valid > 0) {
+      const bool row_ok = row < keys_valid;
       const size_t base = ((size_t)(s.kv_start + (row_ok ? key : kv0)) * p.Hkv + g) * (size_t)p.d;
       DT* dkp = static_cast<DT*>(bp.dk) + base;
       DT* dvp = static_cast<DT*>(bp.dv) + base;
@@ -593,10 +546,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               x.y = Tr::pack2(__uint_as_float(a[e + 2]) * p.scale, __uint_as_float(a[e + 3]) * p.scale);
               x.z = Tr::pack2(__uint_as_float(a[e + 4]) * p.scale, __uint_as_float(a[e + 5]) * p.scale);
               x.w = Tr::pack2(__uint_as_float(a[e + 6]) * p.scale, __uint_as_float(a[e + 7]) * p.scale);
-              y.x = Tr::pack2(__uint_as_float(b[e]) * kUnlift, __uint_as_float(b[e + 1]) * kUnlift);
-              y.y = Tr::pack2(__uint_as_float(b[e + 2]) * kUnlift, __uint_as_float(b[e + 3]) * kUnlift);
-              y.z = Tr::pack2(__uint_as_float(b[e + 4]) * kUnlift, __uint_as_float(b[e + 5]) * kUnlift);
-              y.w = Tr::pack2(__uint_as_float(b[e + 6]) * kUnlift, __uint_as_float(b[e + 7]) * kUnlift);
+              y.x = Tr::pack2(__uint_as_float(b[e]), __uint_as_float(b[e + 1]));
+              y.y = Tr::pack2(__uint_as_float(b[e + 2]), __uint_as_float(b[e + 3]));
+              y.z = Tr::pack2(__uint_as_float(b[e + 4]), __uint_as_float(b[e + 5]));
+              y.w = Tr::pack2(__uint_as_float(b[e + 6]), __uint_as_float(b[e + 7]));
               *reinterpret_cast<uint4*>(dkp + 32 * c + e) = x;
               *reinterpret_cast<uint4*>(dvp + 32 * c + e) = y;
             }

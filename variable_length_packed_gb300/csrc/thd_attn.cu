@@ -14,6 +14,7 @@
 #include "attn_fwd_serial.cuh"
 #include "attn_fwd_ws.cuh"
 #include "attn_bwd.cuh"
+#include "attn_bwd_ws.cuh"
 
 namespace thd {
 cudaError_t launch_padding_mask(const int32_t* cu, int B, int S, uint8_t* mask, int num_sms, cudaStream_t stream);
@@ -101,14 +102,14 @@ int claim_for(int max_seqlen, long long min_items, int ctas) {
   return c < 1 ? 1 : (c > 8 ? 8 : c);
 }
 
-// 2-D view [rows, heads * d] of a THD tensor, box = 128 rows x 64 columns,
+// 2-D view [rows, heads * d] of a THD tensor, box = 128 rows (or box_rows) x 64 columns,
 // 128-byte swizzle (the layout the UMMA shared-memory descriptors expect).
-bool encode_thd_map(CUtensorMap* map, const void* base, int rows, int heads, int d, bool bf16) {
+bool encode_thd_map(CUtensorMap* map, const void* base, int rows, int heads, int d, bool bf16, int box_rows = 128) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)heads * (cuuint64_t)d, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)heads * (cuuint64_t)d * 2ull};
-  cuuint32_t box[2] = {64u, 128u};
+  cuuint32_t box[2] = {64u, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1u, 1u};
   CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -223,11 +224,19 @@ int launch_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& 
   const int small_grid = sms * 8;
   thd::attn_bwd_pre_kernel<DT><<<small_grid, 256, 0, stream>>>(bp);
   if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;
-  auto kern = bp.a.sinks > 0 ? thd::attn_bwd_kernel<DT, DP, true> : thd::attn_bwd_kernel<DT, DP, false>;
-  const size_t smem = one_cta_per_sm(sizeof(thd::BwdSmem<DP>) + 1024);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return THD_ERR_CUDA;
-  kern<<<sms, thd::kBwdThreads, smem, stream>>>(mq, mk, mv, mdo, mdq, bp);
+  if (bp.a.sinks > 0) {
+    auto kern = thd::attn_bwd_ws_kernel<DT, DP>;
+    const size_t smem = one_cta_per_sm(sizeof(thd::BwsSmem<DP>) + 1024);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      return THD_ERR_CUDA;
+    kern<<<sms, thd::kBwsThreads, smem, stream>>>(mq, mk, mv, mdo, mdq, bp);
+  } else {
+    auto kern = thd::attn_bwd_kernel<DT, DP>;
+    const size_t smem = one_cta_per_sm(sizeof(thd::BwdSmem<DP>) + 1024);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      return THD_ERR_CUDA;
+    kern<<<sms, thd::kBwdThreads, smem, stream>>>(mq, mk, mv, mdo, mdq, bp);
+  }
   if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;
   thd::attn_bwd_post_kernel<DT><<<small_grid, 256, 0, stream>>>(bp);
   return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
@@ -331,10 +340,11 @@ int thd_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* 
   if (cudaMemsetAsync(workspace, 0, 16, st) != cudaSuccess) return THD_ERR_CUDA;
   const bool bf16 = dtype == THD_BF16;
   CUtensorMap mq, mk, mv, mdo, mdq;
-  if (!encode_thd_map(&mq, q, total_tokens, num_heads_q, head_dim, bf16) ||
+  const int q_box = p.sinks == 0 ? thd::kTileM : (head_dim == 128 ? thd::BwsShape<128>::kBQ : thd::BwsShape<64>::kBQ);
+  if (!encode_thd_map(&mq, q, total_tokens, num_heads_q, head_dim, bf16, q_box) ||
       !encode_thd_map(&mk, k, total_tokens, num_heads_kv, head_dim, bf16) ||
       !encode_thd_map(&mv, v, total_tokens, num_heads_kv, head_dim, bf16) ||
-      !encode_thd_map(&mdo, dout, total_tokens, num_heads_q, head_dim, bf16) ||
+      !encode_thd_map(&mdo, dout, total_tokens, num_heads_q, head_dim, bf16, q_box) ||
       !encode_f32_map(&mdq, bp.dacc, total_tokens, (long long)num_heads_q * head_dim))
     return THD_ERR_CUDA;
   if (bf16) {
