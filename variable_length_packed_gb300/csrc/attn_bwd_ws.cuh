@@ -46,7 +46,7 @@ struct BwsSmem {
   alignas(1024) uint8_t dout[kQ][kQBytes];
   alignas(1024) uint8_t ds[kDS][kDsBytes];
   alignas(1024) uint8_t stage[DP == 64 ? kBQ * DP * 4 : 16];   // dQ on its way out (heads of 64)
-  alignas(16) float lse2[kQ][kBQ], dd[kQ][kBQ];
+  alignas(16) float lse2[kQ][kBQ], dd[kQ][kBQ];   // negative: -LSE * log2(e), -D of the step's queries
   uint64_t item_full[2], item_empty[2], k_full, v_full, k_empty, v_empty, q_full[kQ], q_empty[kQ];
   uint64_t s_full, s_empty, dp_full, ps_full, dv_done, ds_empty[kDS], dq_full, dq_empty, acc_full, acc_empty, drain;
   uint32_t tmem_base, abort;
@@ -159,8 +159,8 @@ __device__ void bws_producer(BwsSmem<DP>& sm, const BwdParams& bp, const CUtenso
       float l_now[kStats], d_now[kStats];
 #pragma unroll
       for (int e = 0; e < kStats; ++e) {
-        l_now[e] = l[e] - kLift;
-        d_now[e] = dd[e] * kUnlift;
+        l_now[e] = kLift - l[e];
+        d_now[e] = -dd[e] * kUnlift;
       }
       const int h_now = h, t_now = t;
       if (++t == x.t1) {
@@ -318,7 +318,7 @@ __device__ void bws_elementwise(BwsSmem<DP>& sm, const BwdParams& bp, uint32_t t
   const int row = 32 * (warp & 3) + lane;   // key of the tile, lane of tensor memory
   const uint32_t t_lane = (uint32_t)(32 * (warp & 3)) << 16;
   const uint32_t tDK = tmem + t_lane, tDV = tDK + DP, tS = tDK + 2 * DP, tDP = tS + kBQ, tP = tDP + kBQ + 64;
-  const float sl2 = p.scale_log2;
+  const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), unlift2 = make_float2(kUnlift, kUnlift);
   uint32_t items = 0, kv = 0, g = 0;
   for (;;) {
     const int slot = items & 1;
@@ -363,10 +363,12 @@ __device__ void bws_elementwise(BwsSmem<DP>& sm, const BwdParams& bp, uint32_t t
 #pragma unroll
       for (int c = 0; c < kCols; c += 4) {
         const float4 l = *reinterpret_cast<const float4*>(lse2 + c);
-        pv[c] = ex2_approx(fmaf(pv[c], sl2, -l.x));
-        pv[c + 1] = ex2_approx(fmaf(pv[c + 1], sl2, -l.y));
-        pv[c + 2] = ex2_approx(fmaf(pv[c + 2], sl2, -l.z));
-        pv[c + 3] = ex2_approx(fmaf(pv[c + 3], sl2, -l.w));
+        const float2 a = __ffma2_rn(make_float2(pv[c], pv[c + 1]), scale2, make_float2(l.x, l.y));
+        const float2 b = __ffma2_rn(make_float2(pv[c + 2], pv[c + 3]), scale2, make_float2(l.z, l.w));
+        pv[c] = ex2_approx(a.x);
+        pv[c + 1] = ex2_approx(a.y);
+        pv[c + 2] = ex2_approx(b.x);
+        pv[c + 3] = ex2_approx(b.y);
       }
       if (!__all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kCols - 1)) {
 #pragma unroll
@@ -377,44 +379,48 @@ __device__ void bws_elementwise(BwsSmem<DP>& sm, const BwdParams& bp, uint32_t t
             if (!(seen >> c & 1)) pv[32 * w + c] = 0.f;
         }
       }
-      // P^T, where the product that read the step before's is done
-      if (g > 0 && !BWS_WAIT_WARP(&sm.dv_done, (g - 1) & 1)) {
-        ok = false;
+      // Where a half is 64 queries, P^T goes out first: its values and dS^T's together are more than a thread's
+      // registers.  Else both wait until they are ready, and only then for the products of the step before.
+      constexpr bool kEarly = kCols > 32;
+      auto put_p = [&]() {
+        if (g > 0 && !BWS_WAIT_WARP(&sm.dv_done, (g - 1) & 1)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int c0 = 0; c0 < kCols; c0 += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = Tr::pack2(pv[c0 + 2 * e], pv[c0 + 2 * e + 1]);
+          tmem_st16(tP + (half * kCols + c0) / 2, pk);
+        }
+        return true;
+      };
+      ok = (!kEarly || put_p()) && BWS_WAIT_WARP(&sm.dp_full, g & 1);
+      if (kEarly && ok && g >= (uint32_t)kDS) ok = BWS_WAIT_WARP(&sm.ds_empty[buf], (g / kDS - 1) & 1);
+      if (!ok) {
+        tmem_st_wait();   // stores above complete before TMEM can be released
         break;
       }
       tc_fence_after();
 #pragma unroll
       for (int c0 = 0; c0 < kCols; c0 += 32) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) pk[e] = Tr::pack2(pv[c0 + 2 * e], pv[c0 + 2 * e + 1]);
-        tmem_st16(tP + (half * kCols + c0) / 2, pk);
-      }
-      if (!BWS_WAIT_WARP(&sm.dp_full, g & 1) ||
-          (g >= (uint32_t)kDS && !BWS_WAIT_WARP(&sm.ds_empty[buf], (g / kDS - 1) & 1))) {
-        tmem_st_wait();   // the stores above complete before TMEM can be released
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-#pragma unroll
-      for (int c0 = 0; c0 < kCols; c0 += 32) {
-        uint32_t dr[32];
+        uint32_t dr[32], pd[16];
         tmem_ld32(tDP + half * kCols + c0, dr);
         tmem_ld_wait_regs32(dr);
-        uint32_t pd[16];
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const float4 d = *reinterpret_cast<const float4*>(dd + c0 + 2 * e);
-          float v[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float du = u == 0 ? d.x : (u == 1 ? d.y : (u == 2 ? d.z : d.w));
-            const float w = __uint_as_float(dr[2 * e + u]);
-            v[u] = pv[c0 + 2 * e + u] * (Tr::kBF16 ? w - du : fmaf(w, kUnlift, -du));
-          }
-          pd[e] = Tr::pack2(v[0], v[1]);
-          pd[e + 1] = Tr::pack2(v[2], v[3]);
+        for (int e = 0; e < 32; e += 4) {
+          const float4 d = *reinterpret_cast<const float4*>(dd + c0 + e);
+          const float2 p0 = make_float2(pv[c0 + e], pv[c0 + e + 1]), p1 = make_float2(pv[c0 + e + 2], pv[c0 + e + 3]);
+          const float2 w0 = make_float2(__uint_as_float(dr[e]), __uint_as_float(dr[e + 1]));
+          const float2 w1 = make_float2(__uint_as_float(dr[e + 2]), __uint_as_float(dr[e + 3]));
+          const float2 d0 = make_float2(d.x, d.y), d1 = make_float2(d.z, d.w);
+          const float2 v0 = __fmul2_rn(p0, Tr::kBF16 ? __fadd2_rn(w0, d0) : __ffma2_rn(w0, unlift2, d0));
+          const float2 v1 = __fmul2_rn(p1, Tr::kBF16 ? __fadd2_rn(w1, d1) : __ffma2_rn(w1, unlift2, d1));
+          pd[e / 2] = Tr::pack2(v0.x, v0.y);
+          pd[e / 2 + 1] = Tr::pack2(v1.x, v1.y);
+        }
+        if (!kEarly) {
+          ok = put_p() && (g < (uint32_t)kDS || BWS_WAIT_WARP(&sm.ds_empty[buf], (g / kDS - 1) & 1));
+          if (!ok) break;
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -422,6 +428,10 @@ __device__ void bws_elementwise(BwsSmem<DP>& sm, const BwdParams& bp, uint32_t t
           *reinterpret_cast<uint4*>(sm.ds[buf] + sw128_offset(row, chunk)) =
               make_uint4(pd[4 * e], pd[4 * e + 1], pd[4 * e + 2], pd[4 * e + 3]);
         }
+      }
+      if (!ok) {
+        tmem_st_wait();
+        break;
       }
       tmem_st_wait();
       fence_proxy_async_smem();
