@@ -126,17 +126,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_paged_kernel(const PagedA
     };
     auto issue = [&](int i, int stage, long long off) {
       if (i < x.steps) {
-        const int first = unit_of<kWin>(x, x.blk0 + i) * kUnit + warp * kWarpKeys;
         const uint32_t dst = ring + stage * (2 * kTileBytes);
 #pragma unroll
         for (int c = 0; c < kCopies; ++c) {
           const int key = c * kLaneKeys + copy_key;
-          const bool take = copy_in && !key_hidden<kWin>(x, first + key);
           const uint32_t at = key * (DP * 2) + ((copy_chunk ^ (key & 7)) << 4);
           const long long ko = __shfl_sync(0xffffffffu, off, key), vo = __shfl_sync(0xffffffffu, off, 16 + key);
-          const int col = take ? copy_chunk * 8 : 0;
-          cp_async16(dst + at, static_cast<const DT*>(p.kc) + ko + col, take);
-          cp_async16(dst + kTileBytes + at, static_cast<const DT*>(p.vc) + vo + col, take);
+          const bool take = copy_in && ko >= 0;
+          const int col = copy_chunk * 8;
+          cp_async16(dst + at, static_cast<const DT*>(p.kc) + (take ? ko + col : 0), take);
+          cp_async16(dst + kTileBytes + at, static_cast<const DT*>(p.vc) + (take ? vo + col : 0), take);
         }
       }
       cp_async_commit();
@@ -669,6 +668,10 @@ int thd_attn_paged_window(const void* q, const void* k_cache, const void* v_cach
   p.num_pages = num_pages;
   p.page_size = page_size;
   p.max_pages = max_pages;
+  p.page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (page_size == 1 << s) p.page_shift = s;
+  p.same_places = p.k_page == p.v_page && p.k_token == p.v_token && p.k_head == p.v_head;
   p.tree_words = tree_mask ? tree_words : 0;
   p.B = batch_size;
   p.T = total_tokens;

@@ -72,6 +72,8 @@ struct PagedArgs {
   long long w_page, w_token, w_head;                                          // elements
   long long table_stride, k_page, k_token, k_head, v_page, v_token, v_head;   // elements
   int num_pages, page_size, max_pages;
+  int page_shift;      // page_size = 2^page_shift, or -1
+  int same_places;     // values lie in their cache as keys in theirs
   int tree_words;
   int win_left, sinks; // kWin: keys before its own slot that a token sees, and first keys that it sees besides
   int B, T, Hq, Hkv, group, d;
@@ -195,6 +197,7 @@ struct Piece {
   int row0, rows;       // the tile's rows of the sequence
   int past;             // keys before the new tokens (negative: fewer keys than tokens)
   int key_end;          // keys from here on no row of the tile sees
+  int full_end;         // keys before here every row sees, but for the window
   int blk0, steps;      // units that some row sees (steps may be 0)
   // kWin: unit i is unit_of(i); the first row's window begins at win_lo and the last one's at win_hi; every row
   // sees the keys before `few` that it could see without a window
@@ -210,6 +213,7 @@ template <bool kWin>
 __device__ __forceinline__ int piece_bounds(const PagedArgs& p, Piece& x) {
   x.past = x.s.kv_len - x.s.q_len;
   x.key_end = p.tree ? x.s.kv_len : min(x.s.kv_len, max(0, x.past + (x.row0 + x.rows - 1) / p.group + 1));
+  x.full_end = min(x.s.kv_len, p.tree ? x.past : x.past + x.row0 / p.group + 1);
   int last = (x.key_end + kUnit - 1) / kUnit;
   if constexpr (kWin) {
     const int tok0 = x.row0 / p.group, tok1 = (x.row0 + x.rows - 1) / p.group;
@@ -320,7 +324,7 @@ __device__ __forceinline__ bool key_hidden(const Piece& x, int key) {
 // Some key of the unit that begins with key `first` may be hidden from some row.
 template <bool kWin>
 __device__ __forceinline__ bool unit_cut(const PagedArgs& p, const Piece& x, int first) {
-  return first + kUnit > min(p.tree ? x.past : x.past + 1, x.s.kv_len) ||
+  return first + kUnit > x.full_end ||
          (kWin && first < x.win_hi && first + kUnit > x.few);
 }
 
@@ -380,12 +384,12 @@ __device__ __forceinline__ void note_split(const PagedArgs& p, const Piece& x, c
 // Place of the piece's partial result.
 __device__ __forceinline__ int part_of_piece(const Piece& x) { return blockIdx.x * 2 + (x.first ? 0 : 1); }
 
-// Element offset of a piece's key or value in its cache: 0 for one that is not read.
+// Element offset of a piece's key or value in its cache: -1 for one that is not read.
 template <bool kWin>
 __device__ __forceinline__ long long cache_offset(const PagedArgs& p, const Piece& x, const int32_t* table, int key,
                                                   bool values) {
-  if (key_hidden<kWin>(x, key)) return 0;
-  const int at = key / p.page_size;
+  if (key_hidden<kWin>(x, key)) return -1;
+  const int at = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
   int page = table[at];
   page = page < 0 ? 0 : (page >= p.num_pages ? p.num_pages - 1 : page);
   const int in = key - at * p.page_size;

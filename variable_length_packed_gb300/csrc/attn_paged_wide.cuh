@@ -27,6 +27,8 @@
 // Every wait is bounded as in the other attention kernels: one that runs out sets the CTA's
 // status word, and the CTA lets what it started finish and leaves.
 #pragma once
+#include <type_traits>
+
 #include "attn_paged_common.cuh"
 
 namespace thd {
@@ -119,23 +121,27 @@ __global__ void __launch_bounds__(kWideThreads, 2) attn_paged_wide_kernel(const 
         const int first = unit_of<kWin>(x, x.blk0 + i) * kUnit + (warp - 4) * kWarpKeys;
         // each lane the place of one key and of its value
         const long long koff = cache_offset<kWin>(p, x, table, first + lane, false);
-        const long long voff = cache_offset<kWin>(p, x, table, first + lane, true);
+        const long long voff = p.same_places ? koff : cache_offset<kWin>(p, x, table, first + lane, true);
         const uint32_t st = n % kWideStages;
         if (n >= kWideStages && !WIDE_WAIT(&sm.empty[st], (n / kWideStages - 1) & 1)) {
           ok = false;
           break;
         }
         const uint32_t kt = smem_u32(sm.k[st]), vt = smem_u32(sm.v[st]);
+        auto copy = [&](auto same) {
 #pragma unroll
-        for (int c = 0; c < kCopies; ++c) {
-          const int key = c * kLaneKeys + copy_key, row = (warp - 4) * kWarpKeys + key;
-          const bool take = copy_in && !key_hidden<kWin>(x, first + key);
-          const uint32_t at = (copy_chunk >> 3) * kPanelBytes + row * 128 + (((copy_chunk & 7) ^ (row & 7)) << 4);
-          const long long ko = __shfl_sync(0xffffffffu, koff, key), vo = __shfl_sync(0xffffffffu, voff, key);
-          const int col = take ? copy_chunk * 8 : 0;
-          cp_async16(kt + at, static_cast<const DT*>(p.kc) + ko + col, take);
-          cp_async16(vt + at, static_cast<const DT*>(p.vc) + vo + col, take);
-        }
+          for (int c = 0; c < kCopies; ++c) {
+            const int key = c * kLaneKeys + copy_key, row = (warp - 4) * kWarpKeys + key;
+            const uint32_t at = (copy_chunk >> 3) * kPanelBytes + row * 128 + (((copy_chunk & 7) ^ (row & 7)) << 4);
+            const long long ko = __shfl_sync(0xffffffffu, koff, key);
+            const long long vo = decltype(same)::value ? ko : __shfl_sync(0xffffffffu, voff, key);
+            const bool take = copy_in && ko >= 0;
+            const int col = copy_chunk * 8;
+            cp_async16(kt + at, static_cast<const DT*>(p.kc) + (take ? ko + col : 0), take);
+            cp_async16(vt + at, static_cast<const DT*>(p.vc) + (take ? vo + col : 0), take);
+          }
+        };
+        if (p.same_places) copy(std::true_type{}); else copy(std::false_type{});
         cp_async_commit();
         if (n > 0) {
           cp_async_wait<1>();
