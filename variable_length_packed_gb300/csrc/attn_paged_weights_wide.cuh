@@ -24,6 +24,8 @@ namespace {
 constexpr int kWwThreads = 384;
 constexpr int kWwKeys = 256;     // keys of an item
 constexpr int kWwRows = 128;     // rows of a query tile at most: whole tokens
+constexpr int kWwStats = 4;      // query tiles whose log-sum-exps are in shared memory: more than tiles, so that a tile's
+                                 // place is free as soon as its products are done
 template <int DP> struct WwDepth { static constexpr int kK = DP == 64 ? 3 : 2, kQ = DP == 64 ? 4 : 2; };
 
 template <int DP>
@@ -32,8 +34,8 @@ struct WwSmem {
   static constexpr int kK = WwDepth<DP>::kK, kQ = WwDepth<DP>::kQ;
   alignas(1024) uint8_t k[kK][2][kTileBytes];
   alignas(1024) uint8_t q[kQ][kTileBytes];
-  alignas(16) float lse[kQ][kWwRows];   // -log2(e) * log-sum-exp of the tile's rows
-  uint64_t k_full[kK], k_empty[kK], q_full[kQ], q_empty[kQ], s_full[2][2], s_empty[2][2], drain, never;
+  alignas(16) float lse[kWwStats][kWwRows];   // -log2(e) * log-sum-exp of the tile's rows
+  uint64_t k_full[kK], k_empty[kK], q_full[kQ], q_empty[kQ], l_full[kWwStats], l_empty[kWwStats], s_full[2][2], s_empty[2][2], drain, never;
   uint32_t tmem_base, abort;
   Share share;
 };
@@ -114,7 +116,11 @@ __global__ void __launch_bounds__(kWwThreads, 1)
     }
     for (int i = 0; i < kQ; ++i) {
       mbar_init(&sm.q_full[i], 1);
-      mbar_init(&sm.q_empty[i], 9);   // the products, and the eight warps that read the log-sum-exps
+      mbar_init(&sm.q_empty[i], 1);   // the products
+    }
+    for (int i = 0; i < kWwStats; ++i) {
+      mbar_init(&sm.l_full[i], 1);
+      mbar_init(&sm.l_empty[i], 8);   // the warps that read them
     }
     for (int i = 0; i < 2; ++i)
       for (int j = 0; j < 2; ++j) {
@@ -208,33 +214,51 @@ __global__ void __launch_bounds__(kWwThreads, 1)
     uint32_t n = 0;   // query tiles issued
     bool ok = true;
     const uint32_t bytes = (uint32_t)(kPanels * 128 * tokens * p.group);
-    while (ok && walk.next(p, x)) {
-      for (int t = x.tile0; t < x.tile1; ++t, ++n) {
-        const uint32_t st = n % kQ;
-        const int tok0 = t * tokens;
-        float l[kWwRows / 32];
+    // the token and the head of this lane's columns
+    int tok_of[kWwRows / 32], head_of[kWwRows / 32];
 #pragma unroll
-        for (int i = 0; i < kWwRows / 32; ++i) {
-          const int c = i * 32 + lane, tok = tok0 + c / p.group;
-          l[i] = c < tokens * p.group && tok < x.s.q_len
-                     ? -1.4426950408889634f *
-                           p.lse[(long long)(x.head * p.group + c % p.group) * p.T + x.s.q_start + tok]
-                     : 0.f;
-        }
+    for (int i = 0; i < kWwRows / 32; ++i) {
+      tok_of[i] = (i * 32 + lane) / p.group;
+      head_of[i] = i * 32 + lane - tok_of[i] * p.group;
+    }
+    float l[kWwRows / 32];
+    auto stats = [&](int t) {   // read a tile ahead
+#pragma unroll
+      for (int i = 0; i < kWwRows / 32; ++i) {
+        const int tok = t * tokens + tok_of[i];
+        l[i] = tok_of[i] < tokens && tok < x.s.q_len
+                   ? -1.4426950408889634f * p.lse[(long long)(x.head * p.group + head_of[i]) * p.T + x.s.q_start + tok]
+                   : 0.f;
+      }
+    };
+    while (ok && walk.next(p, x)) {
+      if (x.tile1 > x.tile0) stats(x.tile0);
+      for (int t = x.tile0; t < x.tile1; ++t, ++n) {
+        const uint32_t st = n % kQ, ls = n % kWwStats;
+        float now[kWwRows / 32];
+#pragma unroll
+        for (int i = 0; i < kWwRows / 32; ++i) now[i] = l[i];
+        if (t + 1 < x.tile1) stats(t + 1);
         if (n >= (uint32_t)kQ && !WW_WAIT(&sm.q_empty[st], (n / kQ - 1) & 1)) {
           ok = false;
           break;
         }
-#pragma unroll
-        for (int i = 0; i < kWwRows / 32; ++i)   // a row that sees no key: its scores are all masked, by -inf
-          sm.lse[st][i * 32 + lane] = l[i] == INFINITY ? 0.f : l[i];
-        __syncwarp();
         if (lane == 0) {
           mbar_arrive_expect_tx(&sm.q_full[st], bytes);
 #pragma unroll
           for (int pn = 0; pn < kPanels; ++pn)
-            tma_load_3d(sm.q[st] + pn * 16384, &tm_q, &sm.q_full[st], pn * 64, x.head * p.group, x.s.q_start + tok0);
+            tma_load_3d(sm.q[st] + pn * 16384, &tm_q, &sm.q_full[st], pn * 64, x.head * p.group, x.s.q_start + t * tokens);
         }
+        if (n >= (uint32_t)kWwStats && !WW_WAIT(&sm.l_empty[ls], (n / kWwStats - 1) & 1)) {
+          ok = false;
+          ++n;   // its copy is on the way
+          break;
+        }
+#pragma unroll
+        for (int i = 0; i < kWwRows / 32; ++i)   // a row that sees no key: its scores are all masked, by -inf
+          sm.lse[ls][i * 32 + lane] = now[i] == INFINITY ? 0.f : now[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.l_full[ls]);
       }
     }
     // copies in flight land before the CTA can exit
@@ -303,8 +327,8 @@ __global__ void __launch_bounds__(kWwThreads, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
       for (int t = x.tile0; t < x.tile1; ++t, ++nq) {
-        const uint32_t qs = nq % kQ;
-        if (!WW_WAIT(&sm.q_full[qs], (nq / kQ) & 1)) {   // the log-sum-exps are there
+        const uint32_t ls = nq % kWwStats;
+        if (!WW_WAIT(&sm.l_full[ls], (nq / kWwStats) & 1)) {
           ok = false;
           break;
         }
@@ -328,7 +352,7 @@ __global__ void __launch_bounds__(kWwThreads, 1)
           const bool by_bits = p.tree && real && key >= x.past;
           const bool whole = __all_sync(0xffffffffu, lo == 0 && end == kWwRows && !by_bits);
 #pragma unroll
-          for (int c0 = 0; c0 < kWwRows; c0 += 64) {
+          for (int c0 = 0; c0 < kWwRows; c0 += 64) {   // all 128 at once: 80 bytes of spills, 9 % slower
             uint32_t s[64];
             tmem_ld32(tS + buf * 128 + c0, s);
             tmem_ld32(tS + buf * 128 + c0 + 32, s + 32);
@@ -358,7 +382,7 @@ __global__ void __launch_bounds__(kWwThreads, 1)
                   if (!(seen >> c & 1)) s[32 * w + c] = __float_as_uint(-INFINITY);
               }
             }
-            const float4* lse = reinterpret_cast<const float4*>(&sm.lse[qs][c0]);
+            const float4* lse = reinterpret_cast<const float4*>(&sm.lse[ls][c0]);
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
               const float4 l = lse[c];
@@ -372,7 +396,7 @@ __global__ void __launch_bounds__(kWwThreads, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_empty[qs]);
+        if (lane == 0) mbar_arrive(&sm.l_empty[ls]);
       }
       if (!ok) break;
       // keys that no token sees are left alone: their pages may be another sequence's by now
