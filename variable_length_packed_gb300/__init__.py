@@ -9,6 +9,7 @@ missing library or a non-CUDA tensor raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -119,6 +120,11 @@ def thd_attn_workspace_size():
     return int(_lib().thd_attn_workspace_size())
 
 
+@functools.lru_cache(maxsize=None)
+def _workspace_bytes():
+    return thd_attn_workspace_size()
+
+
 def thd_set_wait_limit_ns(ns):
     """Time limit of one pipeline wait inside the kernels for later calls (0: the default,
     2 s); returns the previous limit.  A short limit makes waits run out on purpose: the
@@ -142,7 +148,7 @@ def _ptr(t):
 
 
 def _cuda(t, name):
-    if t is None:
+    if t is None or (type(t) is torch.Tensor and t.is_cuda and t.is_contiguous()):
         return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor (no CPU path exists)")
@@ -202,6 +208,24 @@ def _stream_handle(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+# the current stream's handle without the Stream object around it (2 us a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, device, *args):
+    """The library's entry point on the current stream of `device`; its status."""
+    fn = getattr(_lib(), name)
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, _raw_stream(device.index))
+    with torch.cuda.device(device):
+        return fn(*args, _raw_stream(device.index))
+
+
 def _window_args(window):
     left, right = (int(window[0]), int(window[1]))
     if left < -1 or right < -1:
@@ -253,16 +277,14 @@ def thd_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=None,
     if lse is None and return_lse:
         lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = torch.empty(thd_attn_workspace_size(), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(_workspace_bytes(), dtype=torch.uint8, device=q.device)
     left, right = _window_args(window)
     sinks = _sink_count(sink_tokens)
-    with torch.cuda.device(q.device):
-        st = _lib().thd_attn_fwd_sinks(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q), _ptr(cu_seqlens_kv),
-            _ptr(cu_seqlens_q_padded), _ptr(cu_seqlens_kv_padded), _ptr(seq_is_causal),
-            int(batch_size), int(max_seqlen), float(softmax_scale), _ptr(out), _ptr(lse),
-            int(T), int(Hq), int(Hkv), int(d), THD_BF16 if q.dtype == torch.bfloat16 else THD_FP16,
-            left, right, sinks, _ptr(workspace), workspace.numel(), _stream_handle(q.device))
+    st = _call("thd_attn_fwd_sinks", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(cu_seqlens_q),
+               _addr(cu_seqlens_kv), _addr(cu_seqlens_q_padded), _addr(cu_seqlens_kv_padded), _addr(seq_is_causal),
+               int(batch_size), int(max_seqlen), float(softmax_scale), out.data_ptr(), _addr(lse), T, Hq, Hkv, d,
+               THD_BF16 if q.dtype == torch.bfloat16 else THD_FP16, left, right, sinks, workspace.data_ptr(),
+               workspace.numel())
     if st != THD_OK:
         raise ThdError(st, "thd_attn_fwd")
     return out, lse
@@ -422,13 +444,12 @@ def thd_attn_bwd(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlen
     need = int(_lib().thd_attn_bwd_sinks_workspace_size(int(T), int(Hq), int(Hkv), int(d), int(batch_size), left, sinks))
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    with torch.cuda.device(q.device):
-        st = _lib().thd_attn_bwd_sinks(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(cu_seqlens_q), _ptr(cu_seqlens_kv),
-            _ptr(cu_seqlens_q_padded), _ptr(cu_seqlens_kv_padded), _ptr(seq_is_causal), int(batch_size),
-            int(max_seqlen), float(softmax_scale), _ptr(dq), _ptr(dk), _ptr(dv), int(T), int(Hq), int(Hkv), int(d),
-            THD_BF16 if q.dtype == torch.bfloat16 else THD_FP16, left, right, sinks, _ptr(workspace), workspace.numel(),
-            _stream_handle(q.device))
+    st = _call("thd_attn_bwd_sinks", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+               dout.data_ptr(), _addr(cu_seqlens_q), _addr(cu_seqlens_kv), _addr(cu_seqlens_q_padded),
+               _addr(cu_seqlens_kv_padded), _addr(seq_is_causal), int(batch_size), int(max_seqlen), float(softmax_scale),
+               dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), T, Hq, Hkv, d,
+               THD_BF16 if q.dtype == torch.bfloat16 else THD_FP16, left, right, sinks, workspace.data_ptr(),
+               workspace.numel())
     if st != THD_OK:
         raise ThdError(st, "thd_attn_bwd")
     return dq, dk, dv

@@ -15,6 +15,7 @@
 #include "attn_fwd_ws.cuh"
 #include "attn_bwd.cuh"
 #include "attn_bwd_ws.cuh"
+#include "seq_rows.cuh"
 
 namespace thd {
 cudaError_t launch_padding_mask(const int32_t* cu, int B, int S, uint8_t* mask, int num_sms, cudaStream_t stream);
@@ -79,12 +80,10 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+// SM count of the current device, -1 on an error.
 int num_sms_of_current_device() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
-  return n;
+  const int n = thd::device_sms();
+  return n > 0 ? n : -1;
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -160,8 +159,8 @@ int launch_serial(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMa
                   int grid, cudaStream_t stream) {
   auto kern = thd::attn_fwd_serial_kernel<DT, DP, kTMA>;
   const size_t smem = sizeof(thd::SerialSmem<DP>) + 1024;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return THD_ERR_CUDA;
+  static thd::SmemGrant grant;
+  if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
   kern<<<grid, 128, smem, stream>>>(mq, mk, mv, p);
   return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
 }
@@ -189,8 +188,8 @@ int launch_ws(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& m
                                  : thd::attn_fwd_ws_kernel<DT, DP, 1, false>)
                   : (pack ? thd::attn_fwd_ws_kernel<DT, DP, 0, true> : thd::attn_fwd_ws_kernel<DT, DP, 0, false>);
   const size_t smem = one_cta_per_sm(sizeof(thd::WsSmem<DP>) + 1024);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return THD_ERR_CUDA;
+  static thd::SmemGrant grants[4];
+  if (!grants[win ? (p.sinks > 0 ? 3 : 2) : (pack ? 1 : 0)].ask(kern, smem)) return THD_ERR_CUDA;
   kern<<<grid, thd::kWsThreads, smem, stream>>>(mq, mk, mv, p);
   return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
 }
@@ -227,14 +226,14 @@ int launch_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& 
   if (bp.a.sinks > 0) {
     auto kern = thd::attn_bwd_ws_kernel<DT, DP>;
     const size_t smem = one_cta_per_sm(sizeof(thd::BwsSmem<DP>) + 1024);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-      return THD_ERR_CUDA;
+    static thd::SmemGrant grant;
+    if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
     kern<<<sms, thd::kBwsThreads, smem, stream>>>(mq, mk, mv, mdo, mdq, bp);
   } else {
     auto kern = thd::attn_bwd_kernel<DT, DP>;
     const size_t smem = one_cta_per_sm(sizeof(thd::BwdSmem<DP>) + 1024);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-      return THD_ERR_CUDA;
+    static thd::SmemGrant grant;
+    if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
     kern<<<sms, thd::kBwdThreads, smem, stream>>>(mq, mk, mv, mdo, mdq, bp);
   }
   if (cudaGetLastError() != cudaSuccess) return THD_ERR_CUDA;

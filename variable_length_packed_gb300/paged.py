@@ -12,11 +12,9 @@ import math
 
 import torch
 
-from . import THD_BF16, THD_FP16, THD_OK, ThdError, _check_metadata, _sink_count, _window_args, load_library
+from . import THD_BF16, THD_FP16, THD_OK, ThdError, _addr, _check_metadata, _sink_count, _window_args, load_library
+from . import _call as _status_of
 
-# the current stream's handle without the Stream object around it (2 us a call)
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
 _F32 = torch.float32
 _SCORES_MAX = 1 << 30   # bytes that thd_attn_paged allocates at most for scores beside its workspace
 _Places = ctypes.c_int64 * 6
@@ -50,10 +48,6 @@ def thd_attn_paged_weights_workspace_size(head_dim, num_heads_q, batch_size, max
     if max(map(abs, sizes)) > _COUNT_MAX or left > _COUNT_MAX:
         return 0
     return int(load_library().thd_attn_paged_weights_workspace_size(*sizes, left, sinks))
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 def _too_large(name):
@@ -180,12 +174,7 @@ def _weights(wq, wk, device, d, dtype):
 
 def _call(name, device, *args):
     """The library's entry point on the current stream of `device`."""
-    fn = getattr(load_library(), name)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, _raw_stream(device.index))
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, _raw_stream(device.index))
+    st = _status_of(name, device, *args)
     if st != THD_OK:
         raise ThdError(st, name)
 
