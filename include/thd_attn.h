@@ -156,6 +156,8 @@ int thd_attn_fwd_window(const void* q, const void* k, const void* v,
  *     i + shift - window_left <= j <= i + shift + window_right  or  j < sink_tokens.
  * sink_tokens  >= 0; 0 is exactly thd_attn_fwd_window.  Without a window
  *              ((-1, -1)) nothing is hidden and it has no effect.
+ * As everywhere in thd_attn_fwd, rows of no sequence that lie up to 128 rows behind one
+ * must hold finite values in q, k and v (a weight of 0 times them is added).
  * Every other argument, the results and the errors are those of
  * thd_attn_fwd_window (THD_ERR_ARG also for sink_tokens < 0).
  */
@@ -244,7 +246,8 @@ size_t thd_attn_bwd_sinks_workspace_size(int total_tokens, int num_heads_q, int 
  * thd_attn_bwd_window).  dK and dV are summed in a fixed order, so the same call
  * gives the same bits of them.  Other arguments and errors as there, THD_ERR_ARG
  * for sink_tokens < 0, and workspace of at least
- * thd_attn_bwd_sinks_workspace_size's bytes.
+ * thd_attn_bwd_sinks_workspace_size's bytes.  Rows of no sequence of dout must be
+ * finite like those of q, k and v.
  */
 int thd_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* out, const float* lse,
                        const void* dout,
@@ -621,7 +624,7 @@ uint64_t thd_set_wait_limit_ns(uint64_t ns);
 /*
  * thd_set_wait_injection — test setting of the failure path: with enable != 0,
  * every CTA of the attention kernels (forward, windowed forward, no-allocation
- * forward, backward, thd_attn_paged with tiles of 128 rows) called after it
+ * forward, backward, thd_attn_paged with tiles of 128 rows and its key weights) called after it
  * makes one wait on a barrier that nothing completes before the CTA's end.  That wait runs out after the limit of
  * thd_set_wait_limit_ns whatever the timing of the rest of the pipeline, so the
  * call sets THD_STATUS_WAIT_TIMEOUT and its CTAs leave through the failure path
