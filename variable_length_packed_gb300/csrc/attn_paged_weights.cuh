@@ -27,57 +27,88 @@ __device__ __forceinline__ bool token_sees(const PagedArgs& p, const SeqWork& s,
   return key <= own && (!kWin || key >= own - p.win_left || key < p.sinks);
 }
 
-// From kept scores: a warp takes a unit of a head, its lanes two keys each.
+// Units of a sequence's heads that have kept scores.
+__device__ __forceinline__ long long score_units(const PagedArgs& p, const SeqWork& s) {
+  return s.q_len > 0 ? (long long)p.Hkv * s.blocks : 0ll;
+}
+
+// From kept scores: a CTA takes a run of the units of all heads laid end to end, a warp every fourth of them, its
+// lanes two keys each.
 template <bool kWin>
-__device__ void weights_of_scores(const PagedArgs& p) {
+__device__ void weights_of_scores(const PagedArgs& p, const Share& share, long long scores) {
   const int lane = threadIdx.x & 31;
-  const long long warps = (long long)gridDim.x * kWeightWarps;
-  long long step = (long long)blockIdx.x * kWeightWarps + (threadIdx.x >> 5), base = 0, scores = 0;
-  for (int b = 0; b < p.B; ++b) {
+  long long step = share.begin + (threadIdx.x >> 5), base = share.seq_base;
+  for (int b = share.seq; step < share.end; ++b) {
     Piece x;
     x.s = seq_work<kWin>(p, b, kNarrowRows);
-    const long long n = x.s.q_len > 0 ? (long long)p.Hkv * x.s.blocks : 0ll;
-    if (step < base + n) {
+    const long long end = min(base + score_units(p, x.s), share.end);
+    if (step < end) {
       x.row0 = 0;
       x.rows = x.s.q_len * p.group;
       const int last = piece_bounds<kWin>(p, x);
       const int32_t* table = p.table + (long long)b * p.table_stride;
-      for (; step < base + n; step += warps) {
-        const int in = (int)(step - base), head = in / x.s.blocks, blk = in - head * x.s.blocks;
-        if (blk >= last) continue;
-        const int key = unit_of<kWin>(x, blk) * kUnit + lane * 2;
-        float* place[2];
+      constexpr int kAhead = 4;   // units at once: a page, then a weight, then a sum each wait for the one before
+      for (; step < end; step += kAhead * kWeightWarps) {
+        float* place[kAhead][2];
+        float had[kAhead][2];
+        float2 sum[kAhead];
+        const float2* src[kAhead];
+        const float* lse[kAhead];
+        int units = 0;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          place[e] = nullptr;
-          const int k = key + e;
-          // a key that no token sees is left alone: its page may be another sequence's by now
-          if (k < x.s.kv_len && (!kWin || k < p.sinks || k >= x.win_lo)) {
-            const int at = k / p.page_size, page = table[at];
-            if (page >= 0 && page < p.num_pages)
-              place[e] = p.key_weights + page * p.w_page + (k - at * p.page_size) * p.w_token + head * p.w_head;
+        for (int k = 0; k < kAhead; ++k) {
+          place[k][0] = place[k][1] = nullptr;
+          sum[k] = make_float2(0.f, 0.f);
+          // a unit behind the last reads the first one's scores, and writes nothing
+          const bool real = step + k * kWeightWarps < end;
+          const int in = (int)((real ? step + k * kWeightWarps : step) - base), head = in / x.s.blocks, blk = in - head * x.s.blocks;
+          src[k] = reinterpret_cast<const float2*>(p.scores + scores + (long long)in * x.rows * kUnit) + lane;
+          lse[k] = p.lse + (long long)head * p.group * p.T + x.s.q_start;
+          if (real && blk < last) {
+            units = k + 1;
+            const int key = unit_of<kWin>(x, blk) * kUnit + lane * 2;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int at_key = key + e;
+              // a key that no token sees is left alone: its page may be another sequence's by now
+              if (at_key < x.s.kv_len && (!kWin || at_key < p.sinks || at_key >= x.win_lo)) {
+                const int at = p.page_shift >= 0 ? at_key >> p.page_shift : at_key / p.page_size, page = table[at];
+                if (page >= 0 && page < p.num_pages)
+                  place[k][e] = p.key_weights + page * p.w_page + (at_key - at * p.page_size) * p.w_token + head * p.w_head;
+              }
+            }
           }
-        }
-        const float2* src = reinterpret_cast<const float2*>(p.scores + scores + (long long)in * x.rows * kUnit) + lane;
-        float2 sum = make_float2(0.f, 0.f);
-        float had[2] = {0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (place[e] && key + e < x.past) had[e] = *place[e];   // a new token's key had none
-#pragma unroll 4
-        for (int r = 0; r < x.rows; ++r) {
-          const int tok = r / p.group;
-          const float2 s = src[r * (kUnit / 2)];
-          const float l = p.lse[(long long)(head * p.group + r - tok * p.group) * p.T + x.s.q_start + tok];
-          const float l2 = l == -INFINITY ? 0.f : -1.4426950408889634f * l;   // such a row's scores are -inf
-          sum.x += ex2_approx(s.x + l2);
-          sum.y += ex2_approx(s.y + l2);
+          for (int e = 0; e < 2; ++e)   // a new token's key had none
+            had[k][e] = place[k][e] && unit_of<kWin>(x, blk) * kUnit + lane * 2 + e < x.past ? *place[k][e] : 0.f;
         }
-        if (place[0]) *place[0] = had[0] + sum.x;
-        if (place[1]) *place[1] = had[1] + sum.y;
+        if (units == 0) continue;
+        for (int tok = 0, r = 0; tok < x.s.q_len; ++tok)
+          for (int g = 0; g < p.group; ++g, ++r) {
+            float2 s[kAhead];
+            float l[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+              s[k] = src[k][r * (kUnit / 2)];
+              l[k] = lse[k][(long long)g * p.T + tok];
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+              const float l2 = l[k] == -INFINITY ? 0.f : -1.4426950408889634f * l[k];   // such a row's scores are -inf
+              sum[k].x += ex2_approx(s[k].x + l2);
+              sum[k].y += ex2_approx(s[k].y + l2);
+            }
+          }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          if (place[k][0]) *place[k][0] = had[k][0] + sum[k].x;
+          if (place[k][1]) *place[k][1] = had[k][1] + sum[k].y;
+        }
       }
+      // on with the first of this warp's units that was not taken
+      step -= (step - end) / kWeightWarps * kWeightWarps;
     }
-    base += n;
+    base += score_units(p, x.s);
     scores += seq_scores(p, x.s);
   }
 }
@@ -89,9 +120,13 @@ __global__ void __launch_bounds__(kWeightWarps * 32) attn_key_weights_kernel(con
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int qr = lane >> 2, qc = (lane & 3) * 2;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (score_places<kWeightWarps * 32, kWin>(p, 0).fit) {
-    weights_of_scores<kWin>(p);
-    return;
+  if (p.scores) {
+    find_share<kWeightWarps * 32>(p, [&](int b) { return score_units(p, seq_work<kWin>(p, b, kNarrowRows)); }, &share);
+    const ScorePlaces at = score_places<kWeightWarps * 32, kWin>(p, share.seq);
+    if (at.fit) {
+      weights_of_scores<kWin>(p, share, at.base);
+      return;
+    }
   }
   // a unit of 64 keys of a head costs reading its keys and a step for every 8 rows
   auto cost = [&](const SeqWork& s) { return 2ll + (long long)s.q_len * p.group / 8; };
