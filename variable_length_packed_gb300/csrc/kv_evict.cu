@@ -8,7 +8,10 @@
 // Two launches.  The first finds, for every (sequence, head), the weight of the last key to stay by
 // counting digits from the top (three passes over the weights, read once into shared memory where they fit
 // there), and writes the kept slots in order.  The second moves the keys, values and weights; it is bound by
-// reading and writing 4 d + 4 bytes for each kept key and head.
+// reading and writing 4 d + 4 bytes for each kept key and head.  Measured, 32 sequences of 500000 keys in all cut to
+// 4000 to 8000, 8 heads of 128: 365 to 380 us into other pages, of which 281 move 1.69 GB (6.0 TB/s) and 60 select; 420 to
+// 540 in place.  8 lists of 262144 keys cut to half: 364 us into other pages, 690 in place (a round's reads wait for the
+// round before).  1000 keys cut to 500: 15 us on the GPU.
 #include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>
