@@ -584,8 +584,9 @@ int thd_attn_paged_window(const void* q, const void* k_cache, const void* v_cach
  *              pages that the kept keys go to; K is at most new_max_pages * page_size.  They
  *              must be none of the pages that page_table names for any key of the
  *              batch; the old pages are left as they were, so several sequences may
- *              name them.  NULL, or page_table itself: the old pages, in place; no two
- *              sequences of the batch may share one then.
+ *              name them.  NULL, or page_table itself with its stride: the old pages, in
+ *              place (K is at most new_max_pages * page_size here too); no two sequences of
+ *              the batch may share one then.
  * kv_lens, keep_lens  device int32 [>= batch_size].
  * sink_tokens, recent_tokens  >= 0.
  * kept         device int32 [batch_size, Hkv, max_keep]: written with the old slots of the

@@ -57,3 +57,8 @@ def test_packed_sinks_refusals(lib, base, fn, over, status):  # noqa: F811
     (dict(B=0), 0), (dict(B=0, kc=None, w=None, kept=None, lens=None), 0)])
 def test_evict_refusals(lib, over, status):  # noqa: F811
     assert call(lib.thd_kv_evict, EVICT, EVICT, over) == status
+
+
+def test_evict_in_place_takes_the_rows_of_the_table_itself(lib):  # noqa: F811
+    """A new table at the old one's address with rows elsewhere is another table over the same pages."""
+    assert call(lib.thd_kv_evict, EVICT, EVICT, dict(B=2, new=16, nwide=4, nts=8, keep=160)) == -1

@@ -121,6 +121,17 @@ def test_own_table_given_as_the_new_one_is_in_place():
     assert np.array_equal(bits(x["kc"]), bits(y["kc"])) and torch.equal(x["w"], y["w"])
 
 
+def test_fewer_columns_of_the_own_table_bound_what_stays():
+    x, y = make([900, 700], [300, 290], 16, 2, 64), make([900, 700], [128, 128], 16, 2, 64)
+    table = ints(x["table"])
+    kept = torch.zeros((2, 2, 400), dtype=torch.int32, device="cuda")
+    lens = vlp.thd_kv_evict(x["kc"], x["vc"], x["w"], table, ints(x["keys"]), ints(x["keep"]), new_page_table=table[:, :8],
+                            sink_tokens=2, recent_tokens=10, kept=kept)
+    run(y, 2, 10)
+    assert lens.tolist() == [128, 128] and torch.all(kept[:, :, 128:] == -1)
+    assert np.array_equal(bits(x["kc"]), bits(y["kc"])) and torch.equal(x["w"], y["w"])
+
+
 def test_shared_pages_into_other_pages():
     """Two sequences that share their first pages each keep their own keys."""
     x = make([320, 320], [100, 90], 16, 2, 64, apart=True)

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kSelectThreads, 3) kv_evict_select_kernel(cons
     same = (int)left;
   }
   // whether a slot stays whatever its equals do, and whether it is one of those equal to the bound
-  auto judge = [&](int i, bool& more, bool& equal) {
+  auto rank_of = [&](int i, bool& more, bool& equal) {
     more = equal = false;
     if (i < to) {
       if (i < first || i >= end) {
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kSelectThreads, 3) kv_evict_select_kernel(cons
     __syncthreads();
     for (int i = from + tid; i < to; i += kSelectThreads) {
       bool more, equal;
-      judge(i, more, equal);
+      rank_of(i, more, equal);
       n.x += more ? 1 : 0;
       n.y += equal ? 1 : 0;
     }
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kSelectThreads, 3) kv_evict_select_kernel(cons
 #pragma unroll
     for (int w = 0; w < kWords; ++w) {
       bool more, equal;
-      judge(i0 + (warp * kWords + w) * 32 + lane, more, equal);
+      rank_of(i0 + (warp * kWords + w) * 32 + lane, more, equal);
       more_bits[w] = __ballot_sync(0xffffffffu, more);
       same_bits[w] = __ballot_sync(0xffffffffu, equal);
       m_sum += __popc(more_bits[w]);
@@ -415,9 +415,11 @@ extern "C" int thd_kv_evict(void* k_cache, void* v_cache, const int64_t* cache_s
     if (new_lens < lens + batch_size && lens < new_lens + batch_size) return THD_ERR_ARG;
   if (num_pages == 0) max_pages = 0;   // no sequence has keys
   if (max_pages > 0 && (!page_table || !k_cache || !v_cache || !key_weights)) return THD_ERR_ARG;
+  const bool within = !new_page_table || new_page_table == page_table;
+  // the same rows, of which a narrower table names the first pages
+  if (within && new_page_table && batch_size > 1 && new_page_table_stride != page_table_stride) return THD_ERR_ARG;
   const int sms = device_sms();
   if (sms <= 0) return THD_ERR_CUDA;
-  const bool within = !new_page_table || new_page_table == page_table;
   EvictArgs p{};
   p.kc = static_cast<uint16_t*>(k_cache);
   p.vc = static_cast<uint16_t*>(v_cache);
@@ -426,7 +428,7 @@ extern "C" int thd_kv_evict(void* k_cache, void* v_cache, const int64_t* cache_s
   p.table_stride = page_table_stride;
   p.to_table = within ? page_table : new_page_table;
   p.to_stride = within ? page_table_stride : new_page_table_stride;
-  p.to_pages = within ? max_pages : new_max_pages;
+  p.to_pages = new_page_table ? new_max_pages : max_pages;
   p.kv_lens = kv_lens;
   p.keep_lens = keep_lens;
   p.kept = kept;
