@@ -27,7 +27,8 @@
 // Under a window (kWin) the loading warps bounded it while they looked up keys and values apart: 512 tokens of 8
 // sequences over windows of 1023, 190 us, and 137 with one place for both.  Several tiles of many heads over a cache larger than
 // the L2 are under way at once and read it again from memory: 1024 tokens of 4 sequences over 60000 keys, 0.99 ms and
-// 5.6 GB read where the cache is 0.25.  Measured and left: a second score tile with the queries in shared memory and two
+// 5.6 GB read where the cache is 0.25.  Measured and left: two, three or four waves of shares, which keep a wave's keys in
+// the L2 (0.97 ms there, but 166, 189 and 211 us against 137 on the windows); a second score tile with the queries in shared memory and two
 // units on the way (194 us, and 1200 against 876 on 12500 keys of 8 sequences).
 //
 // Every wait is bounded as in the other attention kernels: one that runs out sets the CTA's
