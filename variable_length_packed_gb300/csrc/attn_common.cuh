@@ -75,7 +75,7 @@ struct SeqInfo {
   int lo_off, hi_off;
 };
 
-__device__ __forceinline__ void set_visibility(SeqInfo& s, int code, const AttnParams& p) {
+__host__ __device__ __forceinline__ void set_visibility(SeqInfo& s, int code, const AttnParams& p) {
   s.causal = code != kMaskPadding;
   s.shift = code == kMaskCausalBottomRight ? s.kv_len - s.q_len : 0;
   const int wr = p.win_right >= 0 ? p.win_right : kNoBound;
@@ -86,18 +86,18 @@ __device__ __forceinline__ void set_visibility(SeqInfo& s, int code, const AttnP
 // First / last key of the sequence visible to query position qpos (the first is past the
 // last when none is).  Both grow with qpos, so a block of rows sees keys between the first
 // row's first key and the last row's last key.
-__device__ __forceinline__ int seq_first_key(const SeqInfo& s, int qpos) {
+__host__ __device__ __forceinline__ int seq_first_key(const SeqInfo& s, int qpos) {
   const long long f = (long long)qpos + s.shift - s.lo_off;
   return f < 0 ? 0 : (f > s.kv_len ? s.kv_len : (int)f);
 }
-__device__ __forceinline__ int seq_last_key(const SeqInfo& s, int qpos) {
+__host__ __device__ __forceinline__ int seq_last_key(const SeqInfo& s, int qpos) {
   const long long l = (long long)qpos + s.shift + s.hi_off;
   return l > s.kv_len - 1 ? s.kv_len - 1 : (l < -1 ? -1 : (int)l);
 }
 
 // Keys [0, sink_end) of the sequence are seen by query position qpos wherever its window lies: the first
 // `sinks` ones that the mask type allows.  Grows with qpos, like the two above.
-__device__ __forceinline__ int sink_end(const SeqInfo& s, int qpos, int sinks) {
+__host__ __device__ __forceinline__ int sink_end(const SeqInfo& s, int qpos, int sinks) {
   const long long mask_end = s.causal ? (long long)qpos + s.shift + 1 : (long long)s.kv_len;
   const long long e = min((long long)min(sinks, s.kv_len), mask_end);
   return e < 0 ? 0 : (int)e;
@@ -143,12 +143,12 @@ __device__ __forceinline__ SeqInfo load_seq(const AttnParams& p, int b) {
 // [kv_first_tile, kv_tiles_for), up to the last key visible to the tile's last valid row
 // and from the first key visible to its first row.  kv_tiles_for is 0 when no row sees a
 // key; the range is empty when kv_first_tile >= kv_tiles_for.
-__device__ __forceinline__ int kv_tiles_for(const SeqInfo& s, int q0, int rows) {
+__host__ __device__ __forceinline__ int kv_tiles_for(const SeqInfo& s, int q0, int rows) {
   if (s.kv_len <= 0) return 0;
   const int last = seq_last_key(s, min(q0 + rows, s.q_len) - 1);
   return last < 0 ? 0 : last / kBlockN + 1;
 }
-__device__ __forceinline__ int kv_first_tile(const SeqInfo& s, int q0) { return seq_first_key(s, q0) / kBlockN; }
+__host__ __device__ __forceinline__ int kv_first_tile(const SeqInfo& s, int q0) { return seq_first_key(s, q0) / kBlockN; }
 
 // KV tiles that the 128-row Q tile at position q0 < q_len visits under a window: [0, ns) for the first keys
 // that stay visible, then [j0, n).  Where the two touch they are one range with ns = 0; n = 0 when no
@@ -156,7 +156,7 @@ __device__ __forceinline__ int kv_first_tile(const SeqInfo& s, int q0) { return 
 struct KvTiles {
   int ns, j0, n;
 };
-__device__ __forceinline__ KvTiles kv_tiles_windowed(const SeqInfo& s, int q0, int sinks) {
+__host__ __device__ __forceinline__ KvTiles kv_tiles_windowed(const SeqInfo& s, int q0, int sinks) {
   KvTiles r;
   r.ns = 0;
   r.n = kv_tiles_for(s, q0, kTileM);

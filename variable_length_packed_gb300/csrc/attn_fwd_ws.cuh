@@ -81,7 +81,7 @@ struct WsTile {
   int h;         // query head
   int q0;        // sequence position of the tile's first query row
   int j0, n;     // KV tiles the tile visits: [j0, n); n = 0 when no row sees a key
-  int ns;        // kWin: and [0, ns) before them, ns < j0 (0 where the two ranges are one)
+  int ns;        // kWin: and [0, ns) before them, ns < j0 (0 where the two ranges are one); [j0, n) may be empty then
 };
 
 // Work unit: two Q tiles of a long sequence (two heads of one group over the
@@ -119,12 +119,17 @@ struct MmaUnit {
 };
 
 // KV tile at ring position i of a unit whose tiles share their K/V tiles.
-__device__ __forceinline__ int ws_ring_tile(int i, int nsb, int jb) { return i < nsb ? i : jb + i - nsb; }
+__host__ __device__ __forceinline__ int ws_ring_tile(int i, int nsb, int jb) { return i < nsb ? i : jb + i - nsb; }
+// Whether a Q tile visits KV tile j: [0, ns) (kWinSinks) and [j0, n).
+template <int kWin>
+__host__ __device__ __forceinline__ bool ws_visits(int ns, int j0, int n, int j) {
+  return j < n && (j >= j0 || (kWin == kWinSinks && j < ns));
+}
 
 // KV tile range of a Q tile, [j0, n), normalised to (0, 0) when empty.  kWin:
 // the call has a sliding window (without one every visited range starts at 0).
 template <int kWin>
-__device__ __forceinline__ void ws_tile_range(WsTile& tt, const AttnParams& p) {
+__host__ __device__ __forceinline__ void ws_tile_range(WsTile& tt, const AttnParams& p) {
   const SeqInfo& s = tt.seq;
   if constexpr (kWin) {
     KvTiles r{0, 0, 0};
@@ -136,6 +141,35 @@ __device__ __forceinline__ void ws_tile_range(WsTile& tt, const AttnParams& p) {
     tt.n = s.q_len > tt.q0 ? kv_tiles_for(s, tt.q0, kTileM) : 0;
     tt.j0 = 0;
   }
+}
+
+// The ring of a unit whose tiles share their K/V tiles: jb, nsb and n_all.  Every tile on it is visited by a query
+// tile, whose wait for K is the only one before the K stage is given back to the copies.
+template <int kWin>
+__host__ __device__ __forceinline__ void ws_share_tiles(WsUnit& u) {
+  if (kWin == kWinSinks) {
+    // Rows behind the last key's window see first keys only, [0, n).  Beside a tile with a gap that is [0, ns) and
+    // an empty range at the other's end: as one range [0, n) the ring would hold the gap, which neither visits.
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      WsTile& x = u.t[t];
+      const WsTile& o = u.t[1 - t];
+      if (o.ns > 0 && x.ns == 0 && x.n > 0 && x.n <= o.ns) {
+        x.ns = x.n;
+        x.j0 = x.n = o.n;
+      }
+    }
+  }
+  // tile 0's rows come first, so its window starts no later than tile 1's
+  u.jb = !kWin ? 0 : (u.t[0].n > 0 ? u.t[0].j0 : u.t[1].j0);
+  if (kWin == kWinSinks) {
+    // Tiles with a gap have the same ns: the first keys end theirs, not the mask.  One without a gap starts at
+    // tile 0 and has a window's keys, which reach the other's: two consecutive blocks' windows touch.
+    if (u.t[0].n > 0 && u.t[1].n > 0) u.jb = min(u.jb, u.t[1].j0);
+    u.nsb = min(u.jb, max(u.t[0].ns, u.t[1].ns));
+  }
+  const int jend = max(u.t[0].n, u.t[1].n);
+  u.n_all = jend > u.jb ? u.nsb + jend - u.jb : 0;
 }
 
 template <int DP>
@@ -197,15 +231,7 @@ __device__ __forceinline__ WsUnit ws_decode(SchedSmem& s, const AttnParams& p, u
       u.t[t].q0 = head_pair ? qb * kTileM : qb * kWsBlockM + t * kTileM;
       ws_tile_range<kWin>(u.t[t], p);
     }
-    // tile 0's rows come first, so its window starts no later than tile 1's
-    u.jb = !kWin ? 0 : (u.t[0].n > 0 ? u.t[0].j0 : u.t[1].j0);
-    if (kWin == kWinSinks) {
-      // both tiles have the same ns where both have a gap behind it; a tile without one starts at tile 0
-      if (u.t[0].n > 0 && u.t[1].n > 0) u.jb = min(u.jb, u.t[1].j0);
-      u.nsb = min(u.jb, max(u.t[0].ns, u.t[1].ns));
-    }
-    const int jend = max(u.t[0].n, u.t[1].n);
-    u.n_all = jend > u.jb ? u.nsb + jend - u.jb : 0;
+    ws_share_tiles<kWin>(u);
   } else {
     u.paired = 1;
     u.packed = (kPack && s.pack_on) ? 1 : 0;
@@ -566,7 +592,7 @@ __device__ void ws_mma(WsSmem<DP>& sm, const AttnParams& p, uint32_t tmem, volat
       // KV tiles ws_ring_tile(0 .. n - 1) are ring positions kv_cnt ..; tile t visits [0, ns_t) and [j0_t, n_t).
       const int n = u.n_all;
       auto ring = [&](int i) { return kWin == kWinSinks ? ws_ring_tile(i, u.nsb, u.jb) : u.jb + i; };
-      auto visits = [&](int t, int j) { return j < u.n[t] && (j >= u.j0[t] || (kWin == kWinSinks && j < u.ns[t])); };
+      auto visits = [&](int t, int j) { return ws_visits<kWin>(u.ns[t], u.j0[t], u.n[t], j); };
       const int qs = q_cnt % kQSlots;
       if (!WS_WAIT_WARP(&sm.q_full[qs], (q_cnt / kQSlots) & 1)) break;
       ++q_cnt;
