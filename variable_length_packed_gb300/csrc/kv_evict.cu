@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kSelectThreads, 3) kv_evict_select_kernel(cons
       e += __popc(same_bits[w]);
     }
   }
-  for (int i = K + rank * kSelectThreads + tid; i < p.max_keep; i += C * kSelectThreads) kept[i] = -1;
+  // 64 bits: a list may be as wide as 2^31 - 1, and the step behind its end passes that
+  for (long long i = (long long)K + rank * kSelectThreads + tid; i < p.max_keep; i += C * kSelectThreads) kept[i] = -1;
   if (head == 0 && rank == 0 && tid == 0) p.new_lens[b] = K;
 }
 
