@@ -1,4 +1,4 @@
-"""Eviction at the end of what 32 bits count: lists as wide as they may be."""
+"""Eviction and key weights at the ends of what 32 bits count: lists as wide as they may be, caches of nearly 2^31 keys."""
 import numpy as np
 import pytest
 import torch
@@ -27,3 +27,44 @@ def test_a_list_of_kept_slots_as_wide_as_may_be(keys, keep):
     assert slots == sorted(set(slots)) and (keep == 0 or (slots[0] >= 0 and slots[-1] == keys - 1))
     for at in range(keep, width, 1 << 28):
         assert torch.all(kept[0, 0, at:at + (1 << 28)] == -1)
+
+
+@pytest.mark.parametrize("new,left,sinks", [(20, -1, 0), (20, 1000, 3), (130, -1, 0), (1, -1, 0), (1, 1500, 70)])
+def test_weights_of_a_cache_of_nearly_2_to_the_31_keys(new, left, sinks):
+    """All keys but the last 2048 have no page: the attention reads page 0 for them, zeros here, and they have no weight.
+    The last ones score 40 against their 0.  Tolerances as in test_paged_window_gpu; the sum over the zeros is below
+    2^31 e^-30 of that over the last keys, its roundings far less."""
+    page, d, real = 128, 8, 16
+    wide = 2 ** 24 - 1                     # 2^31 - 128 keys
+    L, n0 = wide * page, wide * page - real * page
+    g = torch.Generator("cuda").manual_seed(new)
+    kc = torch.zeros(real + 1, page, 1, d, dtype=torch.bfloat16, device="cuda")
+    kc[1:] = 3.5 + 0.25 * torch.randn(real, page, 1, d, generator=g, device="cuda").clamp(-3, 3)
+    vc = torch.randn(kc.shape, generator=g, device="cuda").to(torch.bfloat16)
+    q = (4 + 0.25 * torch.randn(new, 1, d, generator=g, device="cuda").clamp(-3, 3)).to(torch.bfloat16)
+    table = torch.full((1, wide), -1, dtype=torch.int32, device="cuda")
+    table[0, -real:] = torch.arange(1, real + 1, device="cuda")
+    w = torch.rand(real + 1, page, 1, generator=g, device="cuda")
+    had = w.clone()
+    _, lse = vlp.thd_attn_paged(q, kc, vc, table, ints([L]), ints([0, new]), window=(left, -1), sink_tokens=sinks,
+                                key_weights=w)
+    torch.cuda.synchronize()
+    # 64 bits: keys n0 .. L - 1, and so many zeros before them
+    k, qq = kc[1:].reshape(-1, d).double(), q[:, 0].double()
+    own = L - new + torch.arange(new, device="cuda")[:, None]
+    key = n0 + torch.arange(real * page, device="cuda")[None]
+    see = (key <= own) & (key >= own - left if left >= 0 else True)
+    s = (qq @ k.T * d ** -0.5).masked_fill(~see, float("-inf"))
+    zeros = n0 if left < 0 else sinks
+    want = torch.logaddexp(s.logsumexp(1), torch.full((new,), float(zeros), dtype=torch.float64, device="cuda").log())
+    S = float((qq.abs() @ k.abs().T).max()) * d ** -0.5
+    e = 136 * 2.0 ** -23 * S + 2.0 ** -21 * (1 + S)
+    assert torch.all((lse[0].double() - want).abs() <= e + 4 * 2.0 ** -24 * want.abs())
+    added = (s - want[:, None]).exp().sum(0)
+    fresh = torch.arange(real * page, device="cuda") >= real * page - new
+    expect = torch.where(fresh, 0.0, had[1:].flatten().double()) + added
+    share = 2 * e + 2.0 ** -20 * (1 + float(want.abs().max())) + new * 2.0 ** -24
+    bound = share * added + 2.0 ** -24 * expect + 2.0 ** -126
+    worst = float(((w[1:].flatten().double() - expect).abs() / bound).max())
+    print(f"weights: largest share of the bound {worst:.3f}")
+    assert worst <= 1.0 and torch.equal(w[0], had[0]) and float(added.max()) > 1e-4

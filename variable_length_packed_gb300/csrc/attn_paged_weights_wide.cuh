@@ -48,6 +48,9 @@ struct WwItem {
   int seq, head, key0, past, tile0, tile1;
 };
 
+// Items of a sequence's head; unsigned, as the last one may end at 2^31.
+__device__ __forceinline__ int ww_items(int kv_len) { return (int)(((uint32_t)kv_len + kWwKeys - 1) / kWwKeys); }
+
 // The items of a CTA's share, in order; an item costs its sequence's query tiles, and 2 for its keys.
 template <bool kWin>
 struct WwWalk {
@@ -59,7 +62,7 @@ struct WwWalk {
 
   __device__ static __forceinline__ long long cost(const SeqWork& s, int tokens) { return 2ll + (s.q_len + tokens - 1) / tokens; }
   __device__ static __forceinline__ long long items(const PagedArgs& p, const SeqWork& s) {
-    return s.q_len > 0 ? (long long)p.Hkv * ((s.kv_len + kWwKeys - 1) / kWwKeys) : 0ll;
+    return s.q_len > 0 ? (long long)p.Hkv * ww_items(s.kv_len) : 0ll;
   }
 
   __device__ __forceinline__ bool next(const PagedArgs& p, WwItem& x) {
@@ -76,7 +79,7 @@ struct WwWalk {
       u = base + item * per;
       if (u >= end) return false;
       u += per;
-      const int blocks = (x.s.kv_len + kWwKeys - 1) / kWwKeys;
+      const int blocks = ww_items(x.s.kv_len);
       x.seq = b;
       x.head = (int)quotient(item, blocks);
       x.key0 = (int)(item - (long long)x.head * blocks) * kWwKeys;
