@@ -26,6 +26,7 @@ _LIB = None
 
 THD_OK, THD_ERR_ARG, THD_ERR_UNSUPPORTED, THD_ERR_CUDA, THD_ERR_WORKSPACE = 0, -1, -2, -3, -4
 THD_BF16, THD_FP16 = 0, 1
+_COUNT_MAX = 2 ** 31 - 1   # the library's counts are C ints, which ctypes would cut to 32 bits without a word
 STATUS_WAIT_TIMEOUT = 0x1
 # per-sequence mask type codes accepted in seq_is_causal (a bool tensor is codes 0 / 1)
 MASK_PADDING, MASK_PADDING_CAUSAL, MASK_PADDING_CAUSAL_BOTTOM_RIGHT = 0, 1, 2
@@ -185,6 +186,8 @@ def _check_qkv(q, k, v):
         raise ValueError("k and v must be [T, Hkv, head_dim] with q's T and head_dim")
     if q.dtype not in (torch.bfloat16, torch.float16) or k.dtype != q.dtype or v.dtype != q.dtype:
         raise TypeError("q, k, v must share dtype bf16 or fp16")
+    if (T | Hq | Hkv | d) > _COUNT_MAX:   # the or of sizes in range is in range
+        raise ValueError("a size of q, k, v does not fit the library's 32 bits")
     return T, Hq, Hkv, d
 
 
@@ -233,6 +236,13 @@ def _window_args(window):
     return left, right
 
 
+def _window_extents(window):
+    left, right = _window_args(window)
+    if max(left, right) > _COUNT_MAX:
+        raise ValueError("window extents must fit the library's 32 bits")
+    return left, right
+
+
 def _sink_count(sink_tokens):
     sinks = int(sink_tokens)
     if not 0 <= sinks < 2 ** 31:
@@ -258,6 +268,8 @@ def thd_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=None,
     Returns (out [T, Hq, d], lse [Hq, T] float32 or None).
     """
     T, Hq, Hkv, d = _check_qkv(q, k, v)
+    left, right = _window_extents(window)
+    sinks = _sink_count(sink_tokens)
     _check_metadata_dtypes(cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, seq_is_causal)
     for name, t in (("q", q), ("k", k), ("v", v), ("cu_seqlens_q", cu_seqlens_q),
                     ("cu_seqlens_kv", cu_seqlens_kv), ("cu_seqlens_q_padded", cu_seqlens_q_padded),
@@ -278,8 +290,6 @@ def thd_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded=None,
         lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = torch.empty(_workspace_bytes(), dtype=torch.uint8, device=q.device)
-    left, right = _window_args(window)
-    sinks = _sink_count(sink_tokens)
     st = _call("thd_attn_fwd_sinks", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(cu_seqlens_q),
                _addr(cu_seqlens_kv), _addr(cu_seqlens_q_padded), _addr(cu_seqlens_kv_padded), _addr(seq_is_causal),
                int(batch_size), int(max_seqlen), float(softmax_scale), out.data_ptr(), _addr(lse), T, Hq, Hkv, d,
@@ -416,6 +426,8 @@ def thd_attn_bwd(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlen
     """Gradients (dq, dk, dv) of thd_attn_fwd for the same batch, window and sink_tokens; out / lse
     are the forward's outputs.  head_dim 64 or 128."""
     T, Hq, Hkv, d = _check_qkv(q, k, v)
+    left, right = _window_extents(window)
+    sinks = _sink_count(sink_tokens)
     _check_metadata_dtypes(cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, seq_is_causal)
     for name, t in (("q", q), ("k", k), ("v", v), ("out", out), ("lse", lse), ("dout", dout),
                     ("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_kv", cu_seqlens_kv),
@@ -439,8 +451,6 @@ def thd_attn_bwd(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_kv, cu_seqlen
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
-    left, right = _window_args(window)
-    sinks = _sink_count(sink_tokens)
     need = int(_lib().thd_attn_bwd_sinks_workspace_size(int(T), int(Hq), int(Hkv), int(d), int(batch_size), left, sinks))
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)

@@ -12,14 +12,14 @@ import math
 
 import torch
 
-from . import THD_BF16, THD_FP16, THD_OK, ThdError, _addr, _check_metadata, _sink_count, _window_args, load_library
+from . import (THD_BF16, THD_FP16, THD_OK, _COUNT_MAX, ThdError, _addr, _check_metadata, _sink_count, _window_args,
+               load_library)
 from . import _call as _status_of
 
 _F32 = torch.float32
 _SCORES_MAX = 1 << 30   # bytes that thd_attn_paged allocates at most for scores beside its workspace
 _Places = ctypes.c_int64 * 6
 _WeightPlaces = ctypes.c_int64 * 3
-_COUNT_MAX = 2 ** 31 - 1   # the library's counts are C ints, which ctypes would cut to 32 bits without a word
 _CODES = {torch.bfloat16: THD_BF16, torch.float16: THD_FP16}
 
 
