@@ -46,7 +46,10 @@ __device__ __forceinline__ void load_tile_manual(uint8_t* dst, const void* src, 
   }
 }
 
-template <typename DT, int DP, bool kTMA>
+// kSinks: under a window with first keys that stay visible, whose selects in one kernel for all calls cost the others
+// 3 % (65536 rows of 64 sequences, 32 + 8 heads, causal, without a window and with one of 511: heads of 96 in 10.99
+// and 6.94 ms against 11.33 and 7.15, of 40 in 6.50 and 4.35 against 6.69 and 4.50; with 4 first keys 7.89 and 4.95).
+template <typename DT, int DP, bool kTMA, bool kSinks>
 __global__ void __launch_bounds__(128, 1)
     attn_fwd_serial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
@@ -109,10 +112,10 @@ __global__ void __launch_bounds__(128, 1)
     const int q0 = it.qblock * kTileM;                  // first query position of the tile
     const int rows_valid = min(kTileM, s.q_len - q0);
     const int kvh = it.h / p.group;
-    // KV tiles [0, ns) and [j0, j0 + nkv - ns) hold the keys the tile's rows see
-    const KvTiles kt = kv_tiles_windowed(s, q0, p.sinks);
-    const int nkv = kt.ns + kt.n - kt.j0;
-    auto first_key_of = [&](int v) { return (v < kt.ns ? v : kt.j0 + v - kt.ns) * kBlockN; };
+    // KV tiles [j0, nkv) hold the keys the tile's rows see; kSinks: they count the tiles of [0, ns) and [kt.j0, n)
+    const KvTiles kt = kv_tiles_windowed(s, q0, kSinks ? p.sinks : 0);
+    const int j0 = kSinks ? 0 : kt.j0, nkv = kSinks ? kt.ns + kt.n - kt.j0 : kt.n;
+    auto first_key_of = [&](int j) { return (!kSinks || j < kt.ns ? j : kt.j0 + j - kt.ns) * kBlockN; };
     const int qpos = q0 + tid;                          // this thread's query position
 
     // l_run: sum of the P values as rounded for the P V product (normalises O, so each
@@ -129,12 +132,12 @@ __global__ void __launch_bounds__(128, 1)
 #pragma unroll
           for (int pn = 0; pn < kPanels; ++pn) {
             tma_load_2d(sm.q + pn * 16384, &tm_q, &sm.bar_load, it.h * p.d + pn * 64, s.q_start + q0);
-            tma_load_2d(sm.k + pn * 16384, &tm_k, &sm.bar_load, kvh * p.d + pn * 64, s.kv_start + first_key_of(0));
-            tma_load_2d(sm.v + pn * 16384, &tm_v, &sm.bar_load, kvh * p.d + pn * 64, s.kv_start + first_key_of(0));
+            tma_load_2d(sm.k + pn * 16384, &tm_k, &sm.bar_load, kvh * p.d + pn * 64, s.kv_start + first_key_of(j0));
+            tma_load_2d(sm.v + pn * 16384, &tm_v, &sm.bar_load, kvh * p.d + pn * 64, s.kv_start + first_key_of(j0));
           }
         }
       } else {
-        const int kvr = first_key_of(0);
+        const int kvr = first_key_of(j0);
         load_tile_manual<DP>(sm.q, p.q, s.q_start + q0, rows_valid, p.Hq, it.h, p.d, p.T);
         load_tile_manual<DP>(sm.k, p.k, s.kv_start + kvr, min(kBlockN, s.kv_len - kvr), p.Hkv, kvh, p.d, p.T);
         load_tile_manual<DP>(sm.v, p.v, s.kv_start + kvr, min(kBlockN, s.kv_len - kvr), p.Hkv, kvh, p.d, p.T);
@@ -142,7 +145,7 @@ __global__ void __launch_bounds__(128, 1)
         __syncthreads();
       }
 
-      for (int j = 0; j < nkv; ++j) {
+      for (int j = j0; j < nkv; ++j) {
         const int kv0 = first_key_of(j);
         // ---- S = Q K^T ----
         if (tid == 0) {
@@ -180,14 +183,15 @@ __global__ void __launch_bounds__(128, 1)
         const long long d0 = (long long)q0 + s.shift;
         const bool need_mask = (kv0 + kBlockN > s.kv_len) || (kv0 + kBlockN - 1 > d0 + s.hi_off) ||
                                (kv0 < d0 + (kTileM - 1) - s.lo_off);
-        const int key_lo = seq_first_key(s, qpos), key_hi = seq_last_key(s, qpos), few = sink_end(s, qpos, p.sinks);
+        const int key_lo = seq_first_key(s, qpos), key_hi = seq_last_key(s, qpos);
+        const int few = kSinks ? sink_end(s, qpos, p.sinks) : 0;
         float mx = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 128; ++c) {
           float x = __uint_as_float(sr[c]);
           if (need_mask) {
             const int kp = kv0 + c;
-            x = (kp >= key_lo && kp <= key_hi) || kp < few ? x : -INFINITY;
+            x = (kp >= key_lo && kp <= key_hi) || (kSinks && kp < few) ? x : -INFINITY;
             sr[c] = __float_as_uint(x);
           }
           mx = fmaxf(mx, x);
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(128, 1)
         m_run = m_new;
 
         // ---- rescale O (after the previous P V has completed) ----
-        if (j > 0) {
+        if (j > j0) {
 #pragma unroll
           for (int c = 0; c < DP / 32; ++c) {
             uint32_t o[32];
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(128, 1)
             const uint32_t voff = kk * 16 * 128;   // 16 key rows of 128 bytes
             umma_ss(tO, smem_desc_sw128(smem_u32(sm.p) + poff, 16, 1024),
                     smem_desc_sw128(smem_u32(sm.v) + voff, 16384, 1024), idesc_pv,
-                    (j > 0 || kk > 0) ? 1u : 0u);
+                    (j > j0 || kk > 0) ? 1u : 0u);
           }
           umma_commit(&sm.bar_mma);
         }

@@ -157,10 +157,10 @@ namespace {
 template <typename DT, int DP, bool kTMA>
 int launch_serial(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const thd::AttnParams& p,
                   int grid, cudaStream_t stream) {
-  auto kern = thd::attn_fwd_serial_kernel<DT, DP, kTMA>;
+  auto kern = p.sinks > 0 ? thd::attn_fwd_serial_kernel<DT, DP, kTMA, true> : thd::attn_fwd_serial_kernel<DT, DP, kTMA, false>;
   const size_t smem = sizeof(thd::SerialSmem<DP>) + 1024;
-  static thd::SmemGrant grant;
-  if (!grant.ask(kern, smem)) return THD_ERR_CUDA;
+  static thd::SmemGrant grants[2];
+  if (!grants[p.sinks > 0 ? 1 : 0].ask(kern, smem)) return THD_ERR_CUDA;
   kern<<<grid, 128, smem, stream>>>(mq, mk, mv, p);
   return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
 }
