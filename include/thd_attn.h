@@ -233,9 +233,12 @@ int thd_attn_bwd_window(const void* q, const void* k, const void* v, const void*
 
 /*
  * thd_attn_bwd_sinks_workspace_size — bytes of device workspace thd_attn_bwd_sinks needs:
- * thd_attn_bwd_workspace_size's, and, with window_left >= 0 and 1 <= sink_tokens <= 512, sums of
- * 8 * head_dim bytes for each such key and head of every sequence and of every 2048 rows.  0 for
- * invalid sizes.
+ * thd_attn_bwd_workspace_size's, and, with window_left >= 0 and 1 <= sink_tokens <= 512, shared sums of
+ *     8 * head_dim * num_heads_kv * keys  bytes, (2 * batch_size + total_tokens / 2048 + 1) times,
+ * keys = sink_tokens, from 129 on rounded up to a multiple of 128 (two buffers, each rounded up to 256
+ * bytes).  They are reserved for every sequence, also for those that are no longer than their window and
+ * use none: 4096 sequences in 65536 rows, 8 key/value heads of 128 and 64 first keys take 4.3 GB of them.
+ * 0 for invalid sizes.
  */
 size_t thd_attn_bwd_sinks_workspace_size(int total_tokens, int num_heads_q, int num_heads_kv, int head_dim,
                                          int batch_size, int window_left, int sink_tokens);

@@ -54,7 +54,11 @@ struct BwdParams {
 // the kernel below: 2.09 ms, against 9.01 in one item each.
 // Query tiles of a far item: its work is that of an ordinary item under a window of 2048.
 constexpr int kFarTiles = 16;
-// Tiles of this many first keys are split; more of them are many items without that.
+// Tiles of this many first keys are split, which bounds the shared sums (4 KB times head_dim a sequence and
+// key/value head).  Of more, each tile is one item over all queries of its sequence again, which costs one long
+// sequence three times as much and a batch nothing: 65536 rows, 512, 513 and 2048 first keys, one sequence,
+// 16 + 4 heads of 64, window 1023: 1.55, 4.68 and 4.55 ms; 32 + 8 heads of 128, window 511: 3.59, 7.98 and 9.05;
+// 64 sequences of those: 2.45, 2.23 and 2.23.
 constexpr int kFarMaxSinks = 512;
 
 // There, fp16 weights are held times 2^14 for the product with dO: of weights near 2^-10, as a window of 1024 has,

@@ -21,7 +21,7 @@
 // step's operands, copies and dS^T are some 1900 cycles of it, and the 8.8 GB that are added to the accumulator pass at 5 TB/s.
 // 65536 rows of one sequence, 16 + 4 heads of 64, fp16, window 1023: 1.04 of 1.20 ms (2.09 before).  Left: dQ of
 // heads of 64 by 16 bytes a lane (1.83 ms) or by whole rows out of shared memory (1.48), a register split by setmaxnreg
-// (spills).
+// (more spills: heads of 64 store 88 bytes a thread in 128 registers and read 120 back, heads of 128 none).
 #pragma once
 #include "attn_bwd.cuh"
 

@@ -20,7 +20,8 @@
 // softmax streams, two score tiles for each and the queries in shared memory took 107 us with
 // keys and values by tensor copies of whole boxes of a page (16 tokens by 64 columns), 153 us with two
 // warps copying rows; with the keys in the L2 it was slower too (78 against 60 us for 54 drafted tokens over
-// 24000 keys).  Two CTAs leave a thread 128 registers; heads of 128 spill 8 to 16 bytes.
+// 24000 keys).  Two CTAs leave a thread 128 registers; heads of 128 spill 8 to 16 bytes, under a
+// window 20 to 24 (36 to 96 read back), heads of 64 there 8.
 // Heads of 64 (68 us at 64 rows, where memory asks 37): a second score tile in the room they leave, twice the
 // units on the way, and pages read a unit ahead changed nothing.
 //

@@ -430,7 +430,9 @@ def thd_attn_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q, cu_se
     first sink_tokens of the sequence; not with a tree_mask.  Keys that no token sees are not read.
     key_weights: float32 [pages, page_size, Hkv] in any order in memory, updated: each cached key's is
     raised by the attention weights that the new tokens and the heads of its group gave it, each new
-    token's key's is set to them.  Returns (out [T, Hq, d], lse [Hq, T] float32 or None); rows of no
+    token's key's is set to them.  Without a workspace, a call with them and at most 16 rows (new tokens times
+    the heads of a group) a sequence allocates room for scores, 4 bytes for each head, token and key that all
+    pages of the cache could hold, 1 GiB at most; a batch whose scores need more reads its keys twice.  Returns (out [T, Hq, d], lse [Hq, T] float32 or None); rows of no
     sequence and rows that see no key are 0 with lse -inf.
     """
     code = _dtype_code(q, "q")
@@ -498,7 +500,8 @@ def thd_kv_evict(k_cache, v_cache, key_weights, page_table, kv_lens, keep_lens, 
     the most weight, of equal ones the lower slots.  They move, with their weights and in their order, to
     slots 0.. of the pages that new_page_table names (int32 [B, pages], none of the old ones), or of
     their own pages without it; the other slots are left as they were.  kept: int32 [B, Hkv, width], filled with
-    the old slots of the kept keys and -1 behind them; no more than width keys stay.
+    the old slots of the kept keys and -1 behind them; no more than width keys stay.  Without it the call
+    allocates and fills one as wide as the narrower table has slots.
     new_lens: int32 [B] (not kv_lens nor keep_lens).
     """
     code = _dtype_code(k_cache, "k_cache")
