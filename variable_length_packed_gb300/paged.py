@@ -12,9 +12,8 @@ import math
 
 import torch
 
-from . import (THD_BF16, THD_FP16, THD_OK, _COUNT_MAX, ThdError, _addr, _check_metadata, _sink_count, _window_args,
-               load_library)
-from . import _call as _status_of
+from . import (THD_BF16, THD_FP16, THD_OK, _COUNT_MAX, ThdError, _addr, _check_metadata, _raw_stream, _sink_count,
+               _window_args, load_library)
 
 _F32 = torch.float32
 _SCORES_MAX = 1 << 30   # bytes that thd_attn_paged allocates at most for scores beside its workspace
@@ -174,7 +173,12 @@ def _weights(wq, wk, device, d, dtype):
 
 def _call(name, device, *args):
     """The library's entry point on the current stream of `device`."""
-    st = _status_of(name, device, *args)
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, _raw_stream(device.index))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _raw_stream(device.index))
     if st != THD_OK:
         raise ThdError(st, name)
 
@@ -459,13 +463,11 @@ def thd_attn_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q, cu_se
         out = torch.empty((T, hq, d), dtype=dtype, device=dev)
     else:
         _whole(out, "out", dev, dtype, q.shape)
-    left, sinks = -1, 0
-    if window != (-1, -1):
+    left, sinks, places, wanted = -1, 0, None, True
+    if sink_tokens != 0 or window != (-1, -1):
         left, sinks = _window_args(window)[0], _sink_count(sink_tokens)
-    elif sink_tokens != 0:
-        _sink_count(sink_tokens)
-    places = None if key_weights is None else _key_weights(key_weights, dev, shape)
-    wanted = return_lse or lse is not None
+    if key_weights is not None:
+        places, wanted = _key_weights(key_weights, dev, shape), return_lse or lse is not None
     if lse is None and (return_lse or key_weights is not None):
         lse = torch.empty((hq, T), dtype=torch.float32, device=dev)
     else:
@@ -481,12 +483,19 @@ def thd_attn_paged(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q, cu_se
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     else:
         _whole(workspace, "workspace", dev, torch.uint8)
-    if (T | hq | shape[2] | d | B | shape[0] | shape[1] | wide | words | abs(max_seqlen_q) | max(left, 0)) > _COUNT_MAX:
+    if (T | hq | shape[2] | d | B | shape[0] | shape[1] | wide | words | abs(max_seqlen_q)) > _COUNT_MAX or left > _COUNT_MAX:
         raise _too_large("thd_attn_paged")
-    _call("thd_attn_paged_window", dev, _addr(q), k_cache.data_ptr(), v_cache.data_ptr(), strides, shape[0], shape[1],
-          page_table.data_ptr(), step, wide, kv_lens.data_ptr(), cu_seqlens_q.data_ptr(), _addr(cu_seqlens_q_padded), B,
-          max_seqlen_q, _addr(tree_mask), words, left, sinks, _addr(key_weights), places,
-          1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale), out.data_ptr(), _addr(lse), T, hq, shape[2], d, code, _addr(workspace), workspace.numel())
+    scale = 1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale)
+    if left < 0 and places is None:   # a decoding step waits for the host: fewer arguments to convert
+        _call("thd_attn_paged", dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), strides, shape[0], shape[1],
+              page_table.data_ptr(), step, wide, kv_lens.data_ptr(), cu_seqlens_q.data_ptr(), _addr(cu_seqlens_q_padded), B,
+              max_seqlen_q, _addr(tree_mask), words, scale, out.data_ptr(), _addr(lse), T, hq, shape[2], d, code,
+              workspace.data_ptr(), workspace.numel())
+    else:
+        _call("thd_attn_paged_window", dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), strides, shape[0], shape[1],
+              page_table.data_ptr(), step, wide, kv_lens.data_ptr(), cu_seqlens_q.data_ptr(), _addr(cu_seqlens_q_padded), B,
+              max_seqlen_q, _addr(tree_mask), words, left, sinks, _addr(key_weights), places, scale, out.data_ptr(),
+              _addr(lse), T, hq, shape[2], d, code, workspace.data_ptr(), workspace.numel())
     return out, lse if wanted else None
 
 
